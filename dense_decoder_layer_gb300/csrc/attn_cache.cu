@@ -1,0 +1,998 @@
+// Attention of a few new tokens per sequence over a cache of bf16, e4m3 or
+// 4-bit rows (pds_attention_tree).
+//
+// Mathematics.  Query row r = t G + i of a (sequence, kv head) is head
+// kv_head G + i of token t (G = H / Hkv).  With the cached row of key j read
+// as scale_j code_j,
+//   z_rj = log2(e)/sqrt(hd) kscale_j (q_r . kcode_j)       (softcap on top)
+//   o_r  = sum_j 2^(z_rj - m_r) vscale_j vcode_j / sum_j 2^(z_rj - m_r)
+// over the keys j that token t sees: the scales stay out of the matrix
+// products, so the codes go into them as exact bf16 integers or e4m3 values
+// and nothing is rounded on the way but P (2^(z-m) vscale, to bf16, as in the
+// prefill attention: its error averages out over the keys) and o (once).
+//
+// What bounds it: every cached row is used by T G query rows, one to a few
+// dozen, so at 2 T G flop per byte of bf16 the call is bound by reading the
+// cache (HBM); few-row calls by latency.  Hence the split: the keys of a
+// sequence are cut into chunks over all SMs, each block holds the T G rows
+// of one kv head (up to 32) and its 8 warps walk the chunk's 16-key steps
+// independently, each through its own ring of asynchronous copies, so no
+// barrier stands between a warp and the memory.  The warp computes
+// S^T = K Q^T with keys as the 16-row operand and 8 query rows per column
+// tile (a decode step has 3 or 4: a query-major tile would be 3/4 empty), and
+// O^T = V^T P^T the same way, P^T being S^T's fragments transposed inside the
+// warp.  A key's scales are then one factor per accumulator row, and a running
+// maximum that moves only when a score exceeds it by 2^8 needs no reduction
+// over keys until the end.
+//
+// Chunks write unnormalised rows and (maximum, sum) to the workspace; a second
+// kernel joins them in chunk order.  The chunk length is made from the
+// sequences' lengths on the device (they change between replays of a graph).
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <algorithm>
+#include <string>
+
+#include "common.cuh"
+#include "fastmath.cuh"
+#include "kv.h"
+#include "tc.h"
+
+namespace pds {
+namespace {
+
+constexpr int kStep = 16;        // keys of a warp's step
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr float kMoveLog2 = 8.0f;  // the reference maximum follows beyond a growth of 2^8
+constexpr int kMaxTiles = 4;     // column tiles of 8 query rows per block
+constexpr int kMaskWords = kMaxDraftTokens / 32;
+
+struct Args {
+  CacheView c;
+  const uint16_t* q;
+  uint16_t* o;
+  int64_t q_stride, o_stride;
+  const int32_t* parents;
+  int n_tokens, n_heads, group;  // group: query heads per kv head
+  int max_len;
+  float scale_log2;              // log2(e) / sqrt(hd)
+  float cap;                     // softcap in units of q.k (0: none)
+  int window;
+  int row_tiles;                 // blocks of query rows per (sequence, kv head)
+  int tile_rows;                 // rows of one
+  int slots;                     // blocks to spread the chunks over; 0: one chunk each
+  int fit;                       // 1: choose chunks so that all units run at once
+  int min_steps;                 // shortest chunk, in steps
+  float* o_part;                 // [unit][tile_rows][hd]
+  float2* ml_part;               // [unit][tile_rows]: (maximum, sum)
+  uint32_t* status;
+};
+
+// --------------------------------------------------------------- schedule
+//
+// Units: (chunk of a sequence) x (kv head, row tile), the latter fastest, so
+// that blocks running together read neighbouring heads of the same rows.
+
+// Steps of sequence s: [first, first + n) in units of kStep keys; n = 0 for a
+// length that does not fit.
+__device__ __forceinline__ int seq_steps(const Args& a, int s, int& first, int& len) {
+  len = a.c.lens[s];
+  first = 0;
+  if (len < 0 || len > a.max_len) return 0;
+  // the first row any token can see: a root's, at position len
+  if (a.window > 0 && len - a.window + 1 > 0) first = (len - a.window + 1) / kStep;
+  return (len + a.n_tokens + kStep - 1) / kStep - first;
+}
+
+__device__ __forceinline__ int warp_sum_int(int v) {
+  return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(v)));
+}
+
+// Steps per chunk (the same for every sequence), by one warp.
+__device__ int chunk_steps(const Args& a, int lane) {
+  if (a.slots == 0) return 1 << 30;
+  const int per = a.c.n_kv_heads * a.row_tiles;
+  int first, len;
+  long long total = 0;
+  for (int s = lane; s < a.c.n_seqs; s += 32) total += seq_steps(a, s, first, len);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  // at most slots + (sequences x per) units: every chunk but a sequence's last is whole
+  int c = max(a.min_steps, static_cast<int>((total * per + a.slots - 1) / a.slots));
+  if (!a.fit) return c;
+  // Sequences' last chunks are short: lengthen until the units fit the slots.
+  // There are at most half as many (sequence, head, tile) as slots, so twice
+  // this length always fits: about 16 rounds of a sixteenth at the very most.
+  for (;;) {
+    int chunks = 0;
+    for (int s = lane; s < a.c.n_seqs; s += 32) {
+      const int n = seq_steps(a, s, first, len);
+      chunks += (n + c - 1) / c;
+    }
+    if (static_cast<long long>(warp_sum_int(chunks)) * per <= a.slots) break;
+    c += max(1, c >> 4);
+  }
+  return c;
+}
+
+struct Unit {
+  int seq, chunk, n_chunks, first, n_steps, len;  // steps [first, first + n_steps)
+  int base;  // (chunk 0 of the sequence) among all chunks
+};
+
+// The sequence and chunk of the w-th chunk overall (w < 0: of sequence `seq`,
+// whole range).  False past the last one.  By one warp; every lane returns it.
+__device__ bool find_unit(const Args& a, int c, int w, int seq, int lane, Unit& u) {
+  int base = 0;
+  for (int s0 = 0; s0 < a.c.n_seqs; s0 += 32) {
+    const int s = s0 + lane;
+    int first = 0, len = 0, n = 0;
+    if (s < a.c.n_seqs) n = seq_steps(a, s, first, len);
+    const int chunks = n == 0 ? 0 : (n - 1) / c + 1;
+    int incl = chunks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const int excl = base + incl - chunks;
+    const bool mine = w >= 0 ? (w >= excl && w < base + incl) : s == seq;
+    const unsigned hit = __ballot_sync(0xffffffffu, mine);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      u.seq = s0 + src;
+      u.n_chunks = __shfl_sync(0xffffffffu, chunks, src);
+      u.base = __shfl_sync(0xffffffffu, excl, src);
+      u.len = __shfl_sync(0xffffffffu, len, src);
+      const int f = __shfl_sync(0xffffffffu, first, src), m = __shfl_sync(0xffffffffu, n, src);
+      u.chunk = w >= 0 ? w - u.base : 0;
+      u.first = f + u.chunk * c;
+      u.n_steps = min(c, m - u.chunk * c);
+      return true;
+    }
+    base = __shfl_sync(0xffffffffu, base + incl, 31);
+  }
+  return false;
+}
+
+// ------------------------------------------------------------ instructions
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes (or zeros, when !live) into shared memory, not through L1.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+// Four 8x8 blocks of 16-bit values, transposed: lane l gives the address of
+// row l % 8 of block l / 8.
+__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+// An 8x8 block of 16-bit values held by the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two e4m3 codes, each in the high byte of a 16-bit half (what the other
+// byte holds does not matter), as a pair of bf16: the exponent and mantissa
+// bits move down by four, and 2^120 turns the bias of 7 into one of 127.
+// Exact for every code, subnormal ones included.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t r) {
+  const uint32_t bits = ((r >> 4) & 0x07f007f0u) | (r & 0x80008000u);
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(bits), "r"(0x7b807b80u));
+  return d;
+}
+// Two 4-bit codes (in the low nibbles of 16-bit halves) less their zero
+// points, as bf16: 128 + code and 128 + zero point (z: as 0x4300 | zero point
+// in each half) are bf16 numbers, their difference is exact.
+__device__ __forceinline__ uint32_t int4_pair(uint32_t r, uint32_t z) {
+  const uint32_t bits = (r & 0x000f000fu) | 0x43004300u;
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(bits), "r"(z));
+  return d;
+}
+
+__device__ __forceinline__ bool not_finite2(uint32_t w) {  // either bf16 of a pair
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// ------------------------------------------------------------ the formats
+
+// Bytes of a head's row, and of one step's K (or V) slice.
+template <int FMT, int HD>
+struct Fmt {
+  static constexpr int kRow = FMT == PDS_KV_BF16 ? 2 * HD : FMT == PDS_KV_E4M3 ? HD : HD / 2;
+  static constexpr int kSlice = kStep * kRow;
+  static constexpr int kChunks = kRow / 16;  // 16-byte chunks of a row
+  static constexpr int kStage = 2 * kSlice + 128;  // K, V, 16 + 16 scale words
+  static constexpr int kKSteps = HD / 16;   // contraction steps of S^T
+  static constexpr int kMTiles = HD / 16;   // channel tiles of O^T
+
+  // Where chunk c of the step's key row r is kept.  The chunks are permuted
+  // within 128-byte lines so that the lanes that load together (K: two rows,
+  // all four quarters; V: keys 0, 2, 4, 6 of a lane group, neighbouring chunks)
+  // hit different banks.
+  static __device__ __forceinline__ uint32_t k_at(int r, int c) {
+    if constexpr (kRow >= 128) return r * kRow + ((c ^ ((r & 1) << 2)) << 4);
+    return r * kRow + (c << 4);
+  }
+  static __device__ __forceinline__ uint32_t v_at(int r, int c) {
+    if constexpr (FMT == PDS_KV_BF16) return r * kRow + ((c ^ (r & 7)) << 4);
+    if constexpr (kRow == 128) return r * 128 + ((c ^ (((r >> 1) & 3) << 1)) << 4);
+    if constexpr (kRow == 64)
+      return (r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (((r >> 1) & 3) << 1)) << 4);
+    return (r >> 2) * 128 + ((((r & 3) * 2 + c) ^ (((r >> 2) & 1) << 1)) << 4);
+  }
+
+  // The contraction runs over the head's channels in an order that lets a lane
+  // read its share of a key's row with wide loads: the two pairs of channels
+  // (first, second operand register) of step ks for the lane's quarter t4.
+  static __device__ __forceinline__ void q_channels(int ks, int t4, int (&ch)[4]) {
+    if constexpr (FMT == PDS_KV_BF16) {
+      const int c = 8 * (t4 + 4 * (ks >> 1)) + 4 * (ks & 1);
+      ch[0] = c, ch[1] = c + 1, ch[2] = c + 2, ch[3] = c + 3;
+    } else if constexpr (FMT == PDS_KV_E4M3) {
+      const int c = 16 * (t4 + 4 * (ks >> 2)) + 4 * (ks & 3);
+      ch[0] = c, ch[1] = c + 2, ch[2] = c + 1, ch[3] = c + 3;
+    } else {
+      const int c = (HD / 4) * t4 + 8 * (ks >> 1) + 2 * (ks & 1);
+      ch[0] = c, ch[1] = c + 4, ch[2] = c + 1, ch[3] = c + 5;
+    }
+  }
+  // Channel of row half hh (0: rows 0-7, 1: rows 8-15), lane group g, of
+  // channel tile i of O^T.
+  static __device__ __forceinline__ int o_channel(int i, int hh, int g) {
+    return FMT == PDS_KV_BF16 ? 16 * i + 8 * hh + g : (HD / 8) * g + 2 * i + hh;
+  }
+};
+
+// S^T (16 keys x 8 NT rows) of one step.
+template <int FMT, int HD, int NT>
+__device__ __forceinline__ void scores(uint32_t ks, uint32_t q_frag, int lane, uint32_t kz0,
+                                       uint32_t kz1, float (&s)[NT][4]) {
+  using F = Fmt<FMT, HD>;
+  const int g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+  auto step = [&](int k, const uint32_t (&a)[4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint2 b = lds64(q_frag + ((k * NT + n) * 32 + lane) * 8);
+      mma(s[n], a, b.x, b.y);
+    }
+  };
+  if constexpr (FMT == PDS_KV_BF16) {
+#pragma unroll
+    for (int c = 0; c < HD / 32; ++c) {
+      const uint4 x = lds128(ks + F::k_at(g, t4 + 4 * c));
+      const uint4 y = lds128(ks + F::k_at(g + 8, t4 + 4 * c));
+      const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
+      step(2 * c, a0);
+      step(2 * c + 1, a1);
+    }
+  } else if constexpr (FMT == PDS_KV_E4M3) {
+#pragma unroll
+    for (int c = 0; c < HD / 64; ++c) {
+      const uint4 xv = lds128(ks + F::k_at(g, t4 + 4 * c));
+      const uint4 yv = lds128(ks + F::k_at(g + 8, t4 + 4 * c));
+      const uint32_t x[4] = {xv.x, xv.y, xv.z, xv.w}, y[4] = {yv.x, yv.y, yv.z, yv.w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t a[4] = {e4m3_pair(x[w] << 8), e4m3_pair(y[w] << 8), e4m3_pair(x[w]),
+                               e4m3_pair(y[w])};
+        step(4 * c + w, a);
+      }
+    }
+  } else {
+    constexpr int kWords = HD / 32;
+    uint32_t x[4], y[4];
+    if constexpr (HD == 128) {
+      const uint4 xv = lds128(ks + F::k_at(g, t4)), yv = lds128(ks + F::k_at(g + 8, t4));
+      x[0] = xv.x, x[1] = xv.y, x[2] = xv.z, x[3] = xv.w;
+      y[0] = yv.x, y[1] = yv.y, y[2] = yv.z, y[3] = yv.w;
+    } else {
+      const uint2 xv = lds64(ks + F::k_at(g, t4 >> 1) + 8 * (t4 & 1));
+      const uint2 yv = lds64(ks + F::k_at(g + 8, t4 >> 1) + 8 * (t4 & 1));
+      x[0] = xv.x, x[1] = xv.y;
+      y[0] = yv.x, y[1] = yv.y;
+    }
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      const uint32_t a0[4] = {int4_pair(x[w], kz0), int4_pair(y[w], kz1),
+                              int4_pair(x[w] >> 4, kz0), int4_pair(y[w] >> 4, kz1)};
+      const uint32_t a1[4] = {int4_pair(x[w] >> 8, kz0), int4_pair(y[w] >> 8, kz1),
+                              int4_pair(x[w] >> 12, kz0), int4_pair(y[w] >> 12, kz1)};
+      step(2 * w, a0);
+      step(2 * w + 1, a1);
+    }
+  }
+}
+
+// O^T += V^T P^T of one step; p: the B fragments of P^T (two registers per
+// column tile); vz0, vz1: zero points of keys (2t, 2t+1) and (2t+8, 2t+9).
+template <int FMT, int HD, int NT>
+__device__ __forceinline__ void accumulate(uint32_t vs, int lane, uint32_t vz0, uint32_t vz1,
+                                           const uint32_t (&p)[NT][2],
+                                           float (&o)[Fmt<FMT, HD>::kMTiles][NT][4]) {
+  using F = Fmt<FMT, HD>;
+  const int g = lane >> 2, t4 = lane & 3;
+  if constexpr (FMT == PDS_KV_BF16) {
+    const int key = (lane & 7) + ((lane >> 4) << 3), odd = (lane >> 3) & 1;
+#pragma unroll
+    for (int i = 0; i < F::kMTiles; ++i) {
+      uint32_t a[4];
+      ldsm4_t(vs + F::v_at(key, 2 * i + odd), a);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma(o[i][n], a, p[n][0], p[n][1]);
+    }
+  } else {
+    // this lane's channels of keys 2t, 2t+1, 2t+8, 2t+9
+    constexpr int kBytes = F::kRow / 8;          // of one key
+    constexpr int kW = kBytes <= 4 ? 1 : kBytes / 4;
+    uint32_t w[4][kW];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = 2 * t4 + (i & 1) + 8 * (i >> 1);
+      if constexpr (kBytes == 16) {
+        const uint4 x = lds128(vs + F::v_at(key, g));
+        w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+      } else if constexpr (kBytes == 8) {
+        const uint2 x = lds64(vs + F::v_at(key, g >> 1) + 8 * (g & 1));
+        w[i][0] = x.x, w[i][1] = x.y;
+      } else {
+        w[i][0] = lds32(vs + F::v_at(key, g >> 2) + 4 * (g & 3));
+      }
+    }
+    if constexpr (FMT == PDS_KV_E4M3) {
+#pragma unroll
+      for (int i = 0; i < F::kMTiles; ++i) {
+        // channel tile i: bytes 2 (i & 1) and + 1 of word i / 2, both keys of a pair
+        const int x = i >> 1;
+        const uint32_t sel = (i & 1) ? 0x6020u : 0x4000u, sel1 = (i & 1) ? 0x7030u : 0x5010u;
+        const uint32_t a[4] = {e4m3_pair(__byte_perm(w[0][x], w[1][x], sel)),
+                               e4m3_pair(__byte_perm(w[0][x], w[1][x], sel1)),
+                               e4m3_pair(__byte_perm(w[2][x], w[3][x], sel)),
+                               e4m3_pair(__byte_perm(w[2][x], w[3][x], sel1))};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma(o[i][n], a, p[n][0], p[n][1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < F::kMTiles; ++i) {
+        // channel tile i: the two nibbles of byte i % 4 of word i / 4
+        const int x = i >> 2, b = i & 3;
+        const uint32_t sel = b | (static_cast<uint32_t>(4 + b) << 8);  // into bytes 0 and 2
+        const uint32_t r0 = __byte_perm(w[0][x], w[1][x], sel);
+        const uint32_t r1 = __byte_perm(w[2][x], w[3][x], sel);
+        const uint32_t a[4] = {int4_pair(r0, vz0), int4_pair(r0 >> 4, vz0), int4_pair(r1, vz1),
+                               int4_pair(r1 >> 4, vz1)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma(o[i][n], a, p[n][0], p[n][1]);
+      }
+    }
+  }
+}
+
+template <int FMT, int HD, int NT>
+struct Cfg {
+  using F = Fmt<FMT, HD>;
+  static constexpr int kRows = 8 * NT;
+  // one block per SM where its registers (32 rows) or its stages (16 KB per
+  // warp in flight) fill it, else two
+  static constexpr int kBlocks = NT == 4 || F::kStage > 8192 ? 1 : 2;
+  static constexpr int kFit = (kBlocks == 1 ? 200 : 100) * 1024 / (kWarps * F::kStage);
+  static constexpr int kStages = kFit < 6 ? kFit : 6;
+  static_assert(kStages >= 2, "a step is read while another is fetched");
+  static constexpr int kQ = 0;  // B fragments of Q
+  static constexpr int kQBytes = F::kKSteps * NT * 32 * 8;
+  static constexpr int kMask = kQ + kQBytes;                  // ancestors of the tile's tokens
+  static constexpr int kDepth = kMask + kRows * kMaskWords * 4;
+  static constexpr int kParent = kDepth + kMaxDraftTokens * 2;
+  static constexpr int kMl = kParent + kMaxDraftTokens * 4;   // per warp and row: (maximum, sum)
+  static constexpr int kMisc = kMl + kWarps * kRows * 8;
+  static constexpr int kRing = (kMisc + 64 + 127) / 128 * 128;
+  static constexpr int kRingBytes = kWarps * kStages * F::kStage;
+  // the warps' O rows are joined in the space of the ring
+  static constexpr int kJoinStride = HD + 4;
+  static constexpr int kJoin = kWarps * kRows * kJoinStride * 4;
+  static constexpr int kSmem = kRing + (kRingBytes > kJoin ? kRingBytes : kJoin);
+  static_assert(kSmem * kBlocks <= 228 * 1024 - 1024 * kBlocks, "shared memory per SM");
+};
+
+// VAR: the call has a softcap or a window.
+template <int FMT, int HD, int NT, bool VAR>
+__global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
+    cache_attn_kernel(const __grid_constant__ Args a) {
+  using F = Fmt<FMT, HD>;
+  using C = Cfg<FMT, HD, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + C::kMask);
+  int16_t* depth = reinterpret_cast<int16_t*>(smem + C::kDepth);
+  int32_t* par = reinterpret_cast<int32_t*>(smem + C::kParent);
+  float2* ml = reinterpret_cast<float2*>(smem + C::kMl);
+  Unit* shared_unit = reinterpret_cast<Unit*>(smem + C::kMisc);
+  int* shared_ok = reinterpret_cast<int*>(smem + C::kMisc + 48);
+
+  const int per = a.c.n_kv_heads * a.row_tiles;
+  const int w = blockIdx.x / per, p = blockIdx.x - w * per;
+  const int head = p % a.c.n_kv_heads, tile = p / a.c.n_kv_heads;
+  if (warp == 0) {
+    Unit u{};
+    const int c = chunk_steps(a, lane);
+    const bool ok = find_unit(a, c, w, 0, lane, u);
+    if (lane == 0) {
+      *shared_unit = u;
+      *shared_ok = ok;
+    }
+    if (blockIdx.x == 0) {  // report lengths that do not fit
+      bool bad = false;
+      int first, len;
+      for (int s = lane; s < a.c.n_seqs; s += 32) bad |= seq_steps(a, s, first, len) == 0;
+      if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kStatusBadLength);
+    }
+  }
+  __syncthreads();
+  if (!*shared_ok) return;
+  const Unit u = *shared_unit;
+  const int r0 = tile * C::kRows;                        // first query row
+  const int rows = a.n_tokens * a.group;
+  const int end = u.len + a.n_tokens;                    // keys [.., end)
+
+  // this warp's steps: u.first + warp, + kWarps, ...
+  const uint32_t ring = smem_addr(smem) + C::kRing + warp * C::kStages * F::kStage;
+  const char* k_base = a.c.k + u.seq * a.c.seq_stride + head * a.c.head_stride;
+  const char* v_base = a.c.v + u.seq * a.c.seq_stride + head * a.c.head_stride;
+  const int64_t word0 = (static_cast<int64_t>(u.seq) * a.c.n_kv_heads + head) * a.c.capacity;
+  const int n_mine = u.n_steps > warp ? (u.n_steps - warp - 1) / kWarps + 1 : 0;
+  auto fetch = [&](int i) {  // step i of this warp into stage i % kStages
+    if (i < n_mine) {
+      const int j0 = (u.first + warp + i * kWarps) * kStep;
+      const uint32_t st = ring + (i % C::kStages) * F::kStage;
+#pragma unroll
+      for (int x = 0; x < (kStep * F::kChunks + 31) / 32; ++x) {
+        const int idx = x * 32 + lane;
+        const int r = idx / F::kChunks, ch = idx - r * F::kChunks;
+        const bool live = j0 + r < end;
+        // a row past the end is not read: its address is that of the last one
+        const int64_t off = static_cast<int64_t>(live ? j0 + r : end - 1) * a.c.row_stride + ch * 16;
+        copy16(st + F::k_at(r, ch), k_base + off, live);
+        copy16(st + F::kSlice + F::v_at(r, ch), v_base + off, live);
+      }
+      if constexpr (FMT != PDS_KV_BF16) {
+        const int r = lane & 15;
+        const bool live = j0 + r < end;
+        const uint32_t* src = (lane < 16 ? a.c.k_scale : a.c.v_scale) + word0;
+        copy4(st + 2 * F::kSlice + lane * 4, src + (live ? j0 + r : end - 1), live);
+      }
+    }
+    copies_commit();
+  };
+  for (int i = 0; i < C::kStages - 1; ++i) fetch(i);
+
+  // Q as B fragments, in the contraction's channel order; rows past the last are zero
+  for (int idx = threadIdx.x; idx < F::kKSteps * NT * 32; idx += kThreads) {
+    const int l = idx & 31, n = (idx >> 5) % NT, ks = idx / (32 * NT);
+    const int r = r0 + 8 * n + (l >> 2);
+    uint32_t b[2] = {0u, 0u};
+    if (r < rows) {
+      const int t = r / a.group, i = r - t * a.group;
+      const uint16_t* src = a.q + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.q_stride +
+                            (head * a.group + i) * HD;
+      int ch[4];
+      F::q_channels(ks, l & 3, ch);
+      b[0] = src[ch[0]] | static_cast<uint32_t>(src[ch[1]]) << 16;
+      b[1] = src[ch[2]] | static_cast<uint32_t>(src[ch[3]]) << 16;
+    }
+    *reinterpret_cast<uint2*>(smem + C::kQ + idx * 8) = make_uint2(b[0], b[1]);
+  }
+  // depths of all tokens and ancestor sets of this tile's
+  const int t_first = r0 / a.group;
+  {
+    const int t = threadIdx.x;
+    if (a.parents && t < a.n_tokens)
+      par[t] = a.parents[static_cast<int64_t>(u.seq) * a.n_tokens + t];
+    const int tl = t - t_first;
+    const bool here = tl >= 0 && tl < C::kRows && t < a.n_tokens;
+    __syncthreads();
+    if (t < a.n_tokens) {
+      const int d = a.parents ? tree_depth(par, t) : t;
+      depth[t] = static_cast<int16_t>(d);
+      if (d == kBadParent) atomicOr(a.status, kStatusBadParent);
+      if (here) {
+        uint32_t bits[kMaskWords];
+#pragma unroll
+        for (int i = 0; i < kMaskWords; ++i)
+          bits[i] = a.parents || t < 32 * i ? 0u
+                    : t >= 32 * i + 31       ? 0xffffffffu
+                                             : (2u << (t - 32 * i)) - 1u;
+        if (a.parents && d >= 0)
+          for (int x = t; x >= 0; x = par[x])
+#pragma unroll
+            for (int i = 0; i < kMaskWords; ++i)
+              if ((x >> 5) == i) bits[i] |= 1u << (x & 31);
+#pragma unroll
+        for (int i = 0; i < kMaskWords; ++i) mask[tl * kMaskWords + i] = bits[i];
+      }
+    }
+  }
+  __syncthreads();
+
+  // this lane's rows: 8 n + 2 t4 + {0, 1}; their tokens (within the tile) and positions
+  int tok[NT][2], pos[NT][2];
+  int pos_hi = 0;  // windows of all rows of the tile start at or below pos_hi - window + 1
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = r0 + 8 * n + 2 * t4 + e;
+      const int t = r < rows ? r / a.group : -1;
+      tok[n][e] = t < 0 || depth[t] < 0 ? -1 : t - t_first;
+      pos[n][e] = u.len + (t < 0 ? 0 : depth[t]);
+      pos_hi = max(pos_hi, pos[n][e]);
+    }
+  if (VAR) pos_hi = __reduce_max_sync(0xffffffffu, pos_hi);
+
+  float o[F::kMTiles][NT][4];
+#pragma unroll
+  for (int i = 0; i < F::kMTiles; ++i)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
+  float m_ref[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) m_ref[n][e] = -INFINITY, l[n][e] = 0.f;
+
+  const uint32_t q_frag = smem_addr(smem) + C::kQ;
+  for (int i = 0; i < n_mine; ++i) {
+    copies_wait<C::kStages - 2>();
+    __syncwarp();
+    fetch(i + C::kStages - 1);  // into the stage that step i - 1 has been read from
+    const uint32_t st = ring + (i % C::kStages) * F::kStage;
+    const int j0 = (u.first + warp + i * kWarps) * kStep;
+
+    // scale words of this lane's keys: g, g + 8 (rows of S^T), and the zero
+    // points that the operands need
+    float kscale[2] = {1.f, 1.f}, vscale[2] = {1.f, 1.f};
+    uint32_t kz[2] = {0u, 0u}, vz[2] = {0u, 0u};
+    if constexpr (FMT != PDS_KV_BF16) {
+      const uint32_t sw = st + 2 * F::kSlice;
+      uint32_t kw[2], vw[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        kw[e] = lds32(sw + (g + 8 * e) * 4);
+        vw[e] = lds32(sw + 64 + (g + 8 * e) * 4);
+        if constexpr (FMT == PDS_KV_INT4) {
+          kz[e] = 0x43004300u | (kw[e] & 15u) | (kw[e] & 15u) << 16;
+          kw[e] &= 0xffff0000u;
+          vw[e] &= 0xffff0000u;
+          const uint2 z = lds64(sw + 64 + (2 * t4 + 8 * e) * 4);
+          vz[e] = 0x43004300u | (z.x & 15u) | (z.y & 15u) << 16;
+        }
+        kscale[e] = __uint_as_float(kw[e]);
+        vscale[e] = __uint_as_float(vw[e]);
+      }
+    }
+
+    float s[NT][4];
+    scores<FMT, HD, NT>(st, q_frag, lane, kz[0], kz[1], s);
+
+    // scaled scores in powers of two
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float z = s[n][e] * kscale[e >> 1];
+        if (VAR && a.cap > 0.f) {
+          // c tanh(z / c) = c - 2 c / (2^(2 log2(e) z / c) + 1)
+          const float ex = exp2_fast(z * (2.0f * 1.4426950408889634f / a.cap));
+          z = a.cap - __fdividef(2.0f * a.cap, ex + 1.0f);
+        }
+        s[n][e] = z * a.scale_log2;
+      }
+    // a step that holds new tokens, the end, or a window's lower edge
+    bool masked = j0 + kStep > u.len;
+    if (VAR && a.window > 0) masked |= j0 <= pos_hi - a.window;
+    if (masked) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = j0 + g + 8 * e, rel = j - u.len;
+        const int key_pos = rel < 0 ? j : u.len + (rel < a.n_tokens ? depth[rel] : 0);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int t = tok[n][x];
+            bool see = t >= 0;
+            if (see && rel >= 0)
+              see = rel < a.n_tokens && ((mask[t * kMaskWords + (rel >> 5)] >> (rel & 31)) & 1u);
+            if (VAR && a.window > 0) see = see && key_pos > pos[n][x] - a.window;
+            if (!see) s[n][2 * e + x] = -INFINITY;
+          }
+      }
+    }
+    // move the reference maxima where a score is far above
+    bool far = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) far |= s[n][e] > m_ref[n][e & 1] + kMoveLog2;
+    if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float m = fmaxf(s[n][x], s[n][2 + x]);
+#pragma unroll
+          for (int sh = 4; sh < 32; sh <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
+          if (m > m_ref[n][x] + kMoveLog2) {
+            const float alpha = exp2f(m_ref[n][x] - m);  // 0 from -inf
+            m_ref[n][x] = m;
+            l[n][x] *= alpha;
+#pragma unroll
+            for (int t = 0; t < F::kMTiles; ++t) {
+              o[t][n][x] *= alpha;
+              o[t][n][2 + x] *= alpha;
+            }
+          }
+        }
+    }
+    // P, its row sums (float32, unrounded) and its transposed fragments
+    uint32_t pf[NT][2];
+    float pv[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float m = m_ref[n][e & 1];
+        const float pe = exp2_fast(s[n][e] - (m == -INFINITY ? 0.f : m));
+        l[n][e & 1] += pe;
+        pv[n][e] = pe;
+        if constexpr (FMT != PDS_KV_BF16)  // a hidden row may have any scale, a NaN too
+          pv[n][e] = masked && pe == 0.f ? 0.f : pe * vscale[e >> 1];
+      }
+      pf[n][0] = transpose8(pack_bf16x2(pv[n][0], pv[n][1]));
+      pf[n][1] = transpose8(pack_bf16x2(pv[n][2], pv[n][3]));
+    }
+    if constexpr (FMT == PDS_KV_BF16) {
+      // A hidden row of a masked step may hold an infinity or a NaN, which a
+      // zero weight would not keep out of the product: such a step is summed
+      // element by element, over what each row sees.
+      if (masked) {
+        bool bad = false;
+#pragma unroll
+        for (int x = 0; x < F::kSlice / 512; ++x) {
+          const uint4 v = lds128(st + F::kSlice + (x * 32 + lane) * 16);
+          bad |= not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) || not_finite2(v.w);
+        }
+        if (__any_sync(0xffffffffu, bad)) {
+          for (int key = 0; key < kStep; ++key) {
+            const int src = (key & 7) * 4 + t4;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const float lo0 = __shfl_sync(0xffffffffu, pv[n][0], src);
+              const float lo1 = __shfl_sync(0xffffffffu, pv[n][1], src);
+              const float hi0 = __shfl_sync(0xffffffffu, pv[n][2], src);
+              const float hi1 = __shfl_sync(0xffffffffu, pv[n][3], src);
+              const float p0 = key < 8 ? lo0 : hi0, p1 = key < 8 ? lo1 : hi1;
+#pragma unroll
+              for (int t = 0; t < F::kMTiles; ++t)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                  const int ch = F::o_channel(t, hh, g);
+                  uint16_t b;
+                  asm volatile("ld.shared.u16 %0, [%1];"
+                               : "=h"(b)
+                               : "r"(st + F::kSlice + F::v_at(key, ch >> 3) + (ch & 7) * 2));
+                  const float v = bf16_to_f32(b);
+                  if (p0 != 0.f) o[t][n][2 * hh] += p0 * v;
+                  if (p1 != 0.f) o[t][n][2 * hh + 1] += p1 * v;
+                }
+            }
+          }
+          continue;
+        }
+      }
+    }
+    accumulate<FMT, HD, NT>(st + F::kSlice, lane, vz[0], vz[1], pf, o);
+  }
+  copies_wait<0>();
+
+  // Join the warps: sums over the lanes that share rows, then over the warps,
+  // in warp order.
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+      for (int sh = 4; sh < 32; sh <<= 1) l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], sh);
+      if (g == 0) ml[warp * C::kRows + 8 * n + 2 * t4 + x] = make_float2(m_ref[n][x], l[n][x]);
+    }
+  __syncthreads();  // every warp is done with the ring
+  float* join = reinterpret_cast<float*>(smem + C::kRing);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float* dst = join + (warp * C::kRows + 8 * n + 2 * t4 + x) * C::kJoinStride;
+#pragma unroll
+      for (int t = 0; t < F::kMTiles; ++t) {
+        if constexpr (FMT == PDS_KV_BF16) {
+          dst[F::o_channel(t, 0, g)] = o[t][n][x];
+          dst[F::o_channel(t, 1, g)] = o[t][n][2 + x];
+        } else {
+          *reinterpret_cast<float2*>(dst + F::o_channel(t, 0, g)) =
+              make_float2(o[t][n][x], o[t][n][2 + x]);
+        }
+      }
+    }
+  __syncthreads();
+  const bool whole = u.n_chunks == 1;
+  for (int idx = threadIdx.x; idx < C::kRows * (HD / 4); idx += kThreads) {
+    const int r = idx / (HD / 4), ch = (idx - r * (HD / 4)) * 4;
+    if (r0 + r >= rows) break;
+    const int t = (r0 + r) / a.group, i = r0 + r - t * a.group;
+    float m = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) m = fmaxf(m, ml[x * C::kRows + r].x);
+    const float mu = m == -INFINITY ? 0.f : m;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) {
+      const float2 v = ml[x * C::kRows + r];
+      const float f = exp2f(v.x - mu);  // 0 for a warp that saw none of the row's keys
+      const float4 y = *reinterpret_cast<const float4*>(join + (x * C::kRows + r) * C::kJoinStride + ch);
+      sum += v.y * f;
+      acc.x += y.x * f;
+      acc.y += y.y * f;
+      acc.z += y.z * f;
+      acc.w += y.w * f;
+    }
+    if (depth[t] < 0) {  // a padding token's rows went along with the others
+      m = -INFINITY;
+      sum = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (whole) {
+      const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // a row that sees nothing is zero
+      uint16_t* dst = a.o + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.o_stride +
+                      (head * a.group + i) * HD + ch;
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    } else {
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * C::kRows + r;
+      *reinterpret_cast<float4*>(a.o_part + slot * HD + ch) = acc;
+      if (ch == 0) a.ml_part[slot] = make_float2(m, sum);
+    }
+  }
+}
+
+// One warp per (sequence, token, head): the row's chunks joined in order.
+template <int HD>
+__global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ Args a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+  const int per_seq = a.n_tokens * a.n_heads;
+  const int64_t seq64 = row / per_seq;
+  if (seq64 >= a.c.n_seqs) return;
+  const int seq = static_cast<int>(seq64), rest = static_cast<int>(row - seq64 * per_seq);
+  const int t = rest / a.n_heads, h = rest - t * a.n_heads;
+  Unit u;
+  const int c = chunk_steps(a, lane);
+  find_unit(a, c, -1, seq, lane, u);
+  if (u.n_chunks <= 1) return;  // written by its block, or refused
+  const int head = h / a.group, r = t * a.group + h - head * a.group;
+  const int tile = r / a.tile_rows;
+  const int per = a.c.n_kv_heads * a.row_tiles;
+  const int64_t first = (static_cast<int64_t>(u.base) * per + tile * a.c.n_kv_heads + head) *
+                            a.tile_rows + (r - tile * a.tile_rows);
+  const int64_t stride = static_cast<int64_t>(per) * a.tile_rows;
+  float m = -INFINITY;
+  for (int x = lane; x < u.n_chunks; x += 32) m = fmaxf(m, a.ml_part[first + x * stride].x);
+  m = warp_max(m);
+  const float mu = m == -INFINITY ? 0.f : m;
+  constexpr int kPer = HD / 32;
+  float acc[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+  float sum = 0.f;
+#pragma unroll 4
+  for (int x = 0; x < u.n_chunks; ++x) {
+    const int64_t slot = first + x * stride;
+    const float2 v = a.ml_part[slot];
+    const float f = exp2f(v.x - mu);
+    sum += v.y * f;
+    const float* src = a.o_part + slot * HD + lane * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] += src[i] * f;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  uint16_t* dst = a.o + (static_cast<int64_t>(seq) * a.n_tokens + t) * a.o_stride + h * HD + lane * kPer;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 2)
+    *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+}
+
+// ------------------------------------------------------------------ launch
+
+int column_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : kMaxTiles; }
+
+int blocks_per_sm(int format, int hd, int nt) {  // Cfg::kBlocks
+  return nt == kMaxTiles || (format == PDS_KV_BF16 && hd == 128) ? 1 : 2;
+}
+
+struct Shape {
+  int nt, row_tiles, per, slots, fit;
+};
+
+// How a call's rows are tiled and over how many blocks its keys are spread.
+Shape make_shape(int format, int hd, int n_seqs, int n_tokens, int n_heads, int n_kv_heads,
+                 int num_sms) {
+  Shape s{};
+  const int rows = n_tokens * (n_heads / n_kv_heads);
+  s.nt = column_tiles(rows);
+  s.row_tiles = (rows + 8 * s.nt - 1) / (8 * s.nt);
+  s.per = n_kv_heads * s.row_tiles;
+  const int64_t units = static_cast<int64_t>(n_seqs) * s.per;
+  const int resident = num_sms * blocks_per_sm(format, hd, s.nt);
+  s.fit = 2 * units <= resident;
+  s.slots = s.fit ? resident : 2 * resident;
+  return s;
+}
+
+int64_t max_units(const Shape& s, int n_seqs) {
+  return s.fit ? s.slots : s.slots + static_cast<int64_t>(n_seqs) * s.per;
+}
+
+template <int FMT, int HD, int NT, bool VAR>
+cudaError_t launch(const Args& a, int64_t grid, cudaStream_t st) {
+  using C = Cfg<FMT, HD, NT>;
+  static_assert(C::kBlocks == (NT == kMaxTiles || (FMT == PDS_KV_BF16 && HD == 128) ? 1 : 2),
+                "blocks_per_sm() says how many blocks an SM holds");
+  const cudaError_t ce = kernel_smem_attr(
+      reinterpret_cast<const void*>(cache_attn_kernel<FMT, HD, NT, VAR>), C::kSmem);
+  if (ce != cudaSuccess) return ce;
+  cache_attn_kernel<FMT, HD, NT, VAR><<<static_cast<unsigned>(grid), kThreads, C::kSmem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int FMT, int HD>
+cudaError_t launch_rows(const Args& a, int nt, int64_t grid, cudaStream_t st) {
+  const bool var = a.cap > 0.f || a.window > 0;
+  switch (nt) {
+    case 1: return var ? launch<FMT, HD, 1, true>(a, grid, st) : launch<FMT, HD, 1, false>(a, grid, st);
+    case 2: return var ? launch<FMT, HD, 2, true>(a, grid, st) : launch<FMT, HD, 2, false>(a, grid, st);
+    default: return var ? launch<FMT, HD, 4, true>(a, grid, st) : launch<FMT, HD, 4, false>(a, grid, st);
+  }
+}
+
+template <int HD>
+cudaError_t launch_format(const Args& a, int format, int nt, int64_t grid, cudaStream_t st) {
+  switch (format) {
+    case PDS_KV_BF16: return launch_rows<PDS_KV_BF16, HD>(a, nt, grid, st);
+    case PDS_KV_E4M3: return launch_rows<PDS_KV_E4M3, HD>(a, nt, grid, st);
+    default: return launch_rows<PDS_KV_INT4, HD>(a, nt, grid, st);
+  }
+}
+
+}  // namespace
+
+size_t tree_attention_ws_bytes(int format, int hd, int n_seqs, int n_tokens, int n_heads,
+                               int n_kv_heads, int num_sms) {
+  const Shape s = make_shape(format, hd, n_seqs, n_tokens, n_heads, n_kv_heads, num_sms);
+  return static_cast<size_t>(max_units(s, n_seqs)) * (8 * s.nt) * (hd * 4 + 8);
+}
+
+pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* err) {
+  const CacheView& c = t.cache;
+  const Shape s = make_shape(t.format, t.head_dim, c.n_seqs, t.n_tokens, t.n_heads, c.n_kv_heads,
+                             t.num_sms);
+  Args a{};
+  a.c = c;
+  a.q = t.q;
+  a.o = t.o;
+  a.q_stride = t.q_stride;
+  a.o_stride = t.o_stride;
+  a.parents = t.parents;
+  a.n_tokens = t.n_tokens;
+  a.n_heads = t.n_heads;
+  a.group = t.n_heads / c.n_kv_heads;
+  a.max_len = t.max_len;
+  a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(t.head_dim));
+  a.cap = t.softcap > 0.f ? t.softcap * sqrtf(static_cast<float>(t.head_dim)) : 0.f;
+  a.window = t.window;
+  a.row_tiles = s.row_tiles;
+  a.tile_rows = 8 * s.nt;
+  a.min_steps = 2 * kWarps;
+  a.status = t.status;
+  // a window's keys, with whole steps at both ends
+  const int64_t prefix = t.window > 0 ? std::min<int64_t>(t.max_len, int64_t{t.window} + 2 * kStep)
+                                      : t.max_len;
+  const int64_t span = prefix + t.n_tokens;
+  const int64_t most_chunks = (span + kStep * a.min_steps - 1) / (kStep * a.min_steps);
+  const int64_t units = static_cast<int64_t>(c.n_seqs) * s.per;
+  int64_t grid = units;
+  if (t.ws && most_chunks > 1) {
+    a.slots = s.slots;
+    a.fit = s.fit;
+    const int64_t most = max_units(s, c.n_seqs);
+    grid = std::min(most, units * most_chunks);
+    a.o_part = reinterpret_cast<float*>(t.ws);
+    a.ml_part = reinterpret_cast<float2*>(t.ws + static_cast<size_t>(most) * a.tile_rows *
+                                                     t.head_dim * 4);
+  }
+  cudaError_t ce = t.head_dim == 128 ? launch_format<128>(a, t.format, s.nt, grid, st)
+                                     : launch_format<64>(a, t.format, s.nt, grid, st);
+  if (ce == cudaSuccess && a.slots > 0) {
+    const int64_t rows = static_cast<int64_t>(c.n_seqs) * t.n_tokens * t.n_heads;
+    const unsigned blocks = static_cast<unsigned>((rows + 7) / 8);
+    if (t.head_dim == 128)
+      cache_join_kernel<128><<<blocks, 256, 0, st>>>(a);
+    else
+      cache_join_kernel<64><<<blocks, 256, 0, st>>>(a);
+    ce = cudaGetLastError();
+  }
+  if (ce != cudaSuccess) {
+    *err = std::string("cache attention launch: ") + cudaGetErrorString(ce);
+    return PDS_ELAUNCH;
+  }
+  return PDS_OK;
+}
+
+}  // namespace pds

@@ -11,6 +11,8 @@ namespace pds {
 enum : uint32_t {
   kStatusTimeout = 1u,      // a bounded mbarrier / flag wait gave up
   kStatusBadSchedule = 2u,  // a kernel met a work split it cannot serve
+  kStatusBadLength = 4u,    // a sequence's rows do not fit its cache (or the call's bound)
+  kStatusBadParent = 8u,    // a token's path of parents does not end in a root
 };
 
 __device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
@@ -38,6 +40,23 @@ __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
+}
+
+// Depth of token t of a forest given by parents (-1: a root): kNoToken for
+// padding (a parent below -1), kBadParent if the path upwards meets an index
+// that is not an earlier token or a padding token.  Every step goes to a smaller
+// index, so the walk ends.
+enum : int { kNoToken = -1, kBadParent = -2 };
+__device__ __forceinline__ int tree_depth(const int32_t* parents, int t) {
+  int p = parents[t], depth = 0;
+  if (p < -1) return kNoToken;
+  while (p != -1) {
+    if (p < -1 || p >= t) return kBadParent;
+    t = p;
+    p = parents[t];
+    ++depth;
+  }
+  return depth;
 }
 
 // Row scale of RMSNorm from the row's sum-of-squares partials (one per

@@ -1,0 +1,70 @@
+// Rotary positions, the quantised K/V cache and the attention of drafted
+// tokens over it: launch interface between the host library and the kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <string>
+
+#include "../../include/pds.h"
+
+namespace pds {
+
+// A pds_cache as the kernels see it: strides in bytes.
+struct CacheView {
+  char* k;
+  char* v;
+  uint32_t* k_scale;
+  uint32_t* v_scale;
+  const int32_t* lens;
+  int64_t seq_stride, row_stride, head_stride;
+  int n_seqs, capacity, n_kv_heads;
+};
+
+// Rotated pairs of a head: pair i turns by p * turns[i] / 2^64 of a full turn
+// at position p.
+constexpr int kMaxTurnPairs = 128;
+struct RopeTurns {
+  uint64_t turns[kMaxTurnPairs];
+  int rot_dim;  // rotated channels (2 * pairs); 0: no rotation
+  int layout;
+  float mscale;
+  float sign;   // -1: the inverse rotation
+};
+
+// The most tokens of a sequence that may form a tree, and that
+// pds_attention_tree takes.
+constexpr int kMaxDraftTokens = 256;
+
+struct TreeAttnCall {
+  CacheView cache;
+  int format, head_dim;
+  const uint16_t* q;
+  uint16_t* o;
+  int64_t q_stride, o_stride;  // elements
+  const int32_t* parents;
+  int n_tokens, n_heads;
+  int max_len;
+  float softcap;
+  int window;
+  char* ws;  // null: key ranges are not split
+  uint32_t* status;
+  int num_sms;
+};
+
+cudaError_t launch_rope(const RopeTurns& r, const uint16_t* x, uint16_t* y, int rows, int heads,
+                        int hd, int64_t x_stride, int64_t y_stride, const int32_t* positions,
+                        int start_pos, cudaStream_t st);
+cudaError_t launch_cache_write(const CacheView& c, int format, int hd, const RopeTurns& r,
+                               const uint16_t* k, const uint16_t* v, int n_tokens,
+                               int64_t k_stride, int64_t v_stride, const int32_t* parents,
+                               const int32_t* positions, uint32_t* status, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheView& c, int format, int hd, int first_row, int rows,
+                              uint16_t* k_out, uint16_t* v_out, uint32_t* status, cudaStream_t st);
+size_t tree_attention_ws_bytes(int format, int hd, int n_seqs, int n_tokens, int n_heads,
+                               int n_kv_heads, int num_sms);
+pds_status tree_attention(const TreeAttnCall& a, cudaStream_t st, std::string* err);
+
+}  // namespace pds

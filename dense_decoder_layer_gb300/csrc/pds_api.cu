@@ -21,6 +21,7 @@
 
 #include "../../include/pds.h"
 #include "kernels.h"
+#include "kv.h"
 #include "plan.h"
 #include "tc.h"
 
@@ -379,6 +380,316 @@ pds_status pds_attention(const uint16_t* q, const uint16_t* k, const uint16_t* v
                                      softcap, window, static_cast<char*>(workspace),
                                      workspace_bytes, static_cast<cudaStream_t>(stream), &err);
   if (st != PDS_OK) return fail(st, err);
+  return PDS_OK;
+}
+
+// ------------------------------------------------------ cached decoding
+
+namespace {
+
+// The turns of a spec's pairs; false (with a message) for a bad one.  A null
+// spec is no rotation.
+pds_status make_turns(const char* fn, const pds_rope_spec* spec, int hd, bool inverse,
+                      pds::RopeTurns* r) {
+  *r = pds::RopeTurns{};
+  if (!spec) return PDS_OK;
+  const pds_rope_spec& p = *spec;
+  const std::string name = fn;
+  if (!(p.theta > 0.f) || !std::isfinite(p.theta))
+    return fail(PDS_EINVAL, name + ": rope theta must be > 0");
+  if (p.layout != PDS_ROPE_NEOX && p.layout != PDS_ROPE_NORM)
+    return fail(PDS_EINVAL, name + ": rope layout must be PDS_ROPE_NEOX or PDS_ROPE_NORM");
+  if (p.rot_dim < 0 || p.rot_dim > hd)
+    return fail(PDS_EINVAL, name + ": rot_dim must be 0 .. head_dim");
+  const int rot = p.rot_dim ? p.rot_dim : hd;
+  if (rot % 16) return fail(PDS_DECLINED, "declined: " + name + " needs rot_dim % 16 == 0");
+  if (!std::isfinite(p.mscale) || p.mscale < 0.f)
+    return fail(PDS_EINVAL, name + ": rope mscale must be 0 or > 0");
+  if (p.scaling != PDS_ROPE_UNSCALED && p.scaling != PDS_ROPE_LINEAR && p.scaling != PDS_ROPE_YARN)
+    return fail(PDS_EINVAL, name + ": unknown rope scaling");
+  if (p.scaling != PDS_ROPE_UNSCALED && (!(p.factor > 0.f) || !std::isfinite(p.factor)))
+    return fail(PDS_EINVAL, name + ": rope factor must be > 0");
+  double lo = 0.0, hi = 0.0;
+  if (p.scaling == PDS_ROPE_YARN) {
+    if (!(p.theta > 1.f) || p.orig_context < 1 || !(p.beta_slow > 0.f) ||
+        !(p.beta_fast > p.beta_slow) || !std::isfinite(p.beta_fast))
+      return fail(PDS_EINVAL, name + ": YaRN needs theta > 1, orig_context >= 1, beta_fast > beta_slow > 0");
+    auto edge = [&](double beta) {
+      return rot * std::log(p.orig_context / (2.0 * M_PI * beta)) / (2.0 * std::log(double{p.theta}));
+    };
+    lo = std::max(0.0, std::floor(edge(p.beta_fast)));
+    hi = std::min(rot - 1.0, std::ceil(edge(p.beta_slow)));
+  }
+  // theta^(-2i/rot) in float64, eight neighbours from one power
+  const double next = std::pow(double{p.theta}, -2.0 / rot);
+  double omega = 1.0;
+  for (int i = 0; i < rot / 2; ++i) {
+    omega = i % 8 ? omega * next : std::pow(double{p.theta}, -2.0 * i / rot);
+    double w = omega;
+    if (p.freq_factors) {
+      const float f = p.freq_factors[i];
+      if (!(f > 0.f) || !std::isfinite(f))
+        return fail(PDS_EINVAL, name + ": freq_factors must be finite and > 0");
+      w /= f;
+    }
+    if (p.scaling == PDS_ROPE_LINEAR) w /= p.factor;
+    if (p.scaling == PDS_ROPE_YARN) {
+      const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 1e-3)));
+      w *= (1.0 - ramp) + ramp / p.factor;
+    }
+    // positions are whole numbers: whole turns per position drop out
+    const double turns = w / (2.0 * M_PI);
+    r->turns[i] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));
+  }
+  r->rot_dim = rot;
+  r->layout = p.layout;
+  r->mscale = p.mscale > 0.f ? p.mscale : 1.0f;
+  r->sign = inverse ? -1.0f : 1.0f;
+  return PDS_OK;
+}
+
+// The kernels' view of a cache, or the reason it is refused.
+pds_status make_view(const char* fn, const pds_cache* cache, pds::CacheView* v) {
+  const std::string name = fn;
+  if (!cache) return fail(PDS_EINVAL, name + ": cache is NULL");
+  const pds_cache& c = *cache;
+  if (c.format != PDS_KV_BF16 && c.format != PDS_KV_E4M3 && c.format != PDS_KV_INT4)
+    return fail(PDS_EINVAL, name + ": unknown cache format");
+  if (c.reserved != 0) return fail(PDS_EINVAL, name + ": cache.reserved must be 0");
+  if (c.n_seqs < 1 || c.capacity < 1 || c.n_kv_heads < 1 || c.head_dim < 1)
+    return fail(PDS_EINVAL, name + ": every cache size must be positive");
+  if (c.head_dim != 64 && c.head_dim != 128)
+    return fail(PDS_DECLINED, "declined: " + name + " needs head_dim 64 or 128");
+  if (c.n_seqs > 4096 || c.n_kv_heads > 1024 || c.capacity > (1 << 30))
+    return fail(PDS_DECLINED, "declined: " + name +
+                                  " serves at most 4096 sequences, 1024 kv heads and 2^30 rows");
+  if (!c.k || !c.v || !c.lens) return fail(PDS_EINVAL, name + ": cache k / v / lens is NULL");
+  if (!aligned16(c.k) || !aligned16(c.v))
+    return fail(PDS_EINVAL, name + ": cache k / v not 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(c.lens) & 3u)
+    return fail(PDS_EINVAL, name + ": cache lens not 4-byte aligned");
+  if (c.format != PDS_KV_BF16) {
+    if (!c.k_scale || !c.v_scale) return fail(PDS_EINVAL, name + ": cache scale words are NULL");
+    if ((reinterpret_cast<uintptr_t>(c.k_scale) | reinterpret_cast<uintptr_t>(c.v_scale)) & 3u)
+      return fail(PDS_EINVAL, name + ": cache scale words not 4-byte aligned");
+  }
+  int64_t hs = c.head_stride, rs = c.row_stride, ss = c.seq_stride;
+  if (hs == 0 && rs == 0 && ss == 0) {
+    hs = c.head_dim;
+    rs = hs * c.n_kv_heads;
+    ss = rs * c.capacity;
+  }
+  const int per16 = c.format == PDS_KV_BF16 ? 8 : c.format == PDS_KV_E4M3 ? 16 : 32;
+  if (hs < c.head_dim || rs < c.head_dim || (c.n_seqs > 1 ? ss < c.head_dim : ss < 0))
+    return fail(PDS_EINVAL, name + ": a cache stride is smaller than a head's row");
+  if (hs % per16 || rs % per16 || ss % per16)
+    return fail(PDS_EINVAL, name + ": cache strides must be multiples of 16 bytes");
+  // half bytes: elements to bytes
+  auto bytes = [&](int64_t e) { return c.format == PDS_KV_BF16 ? 2 * e : c.format == PDS_KV_E4M3 ? e : e / 2; };
+  *v = pds::CacheView{static_cast<char*>(c.k), static_cast<char*>(c.v), c.k_scale, c.v_scale,
+                      c.lens, bytes(ss), bytes(rs), bytes(hs), c.n_seqs, c.capacity, c.n_kv_heads};
+  return PDS_OK;
+}
+
+// A row stride in elements: 0 is packed.
+pds_status row_stride(const char* fn, int64_t packed, int64_t* stride) {
+  if (*stride == 0) *stride = packed;
+  if (*stride < packed || *stride % 8)
+    return fail(PDS_EINVAL, std::string(fn) + ": row strides must be 0, or multiples of 8 and no "
+                                              "smaller than a packed row");
+  return PDS_OK;
+}
+
+// The status word and SM count of the current device, looked up once per
+// device; ptr has to be memory of that device.
+constexpr int kMaxDevices = 64;
+struct DeviceFacts {
+  std::once_flag once;
+  uint32_t* status = nullptr;
+  int sms = 0;
+};
+pds_status device_facts(const char* fn, const void* ptr, uint32_t** status, int* sms) {
+  static DeviceFacts facts[kMaxDevices];
+  const std::string name = fn;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return fail(PDS_ELAUNCH, name + ": no CUDA device");
+  }
+  cudaPointerAttributes at{};
+  if (cudaPointerGetAttributes(&at, ptr) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(PDS_ELAUNCH, name + ": no CUDA device");
+  }
+  if ((at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) ||
+      (at.type == cudaMemoryTypeDevice && at.device != dev))
+    return fail(PDS_EINVAL, name + ": a buffer is not memory of the current device");
+  DeviceFacts& f = facts[dev];
+  std::string err;
+  std::call_once(f.once, [&] {
+    f.status = pds::component_status(&err);
+    if (cudaDeviceGetAttribute(&f.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) f.sms = 0;
+  });
+  if (!f.status || f.sms < 1) return fail(PDS_ELAUNCH, name + ": status word or SM count: " + err);
+  *status = f.status;
+  *sms = f.sms;
+  return PDS_OK;
+}
+
+pds_status launched(const char* fn, cudaError_t ce) {
+  if (ce == cudaSuccess) return PDS_OK;
+  return fail(PDS_ELAUNCH, std::string(fn) + " launch: " + cudaGetErrorString(ce));
+}
+
+}  // namespace
+
+pds_status pds_rope(const pds_rope_spec* spec, const uint16_t* x, uint16_t* y, int32_t rows,
+                    int32_t n_heads, int32_t head_dim, int64_t x_stride, int64_t y_stride,
+                    const int32_t* positions, int32_t start_pos, int32_t inverse, void* stream) {
+  if (!spec || !x || !y) return fail(PDS_EINVAL, "pds_rope: NULL operand");
+  if (rows < 1 || n_heads < 1 || head_dim < 1) return fail(PDS_EINVAL, "pds_rope: bad size");
+  if (head_dim % 16 || head_dim > 256 || n_heads > (1 << 20))
+    return fail(PDS_DECLINED, "declined: pds_rope needs head_dim % 16 == 0, head_dim <= 256");
+  if (!aligned16(x) || !aligned16(y) || (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return fail(PDS_EINVAL, "pds_rope: operand not aligned");
+  const int64_t packed = static_cast<int64_t>(n_heads) * head_dim;
+  pds_status rc;
+  if ((rc = row_stride("pds_rope", packed, &x_stride)) != PDS_OK ||
+      (rc = row_stride("pds_rope", packed, &y_stride)) != PDS_OK)
+    return rc;
+  if (x == y && x_stride != y_stride)
+    return fail(PDS_EINVAL, "pds_rope: in place needs one stride");
+  pds::RopeTurns turns;
+  if ((rc = make_turns("pds_rope", spec, head_dim, inverse != 0, &turns)) != PDS_OK) return rc;
+  uint32_t* status;
+  int sms;
+  if ((rc = device_facts("pds_rope", x, &status, &sms)) != PDS_OK) return rc;
+  return launched("pds_rope", pds::launch_rope(turns, x, y, rows, n_heads, head_dim, x_stride,
+                                               y_stride, positions, start_pos,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+pds_status pds_cache_write(const pds_cache* cache, const pds_rope_spec* spec, const uint16_t* k,
+                           const uint16_t* v, int32_t n_tokens, int64_t k_stride,
+                           int64_t v_stride, const int32_t* parents, const int32_t* positions,
+                           void* stream) {
+  pds::CacheView view;
+  pds_status rc = make_view("pds_cache_write", cache, &view);
+  if (rc != PDS_OK) return rc;
+  if (!k || !v) return fail(PDS_EINVAL, "pds_cache_write: NULL operand");
+  if (!aligned16(k) || !aligned16(v) ||
+      ((reinterpret_cast<uintptr_t>(parents) | reinterpret_cast<uintptr_t>(positions)) & 3u))
+    return fail(PDS_EINVAL, "pds_cache_write: operand not aligned");
+  if (n_tokens < 1) return fail(PDS_EINVAL, "pds_cache_write: n_tokens must be >= 1");
+  if (n_tokens > cache->capacity)
+    return fail(PDS_DECLINED, "declined: pds_cache_write: more tokens than the cache's capacity");
+  if (parents && n_tokens > pds::kMaxDraftTokens)
+    return fail(PDS_DECLINED, "declined: pds_cache_write: at most 256 tokens with parents");
+  if (static_cast<int64_t>(cache->n_seqs) * n_tokens > INT32_MAX)
+    return fail(PDS_DECLINED, "declined: pds_cache_write: too many rows");
+  const int64_t packed = static_cast<int64_t>(cache->n_kv_heads) * cache->head_dim;
+  if ((rc = row_stride("pds_cache_write", packed, &k_stride)) != PDS_OK ||
+      (rc = row_stride("pds_cache_write", packed, &v_stride)) != PDS_OK)
+    return rc;
+  pds::RopeTurns turns;
+  if ((rc = make_turns("pds_cache_write", spec, cache->head_dim, false, &turns)) != PDS_OK)
+    return rc;
+  uint32_t* status;
+  int sms;
+  if ((rc = device_facts("pds_cache_write", cache->k, &status, &sms)) != PDS_OK) return rc;
+  return launched("pds_cache_write",
+                  pds::launch_cache_write(view, cache->format, cache->head_dim, turns, k, v,
+                                          n_tokens, k_stride, v_stride, parents, positions, status,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+pds_status pds_cache_read(const pds_cache* cache, int32_t first_row, int32_t rows,
+                          uint16_t* k_out, uint16_t* v_out, void* stream) {
+  pds::CacheView view;
+  pds_status rc = make_view("pds_cache_read", cache, &view);
+  if (rc != PDS_OK) return rc;
+  if (!k_out && !v_out) return fail(PDS_EINVAL, "pds_cache_read: k_out and v_out are NULL");
+  if (!aligned16(k_out) || !aligned16(v_out))
+    return fail(PDS_EINVAL, "pds_cache_read: output not 16-byte aligned");
+  if (rows < 1 || first_row < PDS_AT_LENS)
+    return fail(PDS_EINVAL, "pds_cache_read: rows must be >= 1 and first_row >= 0 or PDS_AT_LENS");
+  if (static_cast<int64_t>(first_row > 0 ? first_row : 0) + rows > cache->capacity)
+    return fail(PDS_DECLINED, "declined: pds_cache_read: rows past the cache's capacity");
+  uint32_t* status;
+  int sms;
+  if ((rc = device_facts("pds_cache_read", cache->k, &status, &sms)) != PDS_OK) return rc;
+  return launched("pds_cache_read",
+                  pds::launch_cache_read(view, cache->format, cache->head_dim, first_row, rows,
+                                         k_out, v_out, status, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pds_attention_tree_workspace_bytes(const pds_cache* cache, int32_t n_tokens,
+                                          int32_t n_heads) {
+  if (!cache || n_tokens < 1 || n_tokens > pds::kMaxDraftTokens || n_heads < 1 ||
+      cache->n_seqs < 1 || cache->n_seqs > 4096 || cache->n_kv_heads < 1 ||
+      n_heads % cache->n_kv_heads || (cache->head_dim != 64 && cache->head_dim != 128))
+    return 0;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return pds::tree_attention_ws_bytes(cache->format, cache->head_dim, cache->n_seqs, n_tokens,
+                                      n_heads, cache->n_kv_heads, sms);
+}
+
+pds_status pds_attention_tree(const pds_cache* cache, const uint16_t* q, uint16_t* o,
+                              int32_t n_tokens, int32_t n_heads, int64_t q_stride,
+                              int64_t o_stride, const int32_t* parents, float softcap,
+                              int32_t window, int32_t max_len, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  pds::TreeAttnCall a{};
+  pds_status rc = make_view("pds_attention_tree", cache, &a.cache);
+  if (rc != PDS_OK) return rc;
+  if (!q || !o) return fail(PDS_EINVAL, "pds_attention_tree: NULL operand");
+  if (n_tokens < 1 || n_heads < 1) return fail(PDS_EINVAL, "pds_attention_tree: bad size");
+  if (!(softcap >= 0.f) || !std::isfinite(softcap) || window < 0 || max_len < 0)
+    return fail(PDS_EINVAL, "pds_attention_tree: softcap, window and max_len must be >= 0");
+  if (n_heads % cache->n_kv_heads || n_heads > (1 << 20))
+    return fail(PDS_DECLINED, "declined: pds_attention_tree needs H % Hkv == 0");
+  if (n_tokens > pds::kMaxDraftTokens)
+    return fail(PDS_DECLINED, "declined: pds_attention_tree takes at most 256 tokens");
+  if (n_tokens > cache->capacity)
+    return fail(PDS_DECLINED, "declined: pds_attention_tree: more tokens than the cache's capacity");
+  if (!aligned16(q) || !aligned16(o) || (workspace && !aligned16(workspace)) ||
+      (reinterpret_cast<uintptr_t>(parents) & 3u))
+    return fail(PDS_EINVAL, "pds_attention_tree: operand not aligned");
+  const int64_t packed = static_cast<int64_t>(n_heads) * cache->head_dim;
+  if ((rc = row_stride("pds_attention_tree", packed, &q_stride)) != PDS_OK ||
+      (rc = row_stride("pds_attention_tree", packed, &o_stride)) != PDS_OK)
+    return rc;
+  if (static_cast<int64_t>(cache->n_seqs) * n_tokens * n_heads > INT32_MAX)
+    return fail(PDS_DECLINED, "declined: pds_attention_tree: too many query rows");
+  if ((rc = device_facts("pds_attention_tree", cache->k, &a.status, &a.num_sms)) != PDS_OK)
+    return rc;
+  if (workspace && workspace_bytes < pds::tree_attention_ws_bytes(
+                                         cache->format, cache->head_dim, cache->n_seqs, n_tokens,
+                                         n_heads, cache->n_kv_heads, a.num_sms))
+    return fail(PDS_EINVAL,
+                "pds_attention_tree: workspace smaller than pds_attention_tree_workspace_bytes");
+  a.format = cache->format;
+  a.head_dim = cache->head_dim;
+  a.q = q;
+  a.o = o;
+  a.q_stride = q_stride;
+  a.o_stride = o_stride;
+  a.parents = parents;
+  a.n_tokens = n_tokens;
+  a.n_heads = n_heads;
+  const int32_t room = cache->capacity - n_tokens;
+  a.max_len = max_len > 0 ? std::min(max_len, room) : room;
+  a.softcap = softcap;
+  a.window = window;
+  a.ws = static_cast<char*>(workspace);
+  std::string err;
+  rc = pds::tree_attention(a, static_cast<cudaStream_t>(stream), &err);
+  if (rc != PDS_OK) return fail(rc, err);
   return PDS_OK;
 }
 

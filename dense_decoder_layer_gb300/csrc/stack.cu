@@ -103,6 +103,12 @@ pds_status component_sync(cudaStream_t st, std::string* err) {
            std::to_string(flags) + ")";
     return PDS_ETIMEOUT;
   }
+  if (flags & (kStatusBadLength | kStatusBadParent)) {
+    *err = flags & kStatusBadLength
+               ? "a sequence's length and new tokens do not fit its cache or the call's max_len"
+               : "a drafted token's parents do not lead to a root through earlier tokens";
+    return PDS_EINVAL;
+  }
   if (flags) {
     *err = "component status word " + std::to_string(flags);
     return PDS_ELAUNCH;

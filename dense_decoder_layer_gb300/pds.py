@@ -50,6 +50,31 @@ class pds_layer(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in LAYER_FIELDS + EXTRA_FIELDS]
 
 
+PDS_ROPE_UNSCALED, PDS_ROPE_LINEAR, PDS_ROPE_YARN = 0, 1, 2
+
+
+class pds_rope_spec(ctypes.Structure):
+    _fields_ = [("theta", ctypes.c_float), ("layout", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("freq_factors", ctypes.POINTER(ctypes.c_float)), ("mscale", ctypes.c_float),
+                ("factor", ctypes.c_float), ("orig_context", ctypes.c_int32),
+                ("beta_fast", ctypes.c_float), ("beta_slow", ctypes.c_float)]
+
+
+PDS_KV_BF16, PDS_KV_E4M3, PDS_KV_INT4 = 0, 1, 2
+PDS_AT_LENS = -1
+
+
+class pds_cache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("capacity", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("seq_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p)]
+
+
 KERNEL_KINDS = ("prep", "qkv", "attn", "wo", "gateup", "down")
 
 
@@ -74,7 +99,9 @@ def load() -> ctypes.CDLL:
         pass
     lib = ctypes.CDLL(LIB_PATH)
     vp, sz, i32, st = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int
+    i64, f32 = ctypes.c_int64, ctypes.c_float
     pp = ctypes.POINTER(ctypes.c_void_p)
+    rope_p, cache_p = ctypes.POINTER(pds_rope_spec), ctypes.POINTER(pds_cache)
     sig = {
         "pds_plan_create": (st, [ctypes.POINTER(pds_dims), ctypes.POINTER(ctypes.c_void_p)]),
         "pds_plan_destroy": (None, [vp]),
@@ -94,6 +121,12 @@ def load() -> ctypes.CDLL:
         "pds_plan_set_timing": (st, [vp, i32]),
         "pds_selftest_stuck_wait": (st, [ctypes.c_uint32, vp]),
         "pds_component_sync": (st, [vp]),
+        "pds_rope": (st, [rope_p, vp, vp, i32, i32, i32, i64, i64, vp, i32, i32, vp]),
+        "pds_cache_write": (st, [cache_p, rope_p, vp, vp, i32, i64, i64, vp, vp, vp]),
+        "pds_cache_read": (st, [cache_p, i32, i32, vp, vp, vp]),
+        "pds_attention_tree": (st, [cache_p, vp, vp, i32, i32, i64, i64, vp, f32, i32, i32, vp, sz,
+                                    vp]),
+        "pds_attention_tree_workspace_bytes": (sz, [cache_p, i32, i32]),
         "pds_plan_kernel_times": (st, [vp, vp, ctypes.POINTER(pds_kernel_times), i32]),
     }
     for name, (res, args) in sig.items():
@@ -202,6 +235,34 @@ def pds_attention(q, k, v, o, batch, start_pos, n_heads, n_kv_heads, head_dim, s
 
 def pds_attention_workspace_bytes(batch, start_pos, n_heads, head_dim) -> int:
     return load().pds_attention_workspace_bytes(batch, start_pos, n_heads, head_dim)
+
+
+def pds_rope(spec, x, y, rows, n_heads, head_dim, stream, x_stride: int = 0, y_stride: int = 0,
+             positions=None, start_pos: int = 0, inverse: bool = False) -> None:
+    check(load().pds_rope(spec, x, y, rows, n_heads, head_dim, x_stride, y_stride, positions,
+                          start_pos, 1 if inverse else 0, stream))
+
+
+def pds_cache_write(cache, spec, k, v, n_tokens, stream, k_stride: int = 0, v_stride: int = 0,
+                    parents=None, positions=None) -> None:
+    check(load().pds_cache_write(cache, spec, k, v, n_tokens, k_stride, v_stride, parents,
+                                 positions, stream))
+
+
+def pds_cache_read(cache, first_row, rows, k_out, v_out, stream) -> None:
+    check(load().pds_cache_read(cache, first_row, rows, k_out, v_out, stream))
+
+
+def pds_attention_tree(cache, q, o, n_tokens, n_heads, stream, q_stride: int = 0,
+                       o_stride: int = 0, parents=None, softcap: float = 0.0, window: int = 0,
+                       max_len: int = 0, workspace=None, workspace_bytes: int = 0) -> None:
+    check(load().pds_attention_tree(cache, q, o, n_tokens, n_heads, q_stride, o_stride, parents,
+                                    softcap, window, max_len, workspace,
+                                    workspace_bytes if workspace else 0, stream))
+
+
+def pds_attention_tree_workspace_bytes(cache, n_tokens, n_heads) -> int:
+    return load().pds_attention_tree_workspace_bytes(cache, n_tokens, n_heads)
 
 
 def pds_plan_set_timing(plan, enable: bool) -> None:

@@ -288,8 +288,9 @@ pds_status pds_plan_kernel_times(pds_plan* plan, void* stream, pds_kernel_times*
  * pds_attention and pds_selftest_stuck_wait).  Returns PDS_ETIMEOUT if a
  * bounded device wait of any of their kernels gave up since the previous
  * pds_component_sync on this device (the output of that call is then not
- * valid), PDS_ELAUNCH if the stream reports a CUDA error, else PDS_OK.
- * Allocates nothing.
+ * valid), PDS_EINVAL if one of the cached-decoding calls (below) met a
+ * sequence length or a parent index that it cannot serve, PDS_ELAUNCH if the
+ * stream reports a CUDA error, else PDS_OK.  Allocates nothing.
  */
 pds_status pds_component_sync(void* stream);
 
@@ -361,6 +362,185 @@ pds_status pds_attention(const uint16_t* q, const uint16_t* k, const uint16_t* v
  */
 size_t pds_attention_workspace_bytes(int32_t batch, int32_t start_pos, int32_t n_heads,
                                      int32_t head_dim);
+
+/*
+ * Cached decoding: rotary positions, a K/V cache that may hold 8- or 4-bit
+ * rows, and attention of a few new tokens per sequence over it (no
+ * counterpart on the pages, whose cache is float32 on the host and whose
+ * decode is one token at a time).  Component entry points like the ones
+ * above: device buffers of the current device, enqueued on the stream
+ * without synchronizing, nothing allocated, capturable into a CUDA graph.
+ *
+ * What only the device can see -- a sequence length that does not fit, a
+ * parent that is not an earlier token -- is checked by the kernels before
+ * any address is formed from it; the rows concerned are neither read nor
+ * written (attention: their output is not written, or zero for a bad
+ * parent) and the next pds_component_sync returns PDS_EINVAL.
+ */
+
+/*
+ * Rotation of head channels by position.  rot_dim, layout, freq_factors and
+ * mscale mean what they mean in pds_dims; head_dim is an argument of the
+ * calls.  scaling stretches the context:
+ *   PDS_ROPE_UNSCALED  omega_i as in pds_dims
+ *   PDS_ROPE_LINEAR    omega_i / factor (positions divided by factor)
+ *   PDS_ROPE_YARN      omega_i ((1 - r_i) + r_i / factor),
+ *                      r_i = clamp((i - lo) / (hi - lo), 0, 1),
+ *                      lo = max(0, floor(edge(beta_fast))),
+ *                      hi = min(rot_dim - 1, ceil(edge(beta_slow))),
+ *                      edge(b) = rot_dim ln(orig_context / (2 pi b)) / (2 ln theta):
+ *                      pairs that turn more than beta_fast times within the
+ *                      original context keep their frequency, those that turn
+ *                      less than beta_slow times are interpolated (hi - lo is
+ *                      taken as at least 0.001).  Its usual attention factor
+ *                      0.1 ln(factor) + 1 is the caller's to put in mscale.
+ */
+enum { PDS_ROPE_UNSCALED = 0, PDS_ROPE_LINEAR = 1, PDS_ROPE_YARN = 2 };
+typedef struct pds_rope_spec {
+  float theta;               /* > 0 (YaRN: > 1)                            */
+  int32_t layout;            /* PDS_ROPE_NEOX or PDS_ROPE_NORM             */
+  int32_t rot_dim;           /* 0 (= head_dim), or a positive multiple of
+                                16, <= head_dim                            */
+  int32_t scaling;           /* PDS_ROPE_UNSCALED / _LINEAR / _YARN        */
+  const float* freq_factors; /* host [rot_dim/2] > 0, or NULL; not kept    */
+  float mscale;              /* 0 (= 1), or > 0                            */
+  float factor;              /* LINEAR, YARN: > 0                          */
+  int32_t orig_context;      /* YARN: > 0                                  */
+  float beta_fast;           /* YARN: > beta_slow                          */
+  float beta_slow;           /* YARN: > 0                                  */
+} pds_rope_spec;
+
+/*
+ * y = the rows of x turned at their positions: bf16 [rows, n_heads, head_dim]
+ * with head_dim a multiple of 16 up to 256; row r of x starts at element
+ * r * x_stride, of y at r * y_stride (0: packed, n_heads * head_dim; multiples
+ * of 8, no smaller than packed).  y may be x (same stride), else they must not
+ * overlap.  Row r is at position positions[r] (device int32, may be negative)
+ * or, with positions NULL, start_pos + r.  inverse != 0 turns the other way:
+ * for mscale 1 it undoes the rotation, and for any mscale it is the
+ * transpose, i.e. the gradient with respect to x of a loss whose gradient
+ * with respect to y is given as x.  Angles are exact to 2^-31 of a turn at any position;
+ * the products are float32, rounded once to bf16.
+ */
+pds_status pds_rope(const pds_rope_spec* spec, const uint16_t* x, uint16_t* y, int32_t rows,
+                    int32_t n_heads, int32_t head_dim, int64_t x_stride, int64_t y_stride,
+                    const int32_t* positions, int32_t start_pos, int32_t inverse, void* stream);
+
+/*
+ * A K/V cache of n_seqs sequences (one layer's).  The row of sequence s, row
+ * j and kv head g starts at element s seq_stride + j row_stride +
+ * g head_stride of k / v (all three 0: packed [n_seqs, capacity, n_kv_heads,
+ * head_dim]; an "element" is one channel, so half a byte for PDS_KV_INT4; every
+ * stride a multiple of 16 bytes and no smaller than a head's row, and rows
+ * must not overlap).  The head's channels are contiguous.  A cache of
+ * pds_prefill_dense_stack is the PDS_KV_BF16 cache with n_seqs = 1.
+ *
+ * Formats:
+ *   PDS_KV_BF16  the values, bf16.
+ *   PDS_KV_E4M3  a byte per channel, 1-4-3 floating point (bias 7, largest
+ *                448); scale word: the float32 scale.  A row x of a head
+ *                is stored as scale = max|x| / 448, code = x / scale rounded to
+ *                nearest even; it stands for code * scale.
+ *   PDS_KV_INT4  two channels per byte (even channel in the low nibble);
+ *                scale word: bits 31..16 the scale in bf16, bits 3..0 the zero
+ *                point z, the rest 0.  lo = min(0, min x), hi = max(0, max x),
+ *                scale = hi/15 - lo/15, z = rint(-lo / scale) and code =
+ *                rint(x / scale) + z, both limited to 0..15; it stands for
+ *                (code - z) * scale.
+ * A row whose scale would be below the smallest normal float32 is stored as
+ * zeros (scale 0); a row with an infinity or a NaN has a NaN scale and
+ * stands for NaN throughout.  The scale words of sequence s, kv head g and
+ * row j sit at [(s n_kv_heads + g) capacity + j].
+ *
+ * lens[s] is the number of cached rows of sequence s before the call.  The
+ * calls never change it: the caller advances it (on the device) by the
+ * tokens it keeps.
+ */
+enum { PDS_KV_BF16 = 0, PDS_KV_E4M3 = 1, PDS_KV_INT4 = 2 };
+typedef struct pds_cache {
+  int32_t format;
+  int32_t n_seqs;     /* 1 .. 4096                                      */
+  int32_t capacity;   /* rows per sequence, >= 1                        */
+  int32_t n_kv_heads;
+  int32_t head_dim;   /* 64 or 128                                      */
+  int32_t reserved;   /* 0                                              */
+  int64_t seq_stride, row_stride, head_stride; /* elements; all 0: packed */
+  void* k;
+  void* v;
+  uint32_t* k_scale;  /* device [n_seqs, n_kv_heads, capacity]; unused  */
+  uint32_t* v_scale;  /*   (may be NULL) for PDS_KV_BF16                */
+  const int32_t* lens; /* device [n_seqs]                               */
+} pds_cache;
+
+/*
+ * Drafted tokens.  n_tokens tokens per sequence sit at rows lens[s] ..
+ * lens[s] + n_tokens - 1.  parents, device int32 [n_seqs, n_tokens], makes
+ * them a forest: parents[t] is the index of t's parent among the sequence's
+ * tokens (smaller than t), -1 for a root, below -1 for a padding token
+ * (whose row is not written, and whose output is zero).  parents NULL is the
+ * chain t -> t - 1: a decode step, or a run of tokens of the sequence.  A
+ * token's depth is the number of its ancestors and its position
+ * lens[s] + depth.  At most 256 tokens with parents.
+ */
+
+/*
+ * Store n_tokens new K and V rows of every sequence: bf16 input, token t of
+ * sequence s at element (s n_tokens + t) * k_stride (v_stride) of k (v),
+ * [n_kv_heads, head_dim] each (stride 0: packed; multiples of 8).  With spec
+ * not NULL the K rows are rotated first, at the tokens' positions or at
+ * positions[s n_tokens + t] (device) where given; the rotated values are
+ * quantised from float32 (PDS_KV_BF16: rounded to bf16).  Rows other than the
+ * new ones are left as they are.
+ */
+pds_status pds_cache_write(const pds_cache* cache, const pds_rope_spec* spec, const uint16_t* k,
+                           const uint16_t* v, int32_t n_tokens, int64_t k_stride,
+                           int64_t v_stride, const int32_t* parents, const int32_t* positions,
+                           void* stream);
+
+/*
+ * Rows back as bf16 (the value a row stands for, rounded once):
+ * k_out, v_out [n_seqs, rows, n_kv_heads, head_dim], either may be NULL.
+ * first_row >= 0: rows first_row .. first_row + rows - 1, those below
+ * lens[s]; the rest of the output is left as it is.  first_row ==
+ * PDS_AT_LENS: the rows lens[s] .. lens[s] + rows - 1 that a write of `rows`
+ * tokens stored.
+ */
+enum { PDS_AT_LENS = -1 };
+pds_status pds_cache_read(const pds_cache* cache, int32_t first_row, int32_t rows,
+                          uint16_t* k_out, uint16_t* v_out, void* stream);
+
+/*
+ * GQA attention of the n_tokens new tokens of every sequence (already
+ * written) over its cache: token t sees the lens[s] cached rows, its
+ * ancestors and itself; with window > 0 only those whose position (a cached
+ * row's is its index) is above its own less window.  Scores, softcap and the
+ * head groups as in pds_attention; the softmax's statistics are float32.
+ *  q, o     bf16, token t of sequence s at element (s n_tokens + t) * q_stride
+ *           (o_stride), [n_heads, head_dim] each (0: packed; multiples of 8).
+ *           o may not overlap q.
+ *  n_tokens 1 .. 256; n_heads a multiple of n_kv_heads.
+ *  max_len  an upper bound of lens known on the host, or 0 (the capacity less
+ *           n_tokens); sizes the launch, not the result's meaning.  A longer
+ *           sequence is refused as one that does not fit.
+ *  workspace  >= pds_attention_tree_workspace_bytes(...) bytes, so that key
+ *           ranges are split over all SMs, or NULL and 0 (every range on one
+ *           SM).  Its content on entry does not matter; calls that may run at
+ *           the same time need one each.  How ranges are split, and so the
+ *           rounding of the result, depends on whether there is one, on
+ *           max_len and on lens; the same call on the same inputs gives the
+ *           same bits.
+ * A row that sees no key (padding) is zero.  An infinity or a NaN in a row
+ * that a token does not see does not reach its output.
+ */
+pds_status pds_attention_tree(const pds_cache* cache, const uint16_t* q, uint16_t* o,
+                              int32_t n_tokens, int32_t n_heads, int64_t q_stride,
+                              int64_t o_stride, const int32_t* parents, float softcap,
+                              int32_t window, int32_t max_len, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of pds_attention_tree on the current device (0 for bad sizes or without one). */
+size_t pds_attention_tree_workspace_bytes(const pds_cache* cache, int32_t n_tokens,
+                                          int32_t n_heads);
 
 #ifdef __cplusplus
 }
