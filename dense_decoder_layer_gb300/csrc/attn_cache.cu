@@ -37,6 +37,7 @@
 #include "common.cuh"
 #include "fastmath.cuh"
 #include "kv.h"
+#include "sm100.cuh"
 #include "tc.h"
 
 namespace pds {
@@ -86,35 +87,47 @@ __device__ __forceinline__ int seq_steps(const Args& a, int s, int& first, int& 
   return (len + a.n_tokens + kStep - 1) / kStep - first;
 }
 
-__device__ __forceinline__ int warp_sum_int(int v) {
-  return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(v)));
+__device__ __forceinline__ unsigned warp_sum_uint(unsigned v) {
+  return __reduce_add_sync(0xffffffffu, v);
+}
+
+// One warp's view of the schedule: lane i holds sequence i's steps (the first
+// 32 sequences; further ones are read again, from L1, where they are needed).
+struct Lane {
+  int n, first, len;
+};
+__device__ __forceinline__ Lane lane_steps(const Args& a, int s) {
+  Lane l{0, 0, 0};
+  if (s < a.c.n_seqs) l.n = seq_steps(a, s, l.first, l.len);
+  return l;
 }
 
 // Steps per chunk (the same for every sequence), by one warp.
-__device__ int chunk_steps(const Args& a, int lane) {
+__device__ int chunk_steps(const Args& a, int lane, const Lane& mine) {
   if (a.slots == 0) return 1 << 30;
   const int per = a.c.n_kv_heads * a.row_tiles;
-  int first, len;
-  long long total = 0;
-  for (int s = lane; s < a.c.n_seqs; s += 32) total += seq_steps(a, s, first, len);
+  if (!a.fit) {
+    long long total = mine.n;
+    for (int s = lane + 32; s < a.c.n_seqs; s += 32) total += lane_steps(a, s).n;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  // at most slots + (sequences x per) units: every chunk but a sequence's last is whole
-  int c = max(a.min_steps, static_cast<int>((total * per + a.slots - 1) / a.slots));
-  if (!a.fit) return c;
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    // at most slots + (sequences x per) units: every chunk but a sequence's last is whole
+    return max(a.min_steps, static_cast<int>((total * per + a.slots - 1) / a.slots));
+  }
+  float total = static_cast<float>(mine.n);
+  for (int s = lane + 32; s < a.c.n_seqs; s += 32) total += static_cast<float>(lane_steps(a, s).n);
+  total = warp_sum(total);
+  int c = max(a.min_steps, static_cast<int>(__fdividef(total * per, static_cast<float>(a.slots))));
   // Sequences' last chunks are short: lengthen until the units fit the slots.
   // There are at most half as many (sequence, head, tile) as slots, so twice
-  // this length always fits: about 16 rounds of a sixteenth at the very most.
+  // this length always fits: some 16 rounds of a sixteenth at the very most.
+  const unsigned most = static_cast<unsigned>(a.slots / per);
   for (;;) {
-    int chunks = 0;
-    for (int s = lane; s < a.c.n_seqs; s += 32) {
-      const int n = seq_steps(a, s, first, len);
-      chunks += (n + c - 1) / c;
-    }
-    if (static_cast<long long>(warp_sum_int(chunks)) * per <= a.slots) break;
+    unsigned chunks = static_cast<unsigned>(mine.n + c - 1) / static_cast<unsigned>(c);
+    for (int s = lane + 32; s < a.c.n_seqs; s += 32) chunks += (lane_steps(a, s).n + c - 1) / c;
+    if (warp_sum_uint(chunks) <= most) return c;
     c += max(1, c >> 4);
   }
-  return c;
 }
 
 struct Unit {
@@ -124,13 +137,12 @@ struct Unit {
 
 // The sequence and chunk of the w-th chunk overall (w < 0: of sequence `seq`,
 // whole range).  False past the last one.  By one warp; every lane returns it.
-__device__ bool find_unit(const Args& a, int c, int w, int seq, int lane, Unit& u) {
+__device__ bool find_unit(const Args& a, int c, int w, int seq, int lane, const Lane& mine,
+                          Unit& u) {
   int base = 0;
   for (int s0 = 0; s0 < a.c.n_seqs; s0 += 32) {
-    const int s = s0 + lane;
-    int first = 0, len = 0, n = 0;
-    if (s < a.c.n_seqs) n = seq_steps(a, s, first, len);
-    const int chunks = n == 0 ? 0 : (n - 1) / c + 1;
+    const Lane l = s0 == 0 ? mine : lane_steps(a, s0 + lane);
+    const int chunks = l.n == 0 ? 0 : (l.n - 1) / c + 1;
     int incl = chunks;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -138,15 +150,15 @@ __device__ bool find_unit(const Args& a, int c, int w, int seq, int lane, Unit& 
       if (lane >= o) incl += t;
     }
     const int excl = base + incl - chunks;
-    const bool mine = w >= 0 ? (w >= excl && w < base + incl) : s == seq;
-    const unsigned hit = __ballot_sync(0xffffffffu, mine);
+    const bool here = w >= 0 ? (w >= excl && w < base + incl) : s0 + lane == seq;
+    const unsigned hit = __ballot_sync(0xffffffffu, here);
     if (hit) {
       const int src = __ffs(hit) - 1;
       u.seq = s0 + src;
       u.n_chunks = __shfl_sync(0xffffffffu, chunks, src);
       u.base = __shfl_sync(0xffffffffu, excl, src);
-      u.len = __shfl_sync(0xffffffffu, len, src);
-      const int f = __shfl_sync(0xffffffffu, first, src), m = __shfl_sync(0xffffffffu, n, src);
+      u.len = __shfl_sync(0xffffffffu, l.len, src);
+      const int f = __shfl_sync(0xffffffffu, l.first, src), m = __shfl_sync(0xffffffffu, l.n, src);
       u.chunk = w >= 0 ? w - u.base : 0;
       u.first = f + u.chunk * c;
       u.n_steps = min(c, m - u.chunk * c);
@@ -469,18 +481,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
   const int per = a.c.n_kv_heads * a.row_tiles;
   const int w = blockIdx.x / per, p = blockIdx.x - w * per;
   const int head = p % a.c.n_kv_heads, tile = p / a.c.n_kv_heads;
+  sm100::grid_dep_wait();  // everything below reads what earlier kernels wrote
+  sm100::grid_dep_launch();
   if (warp == 0) {
     Unit u{};
-    const int c = chunk_steps(a, lane);
-    const bool ok = find_unit(a, c, w, 0, lane, u);
+    const Lane mine = lane_steps(a, lane);
+    const int c = chunk_steps(a, lane, mine);
+    const bool ok = find_unit(a, c, w, 0, lane, mine, u);
     if (lane == 0) {
       *shared_unit = u;
       *shared_ok = ok;
     }
     if (blockIdx.x == 0) {  // report lengths that do not fit
       bool bad = false;
-      int first, len;
-      for (int s = lane; s < a.c.n_seqs; s += 32) bad |= seq_steps(a, s, first, len) == 0;
+      for (int s = lane; s < a.c.n_seqs; s += 32) bad |= lane_steps(a, s).n == 0;
       if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kStatusBadLength);
     }
   }
@@ -823,50 +837,80 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
   }
 }
 
-// One warp per (sequence, token, head): the row's chunks joined in order.
+// One warp per (sequence, token, head): the row's chunks joined in order.  Its
+// schedule is made while the chunks are still being computed (lens were
+// complete before those began), its loads after.
 template <int HD>
 __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ Args a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + warp;
   const int per_seq = a.n_tokens * a.n_heads;
   const int64_t seq64 = row / per_seq;
-  if (seq64 >= a.c.n_seqs) return;
-  const int seq = static_cast<int>(seq64), rest = static_cast<int>(row - seq64 * per_seq);
+  Unit u{};
+  if (seq64 < a.c.n_seqs) {
+    const Lane mine = lane_steps(a, lane);
+    find_unit(a, chunk_steps(a, lane, mine), -1, static_cast<int>(seq64), lane, mine, u);
+  }
+  sm100::grid_dep_wait();
+  sm100::grid_dep_launch();
+  if (u.n_chunks <= 1) return;  // written by its block, or refused, or no such row
+  const int seq = u.seq, rest = static_cast<int>(row - seq64 * per_seq);
   const int t = rest / a.n_heads, h = rest - t * a.n_heads;
-  Unit u;
-  const int c = chunk_steps(a, lane);
-  find_unit(a, c, -1, seq, lane, u);
-  if (u.n_chunks <= 1) return;  // written by its block, or refused
   const int head = h / a.group, r = t * a.group + h - head * a.group;
   const int tile = r / a.tile_rows;
   const int per = a.c.n_kv_heads * a.row_tiles;
   const int64_t first = (static_cast<int64_t>(u.base) * per + tile * a.c.n_kv_heads + head) *
                             a.tile_rows + (r - tile * a.tile_rows);
   const int64_t stride = static_cast<int64_t>(per) * a.tile_rows;
-  float m = -INFINITY;
-  for (int x = lane; x < u.n_chunks; x += 32) m = fmaxf(m, a.ml_part[first + x * stride].x);
-  m = warp_max(m);
-  const float mu = m == -INFINITY ? 0.f : m;
   constexpr int kPer = HD / 32;
+  constexpr int kBatch = 8;  // chunks whose loads are in flight together
   float acc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-  float sum = 0.f;
-#pragma unroll 4
-  for (int x = 0; x < u.n_chunks; ++x) {
-    const int64_t slot = first + x * stride;
-    const float2 v = a.ml_part[slot];
-    const float f = exp2f(v.x - mu);
-    sum += v.y * f;
-    const float* src = a.o_part + slot * HD + lane * kPer;
+  float sum = 0.f, m = -INFINITY;
+  for (int x0 = 0; x0 < u.n_chunks; x0 += kBatch) {
+    float2 v[kBatch];
+    float y[kBatch][kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] += src[i] * f;
+    for (int x = 0; x < kBatch; ++x) {
+      const bool live = x0 + x < u.n_chunks;
+      const int64_t slot = first + (live ? x0 + x : x0) * stride;
+      v[x] = __ldcg(a.ml_part + slot);
+      if (!live) v[x] = make_float2(-INFINITY, 0.f);
+      const float* src = a.o_part + slot * HD + lane * kPer;
+      if constexpr (kPer == 4) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+        y[x][0] = f.x, y[x][1] = f.y, y[x][2] = f.z, y[x][3] = f.w;
+      } else {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+        y[x][0] = f.x, y[x][1] = f.y;
+      }
+    }
+    float m_new = m;
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) m_new = fmaxf(m_new, v[x].x);
+    const float mu = m_new == -INFINITY ? 0.f : m_new;
+    const float old = exp2f(m - mu);
+    m = m_new;
+    sum *= old;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] *= old;
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      if (x0 + x >= u.n_chunks) break;
+      const float f = exp2f(v[x].x - mu);
+      sum += v[x].y * f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] += y[x][i] * f;
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
   uint16_t* dst = a.o + (static_cast<int64_t>(seq) * a.n_tokens + t) * a.o_stride + h * HD + lane * kPer;
-#pragma unroll
-  for (int i = 0; i < kPer; i += 2)
-    *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
 }
 
 // ------------------------------------------------------------------ launch
@@ -908,8 +952,8 @@ cudaError_t launch(const Args& a, int64_t grid, cudaStream_t st) {
   const cudaError_t ce = kernel_smem_attr(
       reinterpret_cast<const void*>(cache_attn_kernel<FMT, HD, NT, VAR>), C::kSmem);
   if (ce != cudaSuccess) return ce;
-  cache_attn_kernel<FMT, HD, NT, VAR><<<static_cast<unsigned>(grid), kThreads, C::kSmem, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(cache_attn_kernel<FMT, HD, NT, VAR>, dim3(static_cast<unsigned>(grid)),
+                      kThreads, C::kSmem, st, a);
 }
 
 template <int FMT, int HD>
@@ -981,12 +1025,9 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
                                      : launch_format<64>(a, t.format, s.nt, grid, st);
   if (ce == cudaSuccess && a.slots > 0) {
     const int64_t rows = static_cast<int64_t>(c.n_seqs) * t.n_tokens * t.n_heads;
-    const unsigned blocks = static_cast<unsigned>((rows + 7) / 8);
-    if (t.head_dim == 128)
-      cache_join_kernel<128><<<blocks, 256, 0, st>>>(a);
-    else
-      cache_join_kernel<64><<<blocks, 256, 0, st>>>(a);
-    ce = cudaGetLastError();
+    const dim3 blocks(static_cast<unsigned>((rows + 7) / 8));
+    ce = t.head_dim == 128 ? launch_after(cache_join_kernel<128>, blocks, 256, 0, st, a)
+                           : launch_after(cache_join_kernel<64>, blocks, 256, 0, st, a);
   }
   if (ce != cudaSuccess) {
     *err = std::string("cache attention launch: ") + cudaGetErrorString(ce);

@@ -54,6 +54,27 @@ struct TreeAttnCall {
   int num_sms;
 };
 
+// Launch with programmatic stream serialization: the kernel may begin while
+// the one before it ends, so it waits (griddepcontrol.wait) before it touches
+// memory.  Every kernel of the decoding path does and lets its successor begin
+// early in turn: a decode step is a row of kernels of a few microseconds, of
+// which a launch that waits for the end of its predecessor is a large part.
+template <typename... Params, typename... Given>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                         cudaStream_t st, Given&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 cudaError_t launch_rope(const RopeTurns& r, const uint16_t* x, uint16_t* y, int rows, int heads,
                         int hd, int64_t x_stride, int64_t y_stride, const int32_t* positions,
                         int start_pos, cudaStream_t st);

@@ -18,6 +18,7 @@
 
 #include "common.cuh"
 #include "kv.h"
+#include "sm100.cuh"
 
 namespace pds {
 namespace {
@@ -101,6 +102,8 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const uint16_t* x, ui
   __shared__ float2 table[kMaxTurnPairs];
   const int row = blockIdx.x;
   const int per_head = hd >> 4, units = heads * per_head;
+  sm100::grid_dep_wait();
+  sm100::grid_dep_launch();
   const int64_t pos = positions ? static_cast<int64_t>(positions[row])
                                 : static_cast<int64_t>(start_pos) + row;
   const uint16_t* xr = x + row * x_stride;
@@ -166,6 +169,8 @@ __global__ void __launch_bounds__(kRowThreads)
   __shared__ int32_t par[kMaxDraftTokens];
   const int row = blockIdx.x;
   const int s = row / n_tokens, t = row - s * n_tokens;
+  sm100::grid_dep_wait();
+  sm100::grid_dep_launch();
   const int half_units = c.n_kv_heads * kPerHead, units = 2 * half_units;
   int u = threadIdx.x;
   uint4 wa = {}, wb = {};
@@ -298,6 +303,8 @@ __global__ void __launch_bounds__(kRowThreads)
   const char* src = (is_v ? c.v : c.k) + s * c.seq_stride;
   const uint32_t* scales = (is_v ? c.v_scale : c.k_scale);
   uint16_t* out = is_v ? v_out : k_out;
+  sm100::grid_dep_wait();
+  sm100::grid_dep_launch();
   const int len = c.lens[s];
   const bool at_lens = first_row < 0;
   if (len < 0 || len > c.capacity || (at_lens && len > c.capacity - rows)) {
@@ -381,9 +388,8 @@ cudaError_t launch_rope(const RopeTurns& r, const uint16_t* x, uint16_t* y, int 
   const int threads = round_threads(units);
   // few rows: the row's units are spread over several blocks
   const int slices = rows >= 256 ? 1 : (units + threads - 1) / threads;
-  rope_kernel<<<dim3(rows, std::min(slices, 65535)), threads, 0, st>>>(
-      x, y, heads, hd, x_stride, y_stride, positions, start_pos, r);
-  return cudaGetLastError();
+  return launch_after(rope_kernel, dim3(rows, std::min(slices, 65535)), threads, 0, st, x, y, heads,
+                      hd, x_stride, y_stride, positions, start_pos, r);
 }
 
 cudaError_t launch_cache_write(const CacheView& c, int format, int hd, const RopeTurns& r,
@@ -392,9 +398,8 @@ cudaError_t launch_cache_write(const CacheView& c, int format, int hd, const Rop
                                const int32_t* positions, uint32_t* status, cudaStream_t st) {
   const int units = 2 * c.n_kv_heads * (hd / 16);
   return by_format(format, hd, [&](auto fmt, auto w) {
-    cache_write_kernel<fmt, w><<<c.n_seqs * n_tokens, round_threads(units), 0, st>>>(
-        c, r, k, v, n_tokens, k_stride, v_stride, parents, positions, status);
-    return cudaGetLastError();
+    return launch_after(cache_write_kernel<fmt, w>, dim3(c.n_seqs * n_tokens), round_threads(units),
+                        0, st, c, r, k, v, n_tokens, k_stride, v_stride, parents, positions, status);
   });
 }
 
@@ -403,9 +408,8 @@ cudaError_t launch_cache_read(const CacheView& c, int format, int hd, int first_
                               cudaStream_t st) {
   const dim3 grid((rows + kReadRows - 1) / kReadRows, c.n_seqs, k_out && v_out ? 2 : 1);
   return by_format(format, hd, [&](auto fmt, auto w) {
-    cache_read_kernel<fmt, w><<<grid, kRowThreads, 0, st>>>(c, first_row, rows, k_out, v_out,
-                                                            status);
-    return cudaGetLastError();
+    return launch_after(cache_read_kernel<fmt, w>, grid, kRowThreads, 0, st, c, first_row, rows,
+                        k_out, v_out, status);
   });
 }
 

@@ -30,9 +30,12 @@ SCALINGS = {"none": pds.PDS_ROPE_UNSCALED, "linear": pds.PDS_ROPE_LINEAR,
             "yarn": pds.PDS_ROPE_YARN}
 
 
-def _stream(stream, device):
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream
+# A decode step's call is a few microseconds of GPU work, so the wrappers keep
+# to a few cheap attribute reads: device and stream by index, the shape
+# compared as a whole, strides looked at only for tensors that are not packed.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_BF16, _I32 = torch.bfloat16, torch.int32
 
 
 def _need(ok, what):
@@ -40,19 +43,21 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _rows(t, lead, tail, what):
-    """Element stride between consecutive rows of a bf16 tensor [*lead, *tail]
-    whose rows are contiguous and evenly spaced."""
-    _need(t.dtype == torch.bfloat16 and t.is_cuda, f"{what}: a bf16 CUDA tensor")
-    _need(t.shape == (*lead, *tail), f"{what}: shape {tuple(t.shape)}, not {(*lead, *tail)}")
+def _rows(t, shape, n_lead, device, what):
+    """Element stride (0: packed) between consecutive rows of a bf16 tensor of `shape`: its
+    first `n_lead` sizes count rows, which are contiguous and evenly spaced."""
+    if t.dtype != _BF16 or t.get_device() != device or t.shape != shape:
+        raise ValueError(f"{what}: a bf16 tensor {tuple(shape)} on cuda:{device}, not {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
     if t.is_contiguous():
         return 0
+    strides = t.stride()
     width = 1
-    for size, stride in zip(reversed(tail), reversed(t.stride()[len(lead):])):
+    for size, stride in zip(reversed(shape[n_lead:]), reversed(strides[n_lead:])):
         _need(size == 1 or stride == width, f"{what}: a row's heads and channels must be contiguous")
         width *= size
     step, count = None, 1
-    for size, stride in zip(reversed(lead), reversed(t.stride()[:len(lead)])):
+    for size, stride in zip(reversed(shape[:n_lead]), reversed(strides[:n_lead])):
         if size > 1:
             step = stride // count if step is None else step
             _need(stride == step * count, f"{what}: rows must be evenly spaced")
@@ -60,12 +65,23 @@ def _rows(t, lead, tail, what):
     return width if step is None else step
 
 
-def _index(t, shape, device, what):
+def _index(t, rows, device, what):
     if t is None:
         return None
-    _need(t.dtype == torch.int32 and t.device == device and t.is_contiguous() and
-          tuple(t.shape) == tuple(shape), f"{what}: a contiguous int32 tensor {tuple(shape)} on {device}")
+    if t.dtype != _I32 or t.get_device() != device or t.numel() != rows or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous int32 tensor of {rows} values on cuda:{device}")
     return t.data_ptr()
+
+
+def _call(fn, device, stream, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    if _current_device() == device:
+        st = fn(*args, _raw_stream(device) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _raw_stream(device) if stream is None else stream.cuda_stream)
+    if st:
+        pds.check(st)
 
 
 class RopeSpec:
@@ -90,22 +106,20 @@ class RopeSpec:
 def rope(x, spec, positions=None, start_pos=0, out=None, inverse=False, stream=None):
     """The rows of ``x`` [..., heads, head_dim] (bf16) turned at ``positions`` (int32, one per
     row) or ``start_pos + row``; ``out`` may be ``x``.  ``inverse`` turns back (the gradient)."""
-    lead, (heads, hd) = x.shape[:-2], x.shape[-2:]
-    _need(hd == spec.head_dim, f"x: heads of {hd} channels, the spec's have {spec.head_dim}")
+    shape = x.shape
+    heads, hd = shape[-2], shape[-1]
+    if hd != spec.head_dim:
+        raise ValueError(f"x: heads of {hd} channels, the spec's have {spec.head_dim}")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _need(out.device == x.device, "out: on the device of x")
-    xs, ys = _rows(x, lead, (heads, hd), "x"), _rows(out, lead, (heads, hd), "out")
-    rows = 1
-    for n in lead:
-        rows *= n
-    if positions is not None:
-        positions = positions.reshape(-1)
-    if rows and heads:
-        with torch.cuda.device(x.device):
-            pds.pds_rope(spec.c, x.data_ptr(), out.data_ptr(), rows, heads, hd,
-                         _stream(stream, x.device), xs, ys,
-                         _index(positions, (rows,), x.device, "positions"), start_pos, inverse)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    device, lead = x.get_device(), len(shape) - 2
+    xs = _rows(x, shape, lead, device, "x")
+    ys = xs if out is x else _rows(out, shape, lead, device, "out")
+    n = x.numel()
+    if n:
+        rows = n // (heads * hd)
+        _call(pds.load().pds_rope, device, stream, spec.c, x.data_ptr(), out.data_ptr(), rows,
+              heads, hd, xs, ys, _index(positions, rows, device, "positions"), start_pos, inverse)
     return out
 
 
@@ -128,6 +142,7 @@ class KvCache:
         self.device = torch.device(device) if k is None else k.device
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self.index = self.device.index
         dtype, self.per_byte = {"bf16": (torch.bfloat16, 1), "e4m3": (torch.float8_e4m3fn, 1),
                                 "int4": (torch.uint8, 2)}[fmt]
         shape = (self.n_seqs, self.capacity, self.n_kv_heads, self.head_dim // self.per_byte)
@@ -143,19 +158,30 @@ class KvCache:
             return t
 
         self.k, self.v = have(k, shape, dtype, "k", False), have(v, shape, dtype, "v", False)
-        _need(self.k.stride() == self.v.stride(), "k and v: the same strides")
+        packed = self.k.is_contiguous() and self.v.is_contiguous()
+        _need(packed or self.k.stride() == self.v.stride(), "k and v: the same strides")
         self.k_scale = self.v_scale = None
         if word is not None:
             self.k_scale = have(k_scale, words, word, "k_scale", True)
             self.v_scale = have(v_scale, words, word, "v_scale", True)
-        self.lens = have(lens, (self.n_seqs,), torch.int32, "lens", True)
-        seq, row, head, _ = (0, 0, 0, 0) if self.k.is_contiguous() else self.k.stride()
+        self._lens = have(lens, (self.n_seqs,), torch.int32, "lens", True)
+        seq, row, head, _ = (0, 0, 0, 0) if packed else self.k.stride()
         self.c = pds.pds_cache(
             FORMATS[fmt], self.n_seqs, self.capacity, self.n_kv_heads, self.head_dim, 0,
             seq * self.per_byte, row * self.per_byte, head * self.per_byte, self.k.data_ptr(),
             self.v.data_ptr(), self.k_scale.data_ptr() if word is not None else None,
-            self.v_scale.data_ptr() if word is not None else None, self.lens.data_ptr())
+            self.v_scale.data_ptr() if word is not None else None, self._lens.data_ptr())
         self._ws = {}  # attention workspace by (tokens, heads)
+
+    @property
+    def lens(self):
+        """Cached rows of each sequence (int32, on the device); assigning copies into it."""
+        return self._lens
+
+    @lens.setter
+    def lens(self, value):
+        if value is not self._lens:
+            self._lens.copy_(value)
 
     def workspace(self, n_tokens, n_heads):
         """The attention's workspace for this many tokens and heads, made on first use and
@@ -171,32 +197,29 @@ class KvCache:
     def write(self, k, v, rope=None, parents=None, positions=None, stream=None):
         """Store new rows [n_seqs, n_tokens, n_kv_heads, head_dim] (bf16) behind the cached
         ones, K rotated by ``rope`` (a :class:`RopeSpec`) at the tokens' positions."""
-        tail = (self.n_kv_heads, self.head_dim)
-        t = k.shape[1]
-        ks, vs = _rows(k, (self.n_seqs, t), tail, "k"), _rows(v, (self.n_seqs, t), tail, "v")
-        _need(k.device == self.device and v.device == self.device, "k, v: on the cache's device")
-        _need(rope is None or rope.head_dim == self.head_dim, "rope: for this head_dim")
-        with torch.cuda.device(self.device):
-            pds.pds_cache_write(self.c, None if rope is None else rope.c, k.data_ptr(),
-                                v.data_ptr(), t, _stream(stream, self.device), ks, vs,
-                                _index(parents, (self.n_seqs, t), self.device, "parents"),
-                                _index(positions, (self.n_seqs, t), self.device, "positions"))
+        t, device = k.shape[1], self.index
+        shape = (self.n_seqs, t, self.n_kv_heads, self.head_dim)
+        ks, vs = _rows(k, shape, 2, device, "k"), _rows(v, shape, 2, device, "v")
+        if rope is not None and rope.head_dim != self.head_dim:
+            raise ValueError(f"rope: heads of {rope.head_dim} channels, the cache's have {self.head_dim}")
+        rows = self.n_seqs * t
+        _call(pds.load().pds_cache_write, device, stream, self.c, None if rope is None else rope.c,
+              k.data_ptr(), v.data_ptr(), t, ks, vs, _index(parents, rows, device, "parents"),
+              _index(positions, rows, device, "positions"))
 
     def read(self, first_row, rows, k_out=None, v_out=None, stream=None):
         """(K, V) rows ``first_row ...`` as bf16 [n_seqs, rows, n_kv_heads, head_dim]; rows that
         a sequence does not have are left as they are (zero in a new tensor)."""
         shape = (self.n_seqs, rows, self.n_kv_heads, self.head_dim)
-        out = []
-        for t in (k_out, v_out):
-            if t is None:
-                t = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
-            _need(t.dtype == torch.bfloat16 and tuple(t.shape) == shape and t.is_contiguous() and
-                  t.device == self.device, f"output: contiguous bf16 {shape} on {self.device}")
-            out.append(t)
-        with torch.cuda.device(self.device):
-            pds.pds_cache_read(self.c, first_row, rows, out[0].data_ptr(), out[1].data_ptr(),
-                               _stream(stream, self.device))
-        return tuple(out)
+        if k_out is None:
+            k_out = torch.zeros(shape, dtype=_BF16, device=self.device)
+        if v_out is None:
+            v_out = torch.zeros(shape, dtype=_BF16, device=self.device)
+        if _rows(k_out, shape, 0, self.index, "k_out") or _rows(v_out, shape, 0, self.index, "v_out"):
+            raise ValueError("k_out, v_out: contiguous tensors")
+        _call(pds.load().pds_cache_read, self.index, stream, self.c, first_row, rows,
+              k_out.data_ptr(), v_out.data_ptr())
+        return k_out, v_out
 
     def read_new(self, rows, k_out=None, v_out=None, stream=None):
         """(K, V) of the ``rows`` tokens that the last write stored."""
@@ -207,26 +230,23 @@ class KvCache:
         """Attention of the written tokens' queries ``q`` [n_seqs, n_tokens, heads, head_dim]
         (bf16, rotated) over the cache and each other; ``parents`` int32 [n_seqs, n_tokens]
         makes them a tree, without it they are a chain."""
-        t, heads = q.shape[1], q.shape[2]
+        _, t, heads, _ = shape = q.shape
+        device = self.index
+        if shape[0] != self.n_seqs or shape[3] != self.head_dim:
+            raise ValueError(f"q: [{self.n_seqs}, tokens, heads, {self.head_dim}], not {tuple(shape)}")
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _need(q.device == self.device and out.device == self.device, "q, out: on the cache's device")
-        lead, tail = (self.n_seqs, t), (heads, self.head_dim)
-        qs, os_ = _rows(q, lead, tail, "q"), _rows(out, lead, tail, "out")
+            out = torch.empty(shape, dtype=_BF16, device=self.device)
+        qs, os_ = _rows(q, shape, 2, device, "q"), _rows(out, shape, 2, device, "out")
         if workspace is None:
-            workspace = self.workspace(t, heads)
-        with torch.cuda.device(self.device):
-            pds.pds_attention_tree(self.c, q.data_ptr(), out.data_ptr(), t, heads,
-                                   _stream(stream, self.device), qs, os_,
-                                   _index(parents, (self.n_seqs, t), self.device, "parents"),
-                                   softcap, window, max_len, workspace.data_ptr(),
-                                   workspace.numel())
+            workspace = self._ws.get((t, heads))
+            if workspace is None:
+                workspace = self.workspace(t, heads)
+        _call(pds.load().pds_attention_tree, device, stream, self.c, q.data_ptr(), out.data_ptr(),
+              t, heads, qs, os_, _index(parents, self.n_seqs * t, device, "parents"), softcap,
+              window, max_len, workspace.data_ptr(), workspace.numel())
         return out
 
     def sync(self, stream=None):
         """Wait for the stream; raises PdsError where a call met a length or a parent that it
         could not serve."""
-        with torch.cuda.device(self.device):
-            st = pds.pds_component_sync(_stream(stream, self.device))
-        if st != pds.PDS_OK:
-            raise pds.PdsError(st, pds.last_error())
+        _call(pds.load().pds_component_sync, self.index, stream)

@@ -135,7 +135,10 @@ def test_row_strides_of_views():
 
     class Cuda:  # a tensor's shape and strides, seen as a device tensor
         def __init__(self, t):
-            self.t, self.dtype, self.is_cuda, self.shape = t, t.dtype, True, t.shape
+            self.t, self.dtype, self.device, self.shape = t, t.dtype, t.device, t.shape
+
+        def get_device(self):
+            return 0
 
         def stride(self, *a):
             return self.t.stride(*a)
@@ -143,16 +146,20 @@ def test_row_strides_of_views():
         def is_contiguous(self):
             return self.t.is_contiguous()
 
+    def rows(t, lead=2):
+        return kv._rows(Cuda(t), t.shape, lead, 0, "x")
     fused = torch.empty(2, 3, 512, dtype=torch.bfloat16)
     part = fused[..., 128:384].unflatten(-1, (4, 64))
-    assert kv._rows(Cuda(part), (2, 3), (4, 64), "x") == 512
-    assert kv._rows(Cuda(part.contiguous()), (2, 3), (4, 64), "x") == 0
-    assert kv._rows(Cuda(part[:, :1]), (2, 1), (4, 64), "x") == 1536
-    for bad in (part.transpose(0, 1), part[..., ::2]):
+    assert rows(part) == 512
+    assert rows(part.contiguous()) == 0
+    assert rows(part[:, :1]) == 1536
+    for bad in (part.transpose(0, 1), part[..., ::2], part.float()):
         with pytest.raises(ValueError):
-            kv._rows(Cuda(bad), tuple(bad.shape[:2]), tuple(bad.shape[2:]), "x")
+            rows(bad)
     with pytest.raises(ValueError):
-        kv._rows(Cuda(part.float()), (2, 3), (4, 64), "x")
+        kv._rows(Cuda(part), (2, 3, 4, 63), 2, 0, "x")
+    with pytest.raises(ValueError):
+        kv._rows(Cuda(part), part.shape, 2, 1, "x")
 
 
 # ------------------------------------------------------------- the oracle
