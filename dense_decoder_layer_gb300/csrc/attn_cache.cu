@@ -34,8 +34,8 @@
 #include <algorithm>
 #include <string>
 
+#include "attn_cache.cuh"
 #include "common.cuh"
-#include "fastmath.cuh"
 #include "kv.h"
 #include "sm100.cuh"
 #include "tc.h"
@@ -43,170 +43,16 @@
 namespace pds {
 namespace {
 
+using namespace cacheattn;
+
 constexpr int kStep = 16;        // keys of a warp's step
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kMoveLog2 = 8.0f;  // the reference maximum follows beyond a growth of 2^8
 constexpr int kMaxTiles = 4;     // column tiles of 8 query rows per block
-constexpr int kMaskWords = kMaxDraftTokens / 32;
-
-struct Args {
-  CacheView c;
-  const uint16_t* q;
-  uint16_t* o;
-  int64_t q_stride, o_stride;
-  const int32_t* parents;
-  int n_tokens, n_heads, group;  // group: query heads per kv head
-  int max_len;
-  float scale_log2;              // log2(e) / sqrt(hd)
-  float cap;                     // softcap in units of q.k (0: none)
-  int window;
-  int row_tiles;                 // blocks of query rows per (sequence, kv head)
-  int tile_rows;                 // rows of one
-  int slots;                     // blocks to spread the chunks over; 0: one chunk each
-  int fit;                       // 1: choose chunks so that all units run at once
-  int min_steps;                 // shortest chunk, in steps
-  float* o_part;                 // [unit][tile_rows][hd]
-  float2* ml_part;               // [unit][tile_rows]: (maximum, sum)
-  uint32_t* status;
-};
-
-// --------------------------------------------------------------- schedule
-//
-// Units: (chunk of a sequence) x (kv head, row tile), the latter fastest, so
-// that blocks running together read neighbouring heads of the same rows.
-
-// Steps of sequence s: [first, first + n) in units of kStep keys; n = 0 for a
-// length that does not fit.
-__device__ __forceinline__ int seq_steps(const Args& a, int s, int& first, int& len) {
-  len = a.c.lens[s];
-  first = 0;
-  if (len < 0 || len > a.max_len) return 0;
-  // the first row any token can see: a root's, at position len
-  if (a.window > 0 && len - a.window + 1 > 0) first = (len - a.window + 1) / kStep;
-  return (len + a.n_tokens + kStep - 1) / kStep - first;
-}
-
-__device__ __forceinline__ unsigned warp_sum_uint(unsigned v) {
-  return __reduce_add_sync(0xffffffffu, v);
-}
-
-// One warp's view of the schedule: lane i holds sequence i's steps (the first
-// 32 sequences; further ones are read again, from L1, where they are needed).
-struct Lane {
-  int n, first, len;
-};
-__device__ __forceinline__ Lane lane_steps(const Args& a, int s) {
-  Lane l{0, 0, 0};
-  if (s < a.c.n_seqs) l.n = seq_steps(a, s, l.first, l.len);
-  return l;
-}
-
-// Steps per chunk (the same for every sequence), by one warp.
-__device__ int chunk_steps(const Args& a, int lane, const Lane& mine) {
-  if (a.slots == 0) return 1 << 30;
-  const int per = a.c.n_kv_heads * a.row_tiles;
-  if (!a.fit) {
-    long long total = mine.n;
-    for (int s = lane + 32; s < a.c.n_seqs; s += 32) total += lane_steps(a, s).n;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    // at most slots + (sequences x per) units: every chunk but a sequence's last is whole
-    return max(a.min_steps, static_cast<int>((total * per + a.slots - 1) / a.slots));
-  }
-  float total = static_cast<float>(mine.n);
-  for (int s = lane + 32; s < a.c.n_seqs; s += 32) total += static_cast<float>(lane_steps(a, s).n);
-  total = warp_sum(total);
-  int c = max(a.min_steps, static_cast<int>(__fdividef(total * per, static_cast<float>(a.slots))));
-  // Sequences' last chunks are short: lengthen until the units fit the slots.
-  // There are at most half as many (sequence, head, tile) as slots, so twice
-  // this length always fits: some 16 rounds of a sixteenth at the very most.
-  const unsigned most = static_cast<unsigned>(a.slots / per);
-  for (;;) {
-    unsigned chunks = static_cast<unsigned>(mine.n + c - 1) / static_cast<unsigned>(c);
-    for (int s = lane + 32; s < a.c.n_seqs; s += 32) chunks += (lane_steps(a, s).n + c - 1) / c;
-    if (warp_sum_uint(chunks) <= most) return c;
-    c += max(1, c >> 4);
-  }
-}
-
-struct Unit {
-  int seq, chunk, n_chunks, first, n_steps, len;  // steps [first, first + n_steps)
-  int base;  // (chunk 0 of the sequence) among all chunks
-};
-
-// The sequence and chunk of the w-th chunk overall (w < 0: of sequence `seq`,
-// whole range).  False past the last one.  By one warp; every lane returns it.
-__device__ bool find_unit(const Args& a, int c, int w, int seq, int lane, const Lane& mine,
-                          Unit& u) {
-  int base = 0;
-  for (int s0 = 0; s0 < a.c.n_seqs; s0 += 32) {
-    const Lane l = s0 == 0 ? mine : lane_steps(a, s0 + lane);
-    const int chunks = l.n == 0 ? 0 : (l.n - 1) / c + 1;
-    int incl = chunks;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    const int excl = base + incl - chunks;
-    const bool here = w >= 0 ? (w >= excl && w < base + incl) : s0 + lane == seq;
-    const unsigned hit = __ballot_sync(0xffffffffu, here);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      u.seq = s0 + src;
-      u.n_chunks = __shfl_sync(0xffffffffu, chunks, src);
-      u.base = __shfl_sync(0xffffffffu, excl, src);
-      u.len = __shfl_sync(0xffffffffu, l.len, src);
-      const int f = __shfl_sync(0xffffffffu, l.first, src), m = __shfl_sync(0xffffffffu, l.n, src);
-      u.chunk = w >= 0 ? w - u.base : 0;
-      u.first = f + u.chunk * c;
-      u.n_steps = min(c, m - u.chunk * c);
-      return true;
-    }
-    base = __shfl_sync(0xffffffffu, base + incl, 31);
-  }
-  return false;
-}
 
 // ------------------------------------------------------------ instructions
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-// 16 bytes (or zeros, when !live) into shared memory, not through L1.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(live ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-               "r"(live ? 4 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
 // Four 8x8 blocks of 16-bit values, transposed: lane l gives the address of
 // row l % 8 of block l / 8.
 __device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
@@ -227,36 +73,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Two e4m3 codes, each in the high byte of a 16-bit half (what the other
-// byte holds does not matter), as a pair of bf16: the exponent and mantissa
-// bits move down by four, and 2^120 turns the bias of 7 into one of 127.
-// Exact for every code, subnormal ones included.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t r) {
-  const uint32_t bits = ((r >> 4) & 0x07f007f0u) | (r & 0x80008000u);
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(bits), "r"(0x7b807b80u));
-  return d;
-}
-// Two 4-bit codes (in the low nibbles of 16-bit halves) less their zero
-// points, as bf16: 128 + code and 128 + zero point (z: as 0x4300 | zero point
-// in each half) are bf16 numbers, their difference is exact.
-__device__ __forceinline__ uint32_t int4_pair(uint32_t r, uint32_t z) {
-  const uint32_t bits = (r & 0x000f000fu) | 0x43004300u;
-  uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(bits), "r"(z));
-  return d;
-}
-
-__device__ __forceinline__ bool not_finite2(uint32_t w) {  // either bf16 of a pair
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-
 // ------------------------------------------------------------ the formats
 
 // Bytes of a head's row, and of one step's K (or V) slice.
@@ -916,13 +732,19 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
 // ------------------------------------------------------------------ launch
 
 int column_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : kMaxTiles; }
-
 int blocks_per_sm(int format, int hd, int nt) {  // Cfg::kBlocks
   return nt == kMaxTiles || (format == PDS_KV_BF16 && hd == 128) ? 1 : 2;
 }
 
+// More query rows per kv head than this go to the tensor-core kernel.
+constexpr int kTileMinRows = 33;
+
 struct Shape {
-  int nt, row_tiles, per, slots, fit;
+  bool tiles;            // the tensor-core kernel
+  int nt;                // the warp kernel's column tiles
+  int step, tile_rows;   // keys of a step, query rows of a block
+  int row_tiles, per;    // blocks of rows per kv head, and per sequence
+  int slots, fit;
 };
 
 // How a call's rows are tiled and over how many blocks its keys are spread.
@@ -930,11 +752,14 @@ Shape make_shape(int format, int hd, int n_seqs, int n_tokens, int n_heads, int 
                  int num_sms) {
   Shape s{};
   const int rows = n_tokens * (n_heads / n_kv_heads);
+  s.tiles = rows >= kTileMinRows;
   s.nt = column_tiles(rows);
-  s.row_tiles = (rows + 8 * s.nt - 1) / (8 * s.nt);
+  s.step = s.tiles ? 128 : kStep;
+  s.tile_rows = s.tiles ? (rows <= 128 ? 128 : 256) : 8 * s.nt;
+  s.row_tiles = (rows + s.tile_rows - 1) / s.tile_rows;
   s.per = n_kv_heads * s.row_tiles;
   const int64_t units = static_cast<int64_t>(n_seqs) * s.per;
-  const int resident = num_sms * blocks_per_sm(format, hd, s.nt);
+  const int resident = num_sms * (s.tiles ? 1 : blocks_per_sm(format, hd, s.nt));
   s.fit = 2 * units <= resident;
   s.slots = s.fit ? resident : 2 * resident;
   return s;
@@ -980,7 +805,7 @@ cudaError_t launch_format(const Args& a, int format, int nt, int64_t grid, cudaS
 size_t tree_attention_ws_bytes(int format, int hd, int n_seqs, int n_tokens, int n_heads,
                                int n_kv_heads, int num_sms) {
   const Shape s = make_shape(format, hd, n_seqs, n_tokens, n_heads, n_kv_heads, num_sms);
-  return static_cast<size_t>(max_units(s, n_seqs)) * (8 * s.nt) * (hd * 4 + 8);
+  return static_cast<size_t>(max_units(s, n_seqs)) * s.tile_rows * (hd * 4 + 8);
 }
 
 pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* err) {
@@ -1002,14 +827,16 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
   a.cap = t.softcap > 0.f ? t.softcap * sqrtf(static_cast<float>(t.head_dim)) : 0.f;
   a.window = t.window;
   a.row_tiles = s.row_tiles;
-  a.tile_rows = 8 * s.nt;
-  a.min_steps = 2 * kWarps;
+  a.tile_rows = s.tile_rows;
+  a.step = s.step;
+  a.min_steps = s.tiles ? 2 : 2 * kWarps;
   a.status = t.status;
   // a window's keys, with whole steps at both ends
-  const int64_t prefix = t.window > 0 ? std::min<int64_t>(t.max_len, int64_t{t.window} + 2 * kStep)
+  const int64_t prefix = t.window > 0 ? std::min<int64_t>(t.max_len, int64_t{t.window} + 2 * s.step)
                                       : t.max_len;
   const int64_t span = prefix + t.n_tokens;
-  const int64_t most_chunks = (span + kStep * a.min_steps - 1) / (kStep * a.min_steps);
+  const int64_t least = static_cast<int64_t>(a.step) * a.min_steps;
+  const int64_t most_chunks = (span + least - 1) / least;
   const int64_t units = static_cast<int64_t>(c.n_seqs) * s.per;
   int64_t grid = units;
   if (t.ws && most_chunks > 1) {
@@ -1021,9 +848,10 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
     a.ml_part = reinterpret_cast<float2*>(t.ws + static_cast<size_t>(most) * a.tile_rows *
                                                      t.head_dim * 4);
   }
-  cudaError_t ce = t.head_dim == 128 ? launch_format<128>(a, t.format, s.nt, grid, st)
-                                     : launch_format<64>(a, t.format, s.nt, grid, st);
-  if (ce == cudaSuccess && a.slots > 0) {
+  cudaError_t ce = s.tiles ? launch_tile_attention(a, t.format, t.head_dim, grid, st)
+                   : t.head_dim == 128 ? launch_format<128>(a, t.format, s.nt, grid, st)
+                                       : launch_format<64>(a, t.format, s.nt, grid, st);
+  if (ce == cudaSuccess && a.slots > 0 && !s.tiles) {
     const int64_t rows = static_cast<int64_t>(c.n_seqs) * t.n_tokens * t.n_heads;
     const dim3 blocks(static_cast<unsigned>((rows + 7) / 8));
     ce = t.head_dim == 128 ? launch_after(cache_join_kernel<128>, blocks, 256, 0, st, a)

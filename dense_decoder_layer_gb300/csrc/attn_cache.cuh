@@ -1,0 +1,213 @@
+// What the attention kernels over a cache share: the call's arguments, the
+// schedule that cuts the sequences into chunks, asynchronous copies, and the
+// conversion of cached codes.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "kv.h"
+
+namespace pds {
+namespace cacheattn {
+
+constexpr int kMaskWords = kMaxDraftTokens / 32;
+
+struct Args {
+  CacheView c;
+  const uint16_t* q;
+  uint16_t* o;
+  int64_t q_stride, o_stride;
+  const int32_t* parents;
+  int n_tokens, n_heads, group;  // group: query heads per kv head
+  int max_len;
+  float scale_log2;              // log2(e) / sqrt(hd)
+  float cap;                     // softcap in units of q.k (0: none)
+  int window;
+  int step;                      // keys of a step
+  int row_tiles;                 // blocks of query rows per (sequence, kv head)
+  int tile_rows;                 // rows of one
+  int slots;                     // blocks to spread the chunks over; 0: one chunk each
+  int fit;                       // 1: choose chunks so that all units run at once
+  int min_steps;                 // shortest chunk, in steps
+  float* o_part;                 // [unit][tile_rows][hd], each kernel in its own order
+  float2* ml_part;               // [unit][tile_rows]: (maximum, sum)
+  uint32_t* status;
+};
+
+// --------------------------------------------------------------- schedule
+//
+// Units: (chunk of a sequence) x (kv head, row tile), the latter fastest, so
+// that blocks running together read neighbouring heads of the same rows.
+
+// Steps of sequence s: [first, first + n) in units of a.step keys; n = 0 for a
+// length that does not fit.
+__device__ __forceinline__ int seq_steps(const Args& a, int s, int& first, int& len) {
+  len = a.c.lens[s];
+  first = 0;
+  if (len < 0 || len > a.max_len) return 0;
+  // the first row any token can see: a root's, at position len
+  if (a.window > 0 && len - a.window + 1 > 0) first = (len - a.window + 1) / a.step;
+  return (len + a.n_tokens + a.step - 1) / a.step - first;
+}
+
+__device__ __forceinline__ unsigned warp_sum_uint(unsigned v) {
+  return __reduce_add_sync(0xffffffffu, v);
+}
+
+// One warp's view of the schedule: lane i holds sequence i's steps (the first
+// 32 sequences; further ones are read again, from L1, where they are needed).
+struct Lane {
+  int n, first, len;
+};
+__device__ __forceinline__ Lane lane_steps(const Args& a, int s) {
+  Lane l{0, 0, 0};
+  if (s < a.c.n_seqs) l.n = seq_steps(a, s, l.first, l.len);
+  return l;
+}
+
+// Steps per chunk (the same for every sequence), by one warp.
+__device__ __forceinline__ int chunk_steps(const Args& a, int lane, const Lane& mine) {
+  if (a.slots == 0) return 1 << 30;
+  const int per = a.c.n_kv_heads * a.row_tiles;
+  if (!a.fit) {
+    long long total = mine.n;
+    for (int s = lane + 32; s < a.c.n_seqs; s += 32) total += lane_steps(a, s).n;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    // at most slots + (sequences x per) units: every chunk but a sequence's last is whole
+    return max(a.min_steps, static_cast<int>((total * per + a.slots - 1) / a.slots));
+  }
+  float total = static_cast<float>(mine.n);
+  for (int s = lane + 32; s < a.c.n_seqs; s += 32) total += static_cast<float>(lane_steps(a, s).n);
+  total = warp_sum(total);
+  int c = max(a.min_steps, static_cast<int>(__fdividef(total * per, static_cast<float>(a.slots))));
+  // Sequences' last chunks are short: lengthen until the units fit the slots.
+  // There are at most half as many (sequence, head, tile) as slots, so twice
+  // this length always fits: some 16 rounds of a sixteenth at the very most.
+  const unsigned most = static_cast<unsigned>(a.slots / per);
+  for (;;) {
+    unsigned chunks = static_cast<unsigned>(mine.n + c - 1) / static_cast<unsigned>(c);
+    for (int s = lane + 32; s < a.c.n_seqs; s += 32) chunks += (lane_steps(a, s).n + c - 1) / c;
+    if (warp_sum_uint(chunks) <= most) return c;
+    c += max(1, c >> 4);
+  }
+}
+
+struct Unit {
+  int seq, chunk, n_chunks, first, n_steps, len;  // steps [first, first + n_steps)
+  int base;  // (chunk 0 of the sequence) among all chunks
+};
+
+// The sequence and chunk of the w-th chunk overall (w < 0: of sequence `seq`,
+// whole range).  False past the last one.  By one warp; every lane returns it.
+__device__ __forceinline__ bool find_unit(const Args& a, int c, int w, int seq, int lane, const Lane& mine,
+                          Unit& u) {
+  int base = 0;
+  for (int s0 = 0; s0 < a.c.n_seqs; s0 += 32) {
+    const Lane l = s0 == 0 ? mine : lane_steps(a, s0 + lane);
+    const int chunks = l.n == 0 ? 0 : (l.n - 1) / c + 1;
+    int incl = chunks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const int excl = base + incl - chunks;
+    const bool here = w >= 0 ? (w >= excl && w < base + incl) : s0 + lane == seq;
+    const unsigned hit = __ballot_sync(0xffffffffu, here);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      u.seq = s0 + src;
+      u.n_chunks = __shfl_sync(0xffffffffu, chunks, src);
+      u.base = __shfl_sync(0xffffffffu, excl, src);
+      u.len = __shfl_sync(0xffffffffu, l.len, src);
+      const int f = __shfl_sync(0xffffffffu, l.first, src), m = __shfl_sync(0xffffffffu, l.n, src);
+      u.chunk = w >= 0 ? w - u.base : 0;
+      u.first = f + u.chunk * c;
+      u.n_steps = min(c, m - u.chunk * c);
+      return true;
+    }
+    base = __shfl_sync(0xffffffffu, base + incl, 31);
+  }
+  return false;
+}
+
+// ------------------------------------------------------------ instructions
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes (or zeros, when !live) into shared memory, not through L1.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two e4m3 codes, each in the high byte of a 16-bit half (what the other
+// byte holds does not matter), as a pair of bf16: the exponent and mantissa
+// bits move down by four, and 2^120 turns the bias of 7 into one of 127.
+// Exact for every code, subnormal ones included.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t r) {
+  const uint32_t bits = ((r >> 4) & 0x07f007f0u) | (r & 0x80008000u);
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(bits), "r"(0x7b807b80u));
+  return d;
+}
+// Two 4-bit codes (in the low nibbles of 16-bit halves) less their zero
+// points, as bf16: 128 + code and 128 + zero point (z: as 0x4300 | zero point
+// in each half) are bf16 numbers, their difference is exact.
+__device__ __forceinline__ uint32_t int4_pair(uint32_t r, uint32_t z) {
+  const uint32_t bits = (r & 0x000f000fu) | 0x43004300u;
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(bits), "r"(z));
+  return d;
+}
+
+__device__ __forceinline__ bool not_finite2(uint32_t w) {  // either bf16 of a pair
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+
+}  // namespace cacheattn
+
+// The tensor-core kernel and its join (attn_cache_tc.cu): a.step is 128 keys,
+// a.tile_rows 128 or 256 query rows per block, one block per SM.
+cudaError_t launch_tile_attention(const cacheattn::Args& a, int format, int hd, int64_t grid,
+                                  cudaStream_t st);
+
+}  // namespace pds
