@@ -653,13 +653,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
   }
 }
 
-// One warp per (sequence, token, head): the row's chunks joined in order.  Its
-// schedule is made while the chunks are still being computed (lens were
-// complete before those began), its loads after.
+// Four warps per (sequence, token, head) row: warp i joins chunks i, i + 4, ...,
+// and the first joins the four, in order.  The schedule is made while the
+// chunks are still being computed (lens were complete before those began), the
+// loads come after.
 template <int HD>
 __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ Args a) {
+  constexpr int kShare = 4;        // warps of a row
+  constexpr int kPer = HD / 32;
+  constexpr int kBatch = 8;        // chunks whose loads are in flight together
+  __shared__ float part_o[8][HD];
+  __shared__ float2 part_ml[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (8 / kShare) + warp / kShare;
   const int per_seq = a.n_tokens * a.n_heads;
   const int64_t seq64 = row / per_seq;
   Unit u{};
@@ -669,56 +675,75 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
   }
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
-  if (u.n_chunks <= 1) return;  // written by its block, or refused, or no such row
+  const bool live = u.n_chunks > 1;  // else written by its block, or refused, or no such row
   const int seq = u.seq, rest = static_cast<int>(row - seq64 * per_seq);
   const int t = rest / a.n_heads, h = rest - t * a.n_heads;
-  const int head = h / a.group, r = t * a.group + h - head * a.group;
-  const int tile = r / a.tile_rows;
-  const int per = a.c.n_kv_heads * a.row_tiles;
-  const int64_t first = (static_cast<int64_t>(u.base) * per + tile * a.c.n_kv_heads + head) *
-                            a.tile_rows + (r - tile * a.tile_rows);
-  const int64_t stride = static_cast<int64_t>(per) * a.tile_rows;
-  constexpr int kPer = HD / 32;
-  constexpr int kBatch = 8;  // chunks whose loads are in flight together
   float acc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
   float sum = 0.f, m = -INFINITY;
-  for (int x0 = 0; x0 < u.n_chunks; x0 += kBatch) {
-    float2 v[kBatch];
-    float y[kBatch][kPer];
+  if (live) {
+    const int head = h / a.group, r = t * a.group + h - head * a.group;
+    const int tile = r / a.tile_rows;
+    const int per = a.c.n_kv_heads * a.row_tiles;
+    const int64_t first = (static_cast<int64_t>(u.base) * per + tile * a.c.n_kv_heads + head) *
+                              a.tile_rows + (r - tile * a.tile_rows);
+    const int64_t stride = static_cast<int64_t>(per) * a.tile_rows;
+    for (int x0 = warp % kShare; x0 < u.n_chunks; x0 += kBatch * kShare) {
+      float2 v[kBatch];
+      float y[kBatch][kPer];
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      const bool live = x0 + x < u.n_chunks;
-      const int64_t slot = first + (live ? x0 + x : x0) * stride;
-      v[x] = __ldcg(a.ml_part + slot);
-      if (!live) v[x] = make_float2(-INFINITY, 0.f);
-      const float* src = a.o_part + slot * HD + lane * kPer;
-      if constexpr (kPer == 4) {
-        const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-        y[x][0] = f.x, y[x][1] = f.y, y[x][2] = f.z, y[x][3] = f.w;
-      } else {
-        const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-        y[x][0] = f.x, y[x][1] = f.y;
+      for (int x = 0; x < kBatch; ++x) {
+        const bool have = x0 + x * kShare < u.n_chunks;
+        const int64_t slot = first + (have ? x0 + x * kShare : x0) * stride;
+        v[x] = __ldcg(a.ml_part + slot);
+        if (!have) v[x] = make_float2(-INFINITY, 0.f);
+        const float* src = a.o_part + slot * HD + lane * kPer;
+        if constexpr (kPer == 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+          y[x][0] = f.x, y[x][1] = f.y, y[x][2] = f.z, y[x][3] = f.w;
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+          y[x][0] = f.x, y[x][1] = f.y;
+        }
+      }
+      float m_new = m;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) m_new = fmaxf(m_new, v[x].x);
+      const float mu = m_new == -INFINITY ? 0.f : m_new;
+      const float old = exp2f(m - mu);
+      m = m_new;
+      sum *= old;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] *= old;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        if (x0 + x * kShare >= u.n_chunks) break;
+        const float f = exp2f(v[x].x - mu);
+        sum += v[x].y * f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] += y[x][i] * f;
       }
     }
-    float m_new = m;
+  }
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) m_new = fmaxf(m_new, v[x].x);
-    const float mu = m_new == -INFINITY ? 0.f : m_new;
-    const float old = exp2f(m - mu);
-    m = m_new;
-    sum *= old;
+  for (int i = 0; i < kPer; ++i) part_o[warp][lane * kPer + i] = acc[i];
+  if (lane == 0) part_ml[warp] = make_float2(m, sum);
+  __syncthreads();
+  if (!live || warp % kShare) return;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] *= old;
+  for (int x = 0; x < kShare; ++x) m = fmaxf(m, part_ml[warp + x].x);
+  const float mu = m == -INFINITY ? 0.f : m;
+  sum = 0.f;
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      if (x0 + x >= u.n_chunks) break;
-      const float f = exp2f(v[x].x - mu);
-      sum += v[x].y * f;
+  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] += y[x][i] * f;
-    }
+  for (int x = 0; x < kShare; ++x) {
+    const float2 v = part_ml[warp + x];
+    const float f = exp2f(v.x - mu);
+    sum += v.y * f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] += part_o[warp + x][lane * kPer + i] * f;
   }
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
   uint16_t* dst = a.o + (static_cast<int64_t>(seq) * a.n_tokens + t) * a.o_stride + h * HD + lane * kPer;
@@ -754,7 +779,7 @@ Shape make_shape(int format, int hd, int n_seqs, int n_tokens, int n_heads, int 
   const int rows = n_tokens * (n_heads / n_kv_heads);
   s.tiles = rows >= kTileMinRows;
   s.nt = column_tiles(rows);
-  s.step = s.tiles ? 128 : kStep;
+  s.step = s.tiles ? 64 : kStep;
   s.tile_rows = s.tiles ? (rows <= 128 ? 128 : 256) : 8 * s.nt;
   s.row_tiles = (rows + s.tile_rows - 1) / s.tile_rows;
   s.per = n_kv_heads * s.row_tiles;
@@ -829,7 +854,7 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
   a.row_tiles = s.row_tiles;
   a.tile_rows = s.tile_rows;
   a.step = s.step;
-  a.min_steps = s.tiles ? 2 : 2 * kWarps;
+  a.min_steps = s.tiles ? 4 : 2 * kWarps;
   a.status = t.status;
   // a window's keys, with whole steps at both ends
   const int64_t prefix = t.window > 0 ? std::min<int64_t>(t.max_len, int64_t{t.window} + 2 * s.step)
@@ -853,7 +878,7 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
                                        : launch_format<64>(a, t.format, s.nt, grid, st);
   if (ce == cudaSuccess && a.slots > 0 && !s.tiles) {
     const int64_t rows = static_cast<int64_t>(c.n_seqs) * t.n_tokens * t.n_heads;
-    const dim3 blocks(static_cast<unsigned>((rows + 7) / 8));
+    const dim3 blocks(static_cast<unsigned>((rows + 1) / 2));
     ce = t.head_dim == 128 ? launch_after(cache_join_kernel<128>, blocks, 256, 0, st, a)
                            : launch_after(cache_join_kernel<64>, blocks, 256, 0, st, a);
   }
