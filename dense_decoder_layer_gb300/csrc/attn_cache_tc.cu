@@ -14,8 +14,9 @@
 // K/V tile, else they are the even and the odd key tiles of one row tile.
 // While one stream's softmax runs, the tensor pipe works for the other, and
 // each stream has two score buffers.
-//   warp 0       tcgen05.mma issuer: S = Q K^T into TMEM, O += P V with P read
-//                from tensor memory (over its S) and V MN-major from its rows
+//   warps 0, 1   tcgen05.mma issuers, one per stream: S = Q K^T into TMEM,
+//                O += P V with P read from tensor memory (over its S) and V
+//                MN-major from its rows
 //   warps 4-7    K loaders, warps 8-11 V loaders (neither waits for the other's
 //                stages): 16-byte asynchronous copies of cache rows; 8- and
 //                4-bit codes land in slots private to their thread, which
@@ -69,9 +70,12 @@ struct TileCfg {
   static constexpr int kPerRow = kRow / 16;                // 16-byte pieces of a row
   static constexpr int kPieces = 64 * kPerRow / kLoadThreads;  // of a thread, per tile
   static_assert(kPieces >= 1, "every loader has a piece");
-  // Stages of K and of V, and raw slots of each (8- and 4-bit tiles wait there)
-  static constexpr int kKStages = kQuant && HD == 128 ? 3 : 4;
-  static constexpr int kVStages = HD == 64 ? 6 : kQuant ? 3 : 5;
+  // Stages of K and of V, and raw slots of each (8- and 4-bit tiles wait there).
+  // Even numbers: streams over different key tiles then never share a stage,
+  // so a stage's phases are waited for one after the other by one issuer.
+  static constexpr int kKStages = 4;
+  static constexpr int kVStages = HD == 64 ? 6 : kQuant ? 2 : 4;
+  static_assert(kKStages % 2 == 0 && kVStages % 2 == 0, "stages of two streams");
   static constexpr int kRaw = FMT == PDS_KV_E4M3 && HD == 128 ? 3 : 4;
   // Ring of scale words, fetched with K's raw slots.  When K's tile j is turned
   // into its stage, S of tile j - kKStages is done, so (two score buffers, two
@@ -96,20 +100,56 @@ struct TileCfg {
   static constexpr uint32_t kTmS = 0, kTmO = 256, kTmemCols = 512;
 };
 
-// K-major operand of `rows` rows: 16 contraction elements are 32 bytes inside a
-// 128-byte column block, 4 per block, blocks rows x 128 bytes apart.
+// Matrix descriptors (128-byte swizzle): the high words are constants, the low
+// ones an address in 16-byte units plus, for V, the leading offset.
+//  * K-major operand of ROWS rows: 16 contraction elements are 32 bytes inside
+//    a 128-byte column block, 4 per block, blocks ROWS x 128 bytes apart.
+//  * V tile [64 keys][HD] as the MN-major B operand: rows are keys (128 bytes of
+//    64 channels), 8-row groups 1024 bytes apart, channels 64..127 8 KB on.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kKMajorLo = 1u << 16, kVLo = (8192u >> 4) << 16;
 template <int ROWS>
-__device__ __forceinline__ uint64_t kmajor_desc(uint32_t base, int kstep) {
-  return sm100::smem_desc_sw128(base + static_cast<uint32_t>(kstep >> 2) * (ROWS * 128u) +
-                                static_cast<uint32_t>(kstep & 3) * 32u);
+__host__ __device__ constexpr uint32_t kmajor_step(int x) {
+  return (static_cast<uint32_t>(x >> 2) * (ROWS * 128u) + static_cast<uint32_t>(x & 3) * 32u) >> 4;
 }
-// V tile [64 keys][HD] as the MN-major B operand: rows are keys (128 bytes of
-// 64 channels), 8-row groups 1024 bytes apart, channels 64..127 8 KB on.
-__device__ __forceinline__ uint64_t v_desc(uint32_t base, int kstep) {
-  const uint32_t a = base + static_cast<uint32_t>(kstep) * 16u * 128u;
-  return static_cast<uint64_t>((a >> 4) & 0x3FFFu) | static_cast<uint64_t>(8192u >> 4) << 16 |
-         static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1) << 46 |
-         static_cast<uint64_t>(2) << 61;
+__host__ __device__ constexpr uint32_t v_step(int x) { return x * 16u * 128u >> 4; }
+
+// One product step, issued by the leader of a converged warp.  All lanes hold
+// the same operands, so they live in uniform registers: a step costs a few
+// instructions (from one lane of a diverged warp each operand had to be moved
+// there first, and 8 steps took ~900 cycles).
+__device__ __forceinline__ void mma_ss(bool leader, uint32_t d, uint32_t a_lo, uint32_t b_lo,
+                                       uint32_t id, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 a, {%1, %4};\n\t"
+      "mov.b64 b, {%2, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(id), "r"(kDescHi), "r"(static_cast<uint32_t>(accumulate)),
+      "r"(static_cast<uint32_t>(leader))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(bool leader, uint32_t d, uint32_t a_tmem, uint32_t b_lo,
+                                       uint32_t id, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 b, {%2, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(id), "r"(kDescHi), "r"(static_cast<uint32_t>(accumulate)),
+      "r"(static_cast<uint32_t>(leader))
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(bool leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(static_cast<uint32_t>(leader))
+      : "memory");
 }
 __host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) |
@@ -280,82 +320,59 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (warp < kFirstLoadWarp) {
     setmaxnreg_dec<kLeanRegs>();
-    if (warp == 0 && lane == 0 && n > 0) {
+    if (warp < 2 && n > 0) {
+      // One issuer per stream: their products interleave on the tensor pipe, so
+      // one's waits cost the other nothing.  Per tile: S_i into the buffer that
+      // P_{i-2} has left, then O += P_{i-1} V_{i-1} once the softmax has made P.
       constexpr uint32_t kIdS = idesc(128, kKeys, false);
       constexpr uint32_t kIdPV = idesc(128, HD, true);
-      bool ok = mbar_wait(bar_q, 0, abort_flag, a.status);
-      // Per stream and tile: S_i into the buffer that P_{i-2} has left, O += P_i V_i
-      // once the softmax has made P_i.  Whichever product has its operands is
-      // issued next, so neither stream waits behind the other.  (Streams over
-      // different key tiles take their tiles of K in order: a stage's barrier is
-      // asked only for the phase after the last one seen.)
-      int next_k = 0;
-      int s_at[2] = {0, 0}, pv_at[2] = {0, 0};  // tiles whose S / P V has been issued
-      const int tiles[2] = {n_tiles0, n_tiles1};
-      auto try_s = [&](auto stream) {
-        constexpr int s = stream;
-        const int i = s_at[s], b = i & 1;
-        if (i >= tiles[s] || i >= pv_at[s] + 2) return false;
-        const int t = tile_of(s, i), st = t % C::kKStages;
-        if (!two_tiles && t != next_k) return false;
-        if (!mbar_test(bar_k_full(st), (t / C::kKStages) & 1)) return false;
-        if (i >= 2 && !mbar_test(bar_pv(s, b), ((i >> 1) - 1) & 1)) return false;
-        tc_fence_after();
-        const uint32_t q = sbase + C::kQ + (two_tiles ? s * C::kQTile : 0u);
-        const uint32_t k = sbase + C::kK + st * C::kTile;
-#pragma unroll
-        for (int x = 0; x < HD / 16; ++x)
-          umma_bf16(tmem + C::kTmS + s * 128u + b * 64u, kmajor_desc<128>(q, x),
-                    kmajor_desc<64>(k, x), kIdS, x > 0 ? 1u : 0u);
-        umma_commit(bar_s_full(s, b));
-        umma_commit(bar_k_empty(st));
-        ++next_k;
-        s_at[s] = i + 1;
-        return true;
+      const int s = warp, tiles = s == 0 ? n_tiles0 : n_tiles1;
+      const bool leader = lane == 0;
+      bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity, abort_flag, a.status)) != 0;
+        return ok;
       };
-      auto try_pv = [&](auto stream) {
-        constexpr int s = stream;
-        const int i = pv_at[s], b = i & 1;
-        if (i >= s_at[s]) return false;
-        if (!mbar_test(bar_p_full(s, b), (i >> 1) & 1)) return false;
-        const int t = tile_of(s, i), st = t % C::kVStages;
-        if (!mbar_test(bar_v_full(st), (t / C::kVStages) & 1)) return false;
-        tc_fence_after();
-        const uint32_t v = sbase + C::kV + st * C::kTile;
+      const uint32_t q = ((sbase + C::kQ + (two_tiles ? s * C::kQTile : 0u)) >> 4) | kKMajorLo;
+      const uint32_t scores_at = tmem + C::kTmS + s * 128u, o_at = tmem + C::kTmO + s * 128u;
+      const int step = two_tiles ? 1 : 2;
+      // stages and phases of the tile whose S / P V comes next
+      int k_st = two_tiles ? 0 : s, v_st = k_st;
+      uint32_t k_phase = 0, v_phase = 0;
+      wait(bar_q, 0);
+      for (int i = 0; ok && i <= tiles; ++i) {
+        const uint32_t b = i & 1;
+        if (i < tiles) {
+          if (i >= 2 && !wait(bar_pv(s, b), ((i >> 1) - 1) & 1)) break;
+          if (!wait(bar_k_full(k_st), k_phase)) break;
+          tc_fence_after();
+          const uint32_t k = ((sbase + C::kK + k_st * C::kTile) >> 4) | kKMajorLo;
 #pragma unroll
-        for (int x = 0; x < kKeys / 16; ++x)
-          umma_bf16_ts(tmem + C::kTmO + s * 128u, tmem + C::kTmS + s * 128u + b * 64u + x * 8u,
-                       v_desc(v, x), kIdPV, (i > 0 || x > 0) ? 1u : 0u);
-        umma_commit(bar_pv(s, b));
-        umma_commit(bar_v_empty(st));
-        pv_at[s] = i + 1;
-        return true;
-      };
-      uint64_t t0 = 0;
-      uint32_t idle = 0;
-      while (ok && (pv_at[0] < tiles[0] || pv_at[1] < tiles[1])) {
-        bool progress = try_pv(std::integral_constant<int, 0>{});
-        progress |= try_s(std::integral_constant<int, 0>{});
-        progress |= try_pv(std::integral_constant<int, 1>{});
-        progress |= try_s(std::integral_constant<int, 1>{});
-        if (progress) {
-          idle = 0;
-        } else if ((++idle & 255u) == 0) {  // bounded as the other waits are
-          if (idle == 256u) t0 = global_timer_ns();
-          if (*abort_flag) {
-            ok = false;
-          } else if (global_timer_ns() - t0 > kWaitLimitNs) {
-            *abort_flag = 1;
-            atomicOr(a.status, kStatusTimeout);
-            ok = false;
-          }
+          for (int x = 0; x < HD / 16; ++x)
+            mma_ss(leader, scores_at + b * 64u, q + kmajor_step<128>(x), k + kmajor_step<64>(x),
+                   kIdS, x > 0);
+          mma_commit(leader, bar_s_full(s, b));
+          mma_commit(leader, bar_k_empty(k_st));
+          if ((k_st += step) >= C::kKStages) k_st -= C::kKStages, k_phase ^= 1u;
+        }
+        if (i >= 1) {
+          const int e = i - 1;
+          if (!wait(bar_v_full(v_st), v_phase)) break;
+          if (!wait(bar_p_full(s, e & 1), (e >> 1) & 1)) break;
+          tc_fence_after();
+          const uint32_t v = ((sbase + C::kV + v_st * C::kTile) >> 4) | kVLo;
+          const uint32_t p_at = scores_at + (e & 1) * 64u;
+#pragma unroll
+          for (int x = 0; x < kKeys / 16; ++x)
+            mma_ts(leader, o_at, p_at + x * 8u, v + v_step(x), kIdPV, e > 0 || x > 0);
+          mma_commit(leader, bar_pv(s, e & 1));
+          mma_commit(leader, bar_v_empty(v_st));
+          if ((v_st += step) >= C::kVStages) v_st -= C::kVStages, v_phase ^= 1u;
         }
       }
-      umma_commit(bar_done(0));
-      umma_commit(bar_done(1));
+      mma_commit(leader, bar_done(s));
       int dummy = 0;
-      mbar_wait(bar_done(0), 0, &dummy, a.status);
-      mbar_wait(bar_done(1), 0, &dummy, a.status);
+      mbar_wait(bar_done(s), 0, &dummy, a.status);
     }
   } else if (warp < kFirstSoftmaxWarp) {
     setmaxnreg_dec<kLeanRegs>();
