@@ -7,9 +7,10 @@
 //   z_rj = log2(e)/sqrt(hd) kscale_j (q_r . kcode_j)       (softcap on top)
 //   o_r  = sum_j 2^(z_rj - m_r) vscale_j vcode_j / sum_j 2^(z_rj - m_r)
 // over the keys j that token t sees: the scales stay out of the matrix
-// products, so the codes go into them as exact bf16 integers or e4m3 values
-// and nothing is rounded on the way but P (2^(z-m) vscale, to bf16, as in the
-// prefill attention: its error averages out over the keys) and o (once).
+// products, so the codes go into them as they are (fp16 holds every one) and
+// nothing is rounded on the way but P = 2^(z-m) vscale, to fp16, or to bf16 for
+// a bf16 cache, as in the prefill attention (a weight's error averages out over
+// the keys), and o (once).
 //
 // What bounds it: every cached row is used by T G query rows, one to a few
 // dozen, so at 2 T G flop per byte of bf16 the call is bound by reading the
@@ -66,19 +67,27 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
+template <bool BF16>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                     uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // ------------------------------------------------------------ the formats
 
 // Bytes of a head's row, and of one step's K (or V) slice.
 template <int FMT, int HD>
 struct Fmt {
-  static constexpr int kRow = FMT == PDS_KV_BF16 ? 2 * HD : FMT == PDS_KV_E4M3 ? HD : HD / 2;
+  static constexpr bool kBf16 = FMT == PDS_KV_BF16;
+  static constexpr int kRow = kBf16 ? 2 * HD : FMT == PDS_KV_E4M3 ? HD : HD / 2;
   static constexpr int kSlice = kStep * kRow;
   static constexpr int kChunks = kRow / 16;  // 16-byte chunks of a row
   static constexpr int kStage = 2 * kSlice + 128;  // K, V, 16 + 16 scale words
@@ -110,7 +119,7 @@ struct Fmt {
       ch[0] = c, ch[1] = c + 1, ch[2] = c + 2, ch[3] = c + 3;
     } else if constexpr (FMT == PDS_KV_E4M3) {
       const int c = 16 * (t4 + 4 * (ks >> 2)) + 4 * (ks & 3);
-      ch[0] = c, ch[1] = c + 2, ch[2] = c + 1, ch[3] = c + 3;
+      ch[0] = c, ch[1] = c + 1, ch[2] = c + 2, ch[3] = c + 3;
     } else {
       const int c = (HD / 4) * t4 + 8 * (ks >> 1) + 2 * (ks & 1);
       ch[0] = c, ch[1] = c + 4, ch[2] = c + 1, ch[3] = c + 5;
@@ -137,7 +146,7 @@ __device__ __forceinline__ void scores(uint32_t ks, uint32_t q_frag, int lane, u
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const uint2 b = lds64(q_frag + ((k * NT + n) * 32 + lane) * 8);
-      mma(s[n], a, b.x, b.y);
+      mma<F::kBf16>(s[n], a, b.x, b.y);
     }
   };
   if constexpr (FMT == PDS_KV_BF16) {
@@ -157,8 +166,9 @@ __device__ __forceinline__ void scores(uint32_t ks, uint32_t q_frag, int lane, u
       const uint32_t x[4] = {xv.x, xv.y, xv.z, xv.w}, y[4] = {yv.x, yv.y, yv.z, yv.w};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const uint32_t a[4] = {e4m3_pair(x[w] << 8), e4m3_pair(y[w] << 8), e4m3_pair(x[w]),
-                               e4m3_pair(y[w])};
+        uint32_t a[4];
+        e4m3_pairs(x[w], a[0], a[2]);
+        e4m3_pairs(y[w], a[1], a[3]);
         step(4 * c + w, a);
       }
     }
@@ -177,10 +187,11 @@ __device__ __forceinline__ void scores(uint32_t ks, uint32_t q_frag, int lane, u
     }
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
-      const uint32_t a0[4] = {int4_pair(x[w], kz0), int4_pair(y[w], kz1),
-                              int4_pair(x[w] >> 4, kz0), int4_pair(y[w] >> 4, kz1)};
-      const uint32_t a1[4] = {int4_pair(x[w] >> 8, kz0), int4_pair(y[w] >> 8, kz1),
-                              int4_pair(x[w] >> 12, kz0), int4_pair(y[w] >> 12, kz1)};
+      const uint32_t a0[4] = {int4_lo(x[w], kz0), int4_lo(y[w], kz1), int4_hi(x[w], kz0),
+                              int4_hi(y[w], kz1)};
+      x[w] >>= 8, y[w] >>= 8;
+      const uint32_t a1[4] = {int4_lo(x[w], kz0), int4_lo(y[w], kz1), int4_hi(x[w], kz0),
+                              int4_hi(y[w], kz1)};
       step(2 * w, a0);
       step(2 * w + 1, a1);
     }
@@ -188,9 +199,11 @@ __device__ __forceinline__ void scores(uint32_t ks, uint32_t q_frag, int lane, u
 }
 
 // O^T += V^T P^T of one step; p: the B fragments of P^T (two registers per
-// column tile); vz0, vz1: zero points of keys (2t, 2t+1) and (2t+8, 2t+9).
+// column tile); vz0, vz1: zero points of keys (2t, 2t+1) and (2t+8, 2t+9);
+// clean: hidden rows may hold any code.
 template <int FMT, int HD, int NT>
 __device__ __forceinline__ void accumulate(uint32_t vs, int lane, uint32_t vz0, uint32_t vz1,
+                                           bool clean,
                                            const uint32_t (&p)[NT][2],
                                            float (&o)[Fmt<FMT, HD>::kMTiles][NT][4]) {
   using F = Fmt<FMT, HD>;
@@ -202,7 +215,7 @@ __device__ __forceinline__ void accumulate(uint32_t vs, int lane, uint32_t vz0, 
       uint32_t a[4];
       ldsm4_t(vs + F::v_at(key, 2 * i + odd), a);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma(o[i][n], a, p[n][0], p[n][1]);
+      for (int n = 0; n < NT; ++n) mma<true>(o[i][n], a, p[n][0], p[n][1]);
     }
   } else {
     // this lane's channels of keys 2t, 2t+1, 2t+8, 2t+9
@@ -223,18 +236,24 @@ __device__ __forceinline__ void accumulate(uint32_t vs, int lane, uint32_t vz0, 
       }
     }
     if constexpr (FMT == PDS_KV_E4M3) {
+      if (clean) {
 #pragma unroll
-      for (int i = 0; i < F::kMTiles; ++i) {
-        // channel tile i: bytes 2 (i & 1) and + 1 of word i / 2, both keys of a pair
-        const int x = i >> 1;
-        const uint32_t sel = (i & 1) ? 0x6020u : 0x4000u, sel1 = (i & 1) ? 0x7030u : 0x5010u;
-        const uint32_t a[4] = {e4m3_pair(__byte_perm(w[0][x], w[1][x], sel)),
-                               e4m3_pair(__byte_perm(w[0][x], w[1][x], sel1)),
-                               e4m3_pair(__byte_perm(w[2][x], w[3][x], sel)),
-                               e4m3_pair(__byte_perm(w[2][x], w[3][x], sel1))};
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma(o[i][n], a, p[n][0], p[n][1]);
+          for (int x = 0; x < kW; ++x) w[i][x] = e4m3_finite(w[i][x]);
       }
+#pragma unroll
+      for (int x = 0; x < kW; ++x)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          // channel tile 2 x + half: bytes 2 half and + 1 of word x, paired over keys
+          const uint32_t sel = half ? 0x7362u : 0x5140u;
+          uint32_t a[4];
+          e4m3_pairs(__byte_perm(w[0][x], w[1][x], sel), a[0], a[1]);
+          e4m3_pairs(__byte_perm(w[2][x], w[3][x], sel), a[2], a[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma<false>(o[2 * x + half][n], a, p[n][0], p[n][1]);
+        }
     } else {
 #pragma unroll
       for (int i = 0; i < F::kMTiles; ++i) {
@@ -243,10 +262,10 @@ __device__ __forceinline__ void accumulate(uint32_t vs, int lane, uint32_t vz0, 
         const uint32_t sel = b | (static_cast<uint32_t>(4 + b) << 8);  // into bytes 0 and 2
         const uint32_t r0 = __byte_perm(w[0][x], w[1][x], sel);
         const uint32_t r1 = __byte_perm(w[2][x], w[3][x], sel);
-        const uint32_t a[4] = {int4_pair(r0, vz0), int4_pair(r0 >> 4, vz0), int4_pair(r1, vz1),
-                               int4_pair(r1 >> 4, vz1)};
+        const uint32_t a[4] = {int4_lo(r0, vz0), int4_hi(r0, vz0), int4_lo(r1, vz1),
+                               int4_hi(r1, vz1)};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma(o[i][n], a, p[n][0], p[n][1]);
+        for (int n = 0; n < NT; ++n) mma<false>(o[i][n], a, p[n][0], p[n][1]);
       }
     }
   }
@@ -268,7 +287,8 @@ struct Cfg {
   static constexpr int kDepth = kMask + kRows * kMaskWords * 4;
   static constexpr int kParent = kDepth + kMaxDraftTokens * 2;
   static constexpr int kMl = kParent + kMaxDraftTokens * 4;   // per warp and row: (maximum, sum)
-  static constexpr int kMisc = kMl + kWarps * kRows * 8;
+  static constexpr int kInv = kMl + kWarps * kRows * 8;       // per warp: O's unit; Q's maximum
+  static constexpr int kMisc = kInv + 2 * kWarps * 4;
   static constexpr int kRing = (kMisc + 64 + 127) / 128 * 128;
   static constexpr int kRingBytes = kWarps * kStages * F::kStage;
   // the warps' O rows are joined in the space of the ring
@@ -353,23 +373,39 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
   for (int i = 0; i < C::kStages - 1; ++i) fetch(i);
 
   // Q as B fragments, in the contraction's channel order; rows past the last are zero
-  for (int idx = threadIdx.x; idx < F::kKSteps * NT * 32; idx += kThreads) {
+  constexpr int kQFrags = F::kKSteps * NT * 32;
+  constexpr int kQIters = (kQFrags + kThreads - 1) / kThreads;
+  uint32_t* q_max = reinterpret_cast<uint32_t*>(smem + C::kInv) + kWarps;
+  uint32_t qb[kQIters][2], q_top = 0u;
+#pragma unroll
+  for (int it = 0; it < kQIters; ++it) {
+    const int idx = it * kThreads + threadIdx.x;
     const int l = idx & 31, n = (idx >> 5) % NT, ks = idx / (32 * NT);
     const int r = r0 + 8 * n + (l >> 2);
-    uint32_t b[2] = {0u, 0u};
-    if (r < rows) {
+    qb[it][0] = qb[it][1] = 0u;
+    if (idx < kQFrags && r < rows) {
       const int t = r / a.group, i = r - t * a.group;
       const uint16_t* src = a.q + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.q_stride +
                             (head * a.group + i) * HD;
       int ch[4];
       F::q_channels(ks, l & 3, ch);
-      b[0] = src[ch[0]] | static_cast<uint32_t>(src[ch[1]]) << 16;
-      b[1] = src[ch[2]] | static_cast<uint32_t>(src[ch[3]]) << 16;
+      qb[it][0] = src[ch[0]] | static_cast<uint32_t>(src[ch[1]]) << 16;
+      qb[it][1] = src[ch[2]] | static_cast<uint32_t>(src[ch[3]]) << 16;
     }
-    *reinterpret_cast<uint2*>(smem + C::kQ + idx * 8) = make_uint2(b[0], b[1]);
+    if constexpr (!F::kBf16) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        q_top = max(q_top, max(finite_bits(__uint_as_float(qb[it][e] << 16)),
+                               finite_bits(__uint_as_float(qb[it][e] & 0xffff0000u))));
+    }
+  }
+  if constexpr (!F::kBf16) {
+    q_top = __reduce_max_sync(0xffffffffu, q_top);
+    if (lane == 0) q_max[warp] = q_top;
   }
   // depths of all tokens and ancestor sets of this tile's
   const int t_first = r0 / a.group;
+  float q_inv = 1.f;  // what a score is multiplied by besides K's scale
   {
     const int t = threadIdx.x;
     if (a.parents && t < a.n_tokens)
@@ -377,6 +413,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
     const int tl = t - t_first;
     const bool here = tl >= 0 && tl < C::kRows && t < a.n_tokens;
     __syncthreads();
+    float q_mul = 1.f;
+    if constexpr (!F::kBf16) {
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) q_top = max(q_top, q_max[x]);
+      q_mul = q_multiplier(q_top, q_inv);
+    }
+#pragma unroll
+    for (int it = 0; it < kQIters; ++it) {
+      const int idx = it * kThreads + threadIdx.x;
+      if constexpr (!F::kBf16) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          qb[it][e] = pack_f16x2(__uint_as_float(qb[it][e] << 16) * q_mul,
+                                 __uint_as_float(qb[it][e] & 0xffff0000u) * q_mul);
+      }
+      if (idx < kQFrags)
+        *reinterpret_cast<uint2*>(smem + C::kQ + idx * 8) = make_uint2(qb[it][0], qb[it][1]);
+    }
     if (t < a.n_tokens) {
       const int d = a.parents ? tree_depth(par, t) : t;
       depth[t] = static_cast<int16_t>(d);
@@ -428,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 #pragma unroll
     for (int e = 0; e < 2; ++e) m_ref[n][e] = -INFINITY, l[n][e] = 0.f;
 
+  uint32_t v_exp = kMinScaleExp;  // exponent of the largest V scale so far: O's unit
   const uint32_t q_frag = smem_addr(smem) + C::kQ;
   for (int i = 0; i < n_mine; ++i) {
     copies_wait<C::kStages - 2>();
@@ -448,13 +503,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
         kw[e] = lds32(sw + (g + 8 * e) * 4);
         vw[e] = lds32(sw + 64 + (g + 8 * e) * 4);
         if constexpr (FMT == PDS_KV_INT4) {
-          kz[e] = 0x43004300u | (kw[e] & 15u) | (kw[e] & 15u) << 16;
+          kz[e] = int4_zero(kw[e], kw[e]);
           kw[e] &= 0xffff0000u;
           vw[e] &= 0xffff0000u;
           const uint2 z = lds64(sw + 64 + (2 * t4 + 8 * e) * 4);
-          vz[e] = 0x43004300u | (z.x & 15u) | (z.y & 15u) << 16;
+          vz[e] = int4_zero(z.x, z.y);
         }
-        kscale[e] = __uint_as_float(kw[e]);
+        kscale[e] = __uint_as_float(kw[e]) * q_inv;
         vscale[e] = __uint_as_float(vw[e]);
       }
     }
@@ -478,11 +533,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
     // a step that holds new tokens, the end, or a window's lower edge
     bool masked = j0 + kStep > u.len;
     if (VAR && a.window > 0) masked |= j0 <= pos_hi - a.window;
+    bool seen[2] = {true, true};  // whether one of this lane's rows sees its key
     if (masked) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int j = j0 + g + 8 * e, rel = j - u.len;
         const int key_pos = rel < 0 ? j : u.len + (rel < a.n_tokens ? depth[rel] : 0);
+        seen[e] = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -493,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
               see = rel < a.n_tokens && ((mask[t * kMaskWords + (rel >> 5)] >> (rel & 31)) & 1u);
             if (VAR && a.window > 0) see = see && key_pos > pos[n][x] - a.window;
             if (!see) s[n][2 * e + x] = -INFINITY;
+            seen[e] |= see;
           }
       }
     }
@@ -502,7 +560,27 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) far |= s[n][e] > m_ref[n][e & 1] + kMoveLog2;
+    uint32_t v_top = v_exp;
+    if constexpr (!F::kBf16) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (seen[e]) v_top = max(v_top, finite_bits(vscale[e]) >> 23);
+      far |= v_top > v_exp;
+    }
     if (__any_sync(0xffffffffu, far)) {
+      if constexpr (!F::kBf16) {
+        v_top = __reduce_max_sync(0xffffffffu, v_top);
+        if (v_top > v_exp) {  // O in units of the larger scale; exact
+          const float f = v_multiplier(v_top) * v_inverse(v_exp);
+          v_exp = v_top;
+#pragma unroll
+          for (int t = 0; t < F::kMTiles; ++t)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[t][n][e] *= f;
+        }
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -523,6 +601,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
         }
     }
     // P, its row sums (float32, unrounded) and its transposed fragments
+    if constexpr (!F::kBf16) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) vscale[e] *= v_multiplier(v_exp);
+    }
     uint32_t pf[NT][2];
     float pv[NT][4];
 #pragma unroll
@@ -536,8 +618,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
         if constexpr (FMT != PDS_KV_BF16)  // a hidden row may have any scale, a NaN too
           pv[n][e] = masked && pe == 0.f ? 0.f : pe * vscale[e >> 1];
       }
-      pf[n][0] = transpose8(pack_bf16x2(pv[n][0], pv[n][1]));
-      pf[n][1] = transpose8(pack_bf16x2(pv[n][2], pv[n][3]));
+      auto pack = [](float lo, float hi) {
+        return F::kBf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+      };
+      pf[n][0] = transpose8(pack(pv[n][0], pv[n][1]));
+      pf[n][1] = transpose8(pack(pv[n][2], pv[n][3]));
     }
     if constexpr (FMT == PDS_KV_BF16) {
       // A hidden row of a masked step may hold an infinity or a NaN, which a
@@ -579,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
         }
       }
     }
-    accumulate<FMT, HD, NT>(st + F::kSlice, lane, vz[0], vz[1], pf, o);
+    accumulate<FMT, HD, NT>(st + F::kSlice, lane, vz[0], vz[1], masked, pf, o);
   }
   copies_wait<0>();
 
@@ -593,6 +678,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
       for (int sh = 4; sh < 32; sh <<= 1) l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], sh);
       if (g == 0) ml[warp * C::kRows + 8 * n + 2 * t4 + x] = make_float2(m_ref[n][x], l[n][x]);
     }
+  float* unit = reinterpret_cast<float*>(smem + C::kInv);  // of the warps' O
+  if (lane == 0) unit[warp] = F::kBf16 ? 1.f : v_inverse(v_exp);
   __syncthreads();  // every warp is done with the ring
   float* join = reinterpret_cast<float*>(smem + C::kRing);
 #pragma unroll
@@ -628,11 +715,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
       const float2 v = ml[x * C::kRows + r];
       const float f = exp2f(v.x - mu);  // 0 for a warp that saw none of the row's keys
       const float4 y = *reinterpret_cast<const float4*>(join + (x * C::kRows + r) * C::kJoinStride + ch);
+      const float fo = f * unit[x];
       sum += v.y * f;
-      acc.x += y.x * f;
-      acc.y += y.y * f;
-      acc.z += y.z * f;
-      acc.w += y.w * f;
+      acc.x += y.x * fo;
+      acc.y += y.y * fo;
+      acc.z += y.z * fo;
+      acc.w += y.w * fo;
     }
     if (depth[t] < 0) {  // a padding token's rows went along with the others
       m = -INFINITY;

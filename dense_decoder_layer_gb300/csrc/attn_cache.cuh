@@ -178,25 +178,74 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Two e4m3 codes, each in the high byte of a 16-bit half (what the other
-// byte holds does not matter), as a pair of bf16: the exponent and mantissa
-// bits move down by four, and 2^120 turns the bias of 7 into one of 127.
-// Exact for every code, subnormal ones included.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t r) {
-  const uint32_t bits = ((r >> 4) & 0x07f007f0u) | (r & 0x80008000u);
+// 8- and 4-bit rows go into the products as fp16, whose 11 bits hold every code
+// exactly and round P eight times finer than bf16 would; the conversions are
+// few and cheap (one instruction per pair of e4m3 codes, where spreading the
+// bits to bf16 takes five, and the pipe that runs those was the busiest).
+// fp16's range is narrow, so both other operands are brought into it by powers
+// of two:
+//  * Q: all of a block's rows by one, so that its largest value is 2^14 .. 2^15.
+//    What that rounds is below 2^-31 of the largest value.
+//  * P times V's scale: by one that keeps it below 2^15, from the largest V scale
+//    met so far.  A weight is then rounded to 2^-25 or finer, in units of 2^15
+//    for the largest possible one: what is lost is below 2^-32 of a row's
+//    weight per key, also where V's scales differ by 2^20.
+__device__ __forceinline__ void e4m3_pairs(uint32_t r, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(r));
+}
+// Codes that stand for NaN (never stored by a write, but unwritten rows may hold
+// anything) as the largest number instead: a zero weight then keeps them out.
+__device__ __forceinline__ uint32_t e4m3_finite(uint32_t w) {
+  const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return w ^ (nan >> 7);
+}
+// Two 4-bit codes in the low (lo) or high (hi) nibbles of the low bytes of
+// 16-bit halves, less their zero points: 1024 + code and 1024 + 16 code are
+// fp16 numbers, and so is every difference.  Zero points as int4_zero makes them.
+__device__ __forceinline__ uint32_t int4_lo(uint32_t r, uint32_t zero) {
+  const uint32_t bits = (r & 0x000f000fu) | 0x64006400u;
   uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(bits), "r"(0x7b807b80u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(bits), "r"(zero));
   return d;
 }
-// Two 4-bit codes (in the low nibbles of 16-bit halves) less their zero
-// points, as bf16: 128 + code and 128 + zero point (z: as 0x4300 | zero point
-// in each half) are bf16 numbers, their difference is exact.
-__device__ __forceinline__ uint32_t int4_pair(uint32_t r, uint32_t z) {
-  const uint32_t bits = (r & 0x000f000fu) | 0x43004300u;
+__device__ __forceinline__ uint32_t int4_hi(uint32_t r, uint32_t zero) {
+  const uint32_t bits = (r & 0x00f000f0u) | 0x64006400u;
+  // (1024 + 16 code) / 16 - (64 + z); 0xd400 + 16 z is -(64 + z)
+  const uint32_t neg = ((zero & 0x000f000fu) << 4) | 0xd400d400u;
   uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(bits), "r"(z));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(bits), "r"(0x2c002c00u), "r"(neg));
   return d;
 }
+// 1024 + zero point in both halves: of the keys with scale words a (low) and b.
+__device__ __forceinline__ uint32_t int4_zero(uint32_t a, uint32_t b) {
+  return 0x64006400u | (a & 15u) | (b & 15u) << 16;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Bits of |x| if it is finite, else 0 (they order as the values do).
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
+  return b < 0x7f800000u ? b : 0u;
+}
+// Power of two that brings Q's largest value (its bits) to 2^14 .. 2^15, and its inverse.
+__device__ __forceinline__ float q_multiplier(uint32_t max_bits, float& inverse) {
+  const uint32_t e = max(max_bits >> 23, 20u);
+  inverse = __uint_as_float((e - 14u) << 23);
+  return __uint_as_float((268u - e) << 23);
+}
+// The same for V's scales, from the biased exponent of the largest: their
+// products with the multiplier stay below 2^7 (P itself is at most 2^8).
+constexpr uint32_t kMinScaleExp = 8;
+__device__ __forceinline__ float v_multiplier(uint32_t e) { return __uint_as_float((260u - e) << 23); }
+__device__ __forceinline__ float v_inverse(uint32_t e) { return __uint_as_float((e - 6u) << 23); }
 
 __device__ __forceinline__ bool not_finite2(uint32_t w) {  // either bf16 of a pair
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;

@@ -6,7 +6,7 @@
 // 4 R hd flop against 2 hd bits/8 bytes, so beyond some 140 rows of an e4m3
 // cache (280 of a bf16 one) the tensor pipe is the floor, below it HBM; in
 // between stands the work per score -- exp2, packing, and for 8- and 4-bit rows
-// the conversion to bf16 -- which needs every issue slot of the SM, so the
+// the conversion to fp16 -- which needs every issue slot of the SM, so the
 // kernel is built to keep all of these running at once.
 //
 // One block of 896 threads per SM, two streams of 128 query rows, tiles of 64
@@ -20,13 +20,13 @@
 //   warps 4-7    K loaders, warps 8-11 V loaders (neither waits for the other's
 //                stages): 16-byte asynchronous copies of cache rows; 8- and
 //                4-bit codes land in slots private to their thread, which
-//                turns them into the bf16 tile (no barrier in between)
+//                turns them into the fp16 tile (no barrier in between)
 //   warps 12-27  softmax, two threads per query row with 32 of 64 scores each;
 //                exponentials against the row's reference maximum, which
 //                moves only when a score exceeds it by 2^8: two warps agree
 //                on that with one barrier, and exchange maxima only when it does
-// The key's scales are applied to the scores (K) and to P (V): the bf16 tiles
-// hold the codes themselves, exactly.
+// The key's scales are applied to the scores (K) and to P (V): the tiles of 8-
+// and 4-bit rows hold the codes themselves, in fp16.
 //
 // Every wait is bounded; a wait that gives up sets the status word and the
 // block leaves in order.
@@ -82,17 +82,21 @@ struct TileCfg {
   // streams) the softmax is done with tile j - kKStages - 5; tile j + kRaw is
   // fetched next.
   static constexpr int kWordTiles = kKStages + kRaw + 5;
+  // A tile's words: factors of K (64), of V (64), and O's unit they are for.
+  static constexpr uint32_t kWordSlot = 528;
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = 2 * kQTile;
   static constexpr uint32_t kV = kK + kKStages * kTile;
   static constexpr uint32_t kRawAt = kV + kVStages * kTile;   // K's slots, then V's
   static constexpr uint32_t kWords = kRawAt + (kQuant ? 2 * kRaw * kUnit : 0u);
-  static constexpr uint32_t kZero = kWords + (kQuant ? kWordTiles * 512u : 0u);  // int4: own words
+  static constexpr uint32_t kZero = kWords + (kQuant ? kWordTiles * kWordSlot : 0u);  // int4: own words
   static constexpr uint32_t kZeroSlot = kPieces * kLoadThreads * 4u;
   static constexpr uint32_t kMask = kZero + (FMT == PDS_KV_INT4 ? 2 * kRaw * kZeroSlot : 0u);
   static constexpr uint32_t kPar = kMask + kMaskWords * 256u * 4u;
   static constexpr uint32_t kMax = kPar + kMaxDraftTokens * 4u;  // maxima of [stream][part][row]
-  static constexpr uint32_t kBar = kMax + 4u * 128u * 4u;
+  static constexpr uint32_t kQMax = kMax + 4u * 128u * 4u;       // Q's maximum per warp
+  static constexpr uint32_t kUnitAt = kQMax + 64u;               // O's unit of each stream
+  static constexpr uint32_t kBar = kUnitAt + 16u;
   static constexpr int kNumBars = 1 + 2 * (kKStages + kVStages) + 14;
   static constexpr uint32_t kMisc = kBar + 8u * kNumBars;
   static constexpr size_t kSmem = 1024 + kMisc + 96;
@@ -151,8 +155,9 @@ __device__ __forceinline__ void mma_commit(bool leader, uint32_t bar) {
       "r"(static_cast<uint32_t>(leader))
       : "memory");
 }
-__host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) |
+// kind::f16 with both operands bf16 or both fp16, float32 accumulator.
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn, bool bf16) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? (1u << 16) : 0u) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 // Byte offset of 8-channel piece c of row r in a swizzled bf16 tile of ROWS rows.
@@ -324,8 +329,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // One issuer per stream: their products interleave on the tensor pipe, so
       // one's waits cost the other nothing.  Per tile: S_i into the buffer that
       // P_{i-2} has left, then O += P_{i-1} V_{i-1} once the softmax has made P.
-      constexpr uint32_t kIdS = idesc(128, kKeys, false);
-      constexpr uint32_t kIdPV = idesc(128, HD, true);
+      constexpr uint32_t kIdS = idesc(128, kKeys, false, !C::kQuant);
+      constexpr uint32_t kIdPV = idesc(128, HD, true, !C::kQuant);
       const int s = warp, tiles = s == 0 ? n_tiles0 : n_tiles1;
       const bool leader = lane == 0;
       bool ok = true;
@@ -417,11 +422,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             copy4(zero0 + slot * C::kZeroSlot + i * (kLoadThreads * 4u),
                   (is_v ? a.c.v_scale : a.c.k_scale) + word0 + j, live);
         }
-        if (C::kQuant && !is_v) {  // the tile's scale words: K's, then V's
+        if (C::kQuant && !is_v) {  // the tile's scale words: K's by 64 threads, V's by 32
+          const uint32_t at = sbase + C::kWords + (t % C::kWordTiles) * C::kWordSlot;
           const int key = key0 + (tid & 63);
-          copy4(sbase + C::kWords + (t % C::kWordTiles) * 512u + tid * 4u,
-                (tid < 64 ? a.c.k_scale : a.c.v_scale) + word0 + (key < end ? key : end - 1),
-                key < end);
+          if (tid < 96)
+            copy4(at + tid * 4u, (tid < 64 ? a.c.k_scale : a.c.v_scale) + word0 +
+                                     (key < end ? key : end - 1), key < end);
+          if (tid >= 64 && tid < 96) {
+            const int next = key + 32;
+            copy4(at + (tid + 32) * 4u, a.c.v_scale + word0 + (next < end ? next : end - 1),
+                  next < end);
+          }
         }
       }
       copies_commit();
@@ -469,25 +480,38 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     } else {
       for (int t = 0; t < C::kRaw; ++t) issue(t, raw0 + t * C::kUnit, t);
       int st = 0, slot = 0;
-      uint32_t phase = 1;
+      uint32_t phase = 1, v_exp = kMinScaleExp;
+      float k_factor = a.scale_log2;
+      if (!is_v && n > 0) {  // Q's multiplier, once Q is there
+        wait(bar_q, 0);
+        uint32_t top = 0u;
+        const uint32_t* q_max = reinterpret_cast<const uint32_t*>(smem + C::kQMax);
+        for (int x = 0; x < kSoftmaxThreads / 32; ++x) top = max(top, q_max[x]);
+        float inverse;
+        q_multiplier(top, inverse);
+        k_factor *= inverse;
+      }
       for (int t = 0; t < n && ok; ++t) {
         copies_wait<C::kRaw - 1>();
         if (t >= stages) wait(empty0 + 8u * st, phase);
         if (!ok) break;
         const uint32_t src = raw0 + slot * C::kUnit;
         const uint32_t dst = tiles_at + st * C::kTile;
+        const int key0 = (u.first + t) * kKeys;
+        const bool clean = FMT == PDS_KV_E4M3 && is_v && part_hidden(a, key0, kKeys, len);
 #pragma unroll
         for (int i = 0; i < C::kPieces; ++i) {
           const int r = row0 + i * kRowStep;
           const uint4 x = lds128(src + i * (kLoadThreads * 16u));
-          const uint32_t c[4] = {x.x, x.y, x.z, x.w};
+          uint32_t c[4] = {x.x, x.y, x.z, x.w};
           if constexpr (FMT == PDS_KV_E4M3) {
+            if (clean) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) c[e] = e4m3_finite(c[e]);
+            }
             uint32_t y[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[2 * e] = e4m3_pair(__byte_perm(c[e], 0u, 0x1404));
-              y[2 * e + 1] = e4m3_pair(__byte_perm(c[e], 0u, 0x3424));
-            }
+            for (int e = 0; e < 4; ++e) e4m3_pairs(c[e], y[2 * e], y[2 * e + 1]);
             // the two halves in an order that keeps the lanes of a row on different banks
             const bool swap = col & (C::kPerRow >> 1);
             const uint32_t d0 = dst + tile_at<64>(r, 2 * col), d1 = dst + tile_at<64>(r, 2 * col + 1);
@@ -496,25 +520,42 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             st_shared_u4(swap ? d0 : d1, swap ? y[0] : y[4], swap ? y[1] : y[5],
                          swap ? y[2] : y[6], swap ? y[3] : y[7]);
           } else {
-            const uint32_t z = lds32(zero0 + slot * C::kZeroSlot + i * (kLoadThreads * 4u)) & 15u;
-            const uint32_t zz = 0x43004300u | z | z << 16;
+            // a word's 8 channels in the order 0 4 1 5 2 6 3 7 (Q's and O's are the same)
+            const uint32_t w = lds32(zero0 + slot * C::kZeroSlot + i * (kLoadThreads * 4u));
+            const uint32_t z = int4_zero(w, w);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t lo = c[e], hi = c[e] >> 4;
-              st_shared_u4(dst + tile_at<64>(r, 4 * col + e),
-                           int4_pair(__byte_perm(lo, hi, 0x0400), zz),
-                           int4_pair(__byte_perm(lo, hi, 0x0501), zz),
-                           int4_pair(__byte_perm(lo, hi, 0x0602), zz),
-                           int4_pair(__byte_perm(lo, hi, 0x0703), zz));
-            }
+            for (int e = 0; e < 4; ++e)
+              st_shared_u4(dst + tile_at<64>(r, 4 * col + e), int4_lo(c[e], z), int4_hi(c[e], z),
+                           int4_lo(c[e] >> 8, z), int4_hi(c[e] >> 8, z));
           }
         }
         if (!is_v) {
-          // the scale words as factors: of scores in powers of two, and of P
-          float* word = reinterpret_cast<float*>(smem + C::kWords + (t % C::kWordTiles) * 512u) + tid;
-          uint32_t bits = __float_as_uint(*word);
-          if (FMT == PDS_KV_INT4) bits &= 0xffff0000u;
-          *word = __uint_as_float(bits) * (tid < 64 ? a.scale_log2 : 1.0f);
+          // the scale words as factors: of scores in powers of two, and of P in
+          // O's unit, which grows with the largest V scale
+          float* word = reinterpret_cast<float*>(smem + C::kWords +
+                                                 (t % C::kWordTiles) * C::kWordSlot);
+          auto scale = [&](int x) {
+            const uint32_t bits = __float_as_uint(word[x]);
+            return __uint_as_float(FMT == PDS_KV_INT4 ? bits & 0xffff0000u : bits);
+          };
+          if (tid < 64) {
+            word[tid] = scale(tid) * k_factor;
+          } else if (tid < 96) {
+            const float v0 = scale(tid), v1 = scale(tid + 32);
+            auto exponent = [&](float v, int key) -> uint32_t {
+              // (a padding token's row is not written: it may hold any scale)
+              if (key >= len && key < end && a.parents &&
+                  a.parents[static_cast<int64_t>(u.seq) * a.n_tokens + key - len] < -1)
+                return 0u;
+              return finite_bits(v) >> 23;
+            };
+            v_exp = __reduce_max_sync(0xffffffffu, max(v_exp, max(exponent(v0, key0 + tid - 64),
+                                                                  exponent(v1, key0 + tid - 32))));
+            const float f = v_multiplier(v_exp);
+            word[tid] = v0 * f;
+            word[tid + 32] = v1 * f;
+            if (tid == 64) word[128] = __uint_as_float(v_exp);
+          }
         }
         arrive(full0 + 8u * st);
         issue(t + C::kRaw, src, slot);  // into the slot this thread has just emptied
@@ -543,23 +584,54 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (n > 0) {
       const int row = tid >> 1, R = r0 + row;
       constexpr int kPieces = HD / 16;
+      uint4 x[kPieces];
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c) x[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (R < rows && (two_tiles || row < 128)) {
+        const int t = R / a.group, i = R - t * a.group;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.q_stride +
+            (head * a.group + i) * HD) + (tid & 1) * kPieces;
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c) x[c] = src[c];
+      }
+      float q_mul = 1.f;
+      if constexpr (C::kQuant) {
+        uint32_t top = 0u;
+        auto both = [&](uint32_t w) {
+          top = max(top, max(finite_bits(__uint_as_float(w << 16)),
+                             finite_bits(__uint_as_float(w & 0xffff0000u))));
+        };
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c) both(x[c].x), both(x[c].y), both(x[c].z), both(x[c].w);
+        uint32_t* q_max = reinterpret_cast<uint32_t*>(smem + C::kQMax);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) q_max[warp - kFirstSoftmaxWarp] = top;
+        named_bar_sync(1, kSoftmaxThreads);
+        for (int c = 0; c < kSoftmaxThreads / 32; ++c) top = max(top, q_max[c]);
+        float inverse;
+        q_mul = q_multiplier(top, inverse);
+      }
       if (two_tiles || row < 128) {
-        uint4 x[kPieces];
 #pragma unroll
-        for (int c = 0; c < kPieces; ++c) x[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (R < rows) {
-          const int t = R / a.group, i = R - t * a.group;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.q_stride +
-              (head * a.group + i) * HD) + (tid & 1) * kPieces;
+        for (int c = 0; c < kPieces; ++c) {
+          uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+          if constexpr (C::kQuant) {
+            float f[8];
 #pragma unroll
-          for (int c = 0; c < kPieces; ++c) x[c] = src[c];
-        }
+            for (int e = 0; e < 4; ++e) {
+              f[2 * e] = __uint_as_float(w[e] << 16) * q_mul;
+              f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u) * q_mul;
+            }
 #pragma unroll
-        for (int c = 0; c < kPieces; ++c)
+            for (int e = 0; e < 4; ++e)
+              w[e] = FMT == PDS_KV_INT4 ? pack_f16x2(f[e], f[e + 4])
+                                        : pack_f16x2(f[2 * e], f[2 * e + 1]);
+          }
           st_shared_u4(sbase + C::kQ + (row >> 7) * C::kQTile +
                            tile_at<128>(row & 127, (tid & 1) * kPieces + c),
-                       x[c].x, x[c].y, x[c].z, x[c].w);
+                       w[0], w[1], w[2], w[3]);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -612,6 +684,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t pair_bar = 2u + s * 4u + (warp & 3);  // the two warps of these 32 rows
     float* xch_max = reinterpret_cast<float*>(smem + C::kMax);
     float m_ref = -INFINITY, l = 0.f;
+    uint32_t v_exp = kMinScaleExp;  // O's unit: the exponent of the largest V scale so far
     const int n_mine = s == 0 ? n_tiles0 : n_tiles1;
     const int tile_step = two_tiles ? 1 : 2;
     int slot = two_tiles ? 0 : s;                     // of the tile's scale words
@@ -624,7 +697,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // has given up (ok false: the work is skipped), so neither is left waiting.
     for (int i = 0; i < n_mine; ++i) {
       const int b = i & 1;
-      const uint32_t words = words0 + slot * 512u;
+      const uint32_t words = words0 + slot * C::kWordSlot;
       const int key = key0;
       slot += tile_step;
       if (slot >= C::kWordTiles) slot -= C::kWordTiles;
@@ -641,6 +714,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (partial) vis = visible32(key, len, lo, mask);
       float z[32];
       // scores less the reference, in powers of two; again if the reference moves
+      uint32_t unit = v_exp;
+      if constexpr (C::kQuant) unit = lds32(words - part * 128u + 512u);
       bool again = false;  // the same in both warps of the row
       for (;;) {
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // masked scores give 0
@@ -680,7 +755,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           break;
         }
         // (past this barrier both warps have read their scores: P may go over them)
-        const bool move = m_ref == -INFINITY ? mx > -INFINITY : mx > kMoveLog2;
+        const bool move = (m_ref == -INFINITY ? mx > -INFINITY : mx > kMoveLog2) || unit != v_exp;
         if (!named_bar_or(pair_bar, 64, ok && move)) break;
         again = true;
         xch_max[(2 * s + part) * 128 + r] = mx;
@@ -692,6 +767,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           alpha = exp2f(m_ref - m_new);  // 0 from -inf
           m_ref = m_new;
           l *= alpha;
+        }
+        if (C::kQuant) {
+          alpha *= v_multiplier(unit) * v_inverse(v_exp);
+          v_exp = unit;
         }
         if (i > 0) {
           // O at rest: the product of the tile before has completed
@@ -736,7 +815,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       float pk[16];
 #pragma unroll
-      for (int x = 0; x < 16; ++x) pk[x] = __uint_as_float(pack_bf16x2(z[2 * x], z[2 * x + 1]));
+      for (int x = 0; x < 16; ++x)
+        pk[x] = __uint_as_float(C::kQuant ? pack_f16x2(z[2 * x], z[2 * x + 1])
+                                          : pack_bf16x2(z[2 * x], z[2 * x + 1]));
       tmem_store16(ts + part * 16u, pk);
       tc_fence_before();
       __syncwarp();
@@ -754,6 +835,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // away.  Every product is done: the spaces of Q and K are free.
     float2* ml = reinterpret_cast<float2*>(smem + C::kK);  // [stream][part][row]
     ml[(2 * s + part) * 128 + r] = make_float2(m_ref, l);
+    // (a stream's warps all have the same unit, but for those without rows)
+    float* unit_of = reinterpret_cast<float*>(smem + C::kUnitAt);
+    const float my_unit = C::kQuant && n_mine > 0 ? v_inverse(v_exp) : 1.f;
+    if ((tid & 255) == 0) unit_of[s] = my_unit;
     const uint32_t xch = sbase + C::kQ;
     const uint32_t mine_at = static_cast<uint32_t>(r) * (HD * 2);
     auto xch_at = [&](int c4) {  // float4 c4 of the row's given half, spread over the banks
@@ -774,7 +859,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     }
     named_bar_sync(1, kSoftmaxThreads);
-    float mine_f = 1.f, other_f = 0.f;   // factors of this stream's O and of the other's
+    float mine_f = my_unit, other_f = 0.f;  // factors of this stream's O and of the other's
     int c0 = part * (HD / 2), c1 = c0 + HD / 2;  // this thread's columns
     l = ml[2 * s * 128 + r].y + ml[(2 * s + 1) * 128 + r].y;
     if (!two_tiles) {
@@ -785,6 +870,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       other_f = exp2f(x0.x - mu);
       // the first stream's share first, whichever thread adds
       l = s == 0 ? l * mine_f + l_other * other_f : l_other * other_f + l * mine_f;
+      mine_f *= my_unit;
+      other_f *= unit_of[1 - s];
       m_ref = m;
       c0 = s * (HD / 2) + part * (HD / 4);
       c1 = c0 + HD / 4;
@@ -815,6 +902,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               o[4 * x + e] = s == 0 ? mine_o + other_o : other_o + mine_o;
             }
           }
+        } else if (C::kQuant) {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[x] *= mine_f;
+        }
+        if constexpr (FMT == PDS_KV_INT4) {  // the channels back in their order
+          float y[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) y[x] = o[(x & 8) + ((x & 3) << 1) + ((x >> 2) & 1)];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[x] = y[x];
         }
         if constexpr (!C::kQuant) {
           if (*poison && row_live) {  // what the loaders took out, for the rows that see it
