@@ -111,19 +111,13 @@ struct Fmt {
   }
 
   // The contraction runs over the head's channels in an order that lets a lane
-  // read its share of a key's row with wide loads: the two pairs of channels
-  // (first, second operand register) of step ks for the lane's quarter t4.
-  static __device__ __forceinline__ void q_channels(int ks, int t4, int (&ch)[4]) {
-    if constexpr (FMT == PDS_KV_BF16) {
-      const int c = 8 * (t4 + 4 * (ks >> 1)) + 4 * (ks & 1);
-      ch[0] = c, ch[1] = c + 1, ch[2] = c + 2, ch[3] = c + 3;
-    } else if constexpr (FMT == PDS_KV_E4M3) {
-      const int c = 16 * (t4 + 4 * (ks >> 2)) + 4 * (ks & 3);
-      ch[0] = c, ch[1] = c + 1, ch[2] = c + 2, ch[3] = c + 3;
-    } else {
-      const int c = (HD / 4) * t4 + 8 * (ks >> 1) + 2 * (ks & 1);
-      ch[0] = c, ch[1] = c + 4, ch[2] = c + 1, ch[3] = c + 5;
-    }
+  // read its share of a key's row with wide loads: in step ks the lane's quarter
+  // t4 has the channels ch .. ch + 3 from this one on (4-bit rows: ch, ch + 4
+  // and ch + 1, ch + 5), two in each operand register.
+  static __device__ __forceinline__ int q_channel(int ks, int t4) {
+    if constexpr (FMT == PDS_KV_BF16) return 8 * (t4 + 4 * (ks >> 1)) + 4 * (ks & 1);
+    if constexpr (FMT == PDS_KV_E4M3) return 16 * (t4 + 4 * (ks >> 2)) + 4 * (ks & 3);
+    return (HD / 4) * t4 + 8 * (ks >> 1) + 2 * (ks & 1);
   }
   // Channel of row half hh (0: rows 0-7, 1: rows 8-15), lane group g, of
   // channel tile i of O^T.
@@ -319,24 +313,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
   const int head = p % a.c.n_kv_heads, tile = p / a.c.n_kv_heads;
   sm100::grid_dep_wait();  // everything below reads what earlier kernels wrote
   sm100::grid_dep_launch();
-  if (warp == 0) {
-    Unit u{};
-    const Lane mine = lane_steps(a, lane);
-    const int c = chunk_steps(a, lane, mine);
-    const bool ok = find_unit(a, c, w, 0, lane, mine, u);
-    if (lane == 0) {
-      *shared_unit = u;
-      *shared_ok = ok;
+  Unit u{};
+  if (a.c.n_seqs == 1) {
+    const bool ok = only_unit(a, w, u);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && u.n_chunks == 0)
+      atomicOr(a.status, kStatusBadLength);
+    if (!ok) return;
+  } else {
+    if (warp == 0) {
+      const Lane mine = lane_steps(a, lane);
+      const int c = chunk_steps(a, lane, mine);
+      const bool ok = find_unit(a, c, w, 0, lane, mine, u);
+      if (lane == 0) {
+        *shared_unit = u;
+        *shared_ok = ok;
+      }
+      if (blockIdx.x == 0) {  // report lengths that do not fit
+        bool bad = false;
+        for (int s = lane; s < a.c.n_seqs; s += 32) bad |= lane_steps(a, s).n == 0;
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kStatusBadLength);
+      }
     }
-    if (blockIdx.x == 0) {  // report lengths that do not fit
-      bool bad = false;
-      for (int s = lane; s < a.c.n_seqs; s += 32) bad |= lane_steps(a, s).n == 0;
-      if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kStatusBadLength);
-    }
+    __syncthreads();
+    if (!*shared_ok) return;
+    u = *shared_unit;
   }
-  __syncthreads();
-  if (!*shared_ok) return;
-  const Unit u = *shared_unit;
   const int r0 = tile * C::kRows;                        // first query row
   const int rows = a.n_tokens * a.group;
   const int end = u.len + a.n_tokens;                    // keys [.., end)
@@ -370,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
     }
     copies_commit();
   };
+#pragma unroll 1
   for (int i = 0; i < C::kStages - 1; ++i) fetch(i);
 
   // Q as B fragments, in the contraction's channel order; rows past the last are zero
@@ -387,10 +389,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
       const int t = r / a.group, i = r - t * a.group;
       const uint16_t* src = a.q + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.q_stride +
                             (head * a.group + i) * HD;
-      int ch[4];
-      F::q_channels(ks, l & 3, ch);
-      qb[it][0] = src[ch[0]] | static_cast<uint32_t>(src[ch[1]]) << 16;
-      qb[it][1] = src[ch[2]] | static_cast<uint32_t>(src[ch[3]]) << 16;
+      const int ch = F::q_channel(ks, l & 3);
+      if constexpr (FMT == PDS_KV_INT4) {  // channels (ch, ch + 4), (ch + 1, ch + 5)
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(src + ch);
+        const uint32_t y = *reinterpret_cast<const uint32_t*>(src + ch + 4);
+        qb[it][0] = __byte_perm(x, y, 0x5410);
+        qb[it][1] = __byte_perm(x, y, 0x7632);
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(src + ch);
+        qb[it][0] = x.x;
+        qb[it][1] = x.y;
+      }
     }
     if constexpr (!F::kBf16) {
 #pragma unroll
@@ -403,56 +412,49 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
     q_top = __reduce_max_sync(0xffffffffu, q_top);
     if (lane == 0) q_max[warp] = q_top;
   }
-  // depths of all tokens and ancestor sets of this tile's
+  // a tree's depths, and the ancestor sets of this tile's tokens
   const int t_first = r0 / a.group;
+  if (a.parents && threadIdx.x < a.n_tokens)
+    par[threadIdx.x] = a.parents[static_cast<int64_t>(u.seq) * a.n_tokens + threadIdx.x];
+  __syncthreads();
   float q_inv = 1.f;  // what a score is multiplied by besides K's scale
-  {
-    const int t = threadIdx.x;
-    if (a.parents && t < a.n_tokens)
-      par[t] = a.parents[static_cast<int64_t>(u.seq) * a.n_tokens + t];
-    const int tl = t - t_first;
-    const bool here = tl >= 0 && tl < C::kRows && t < a.n_tokens;
-    __syncthreads();
-    float q_mul = 1.f;
+  float q_mul = 1.f;
+  if constexpr (!F::kBf16) {
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) q_top = max(q_top, q_max[x]);
+    q_mul = q_multiplier(q_top, q_inv);
+  }
+#pragma unroll
+  for (int it = 0; it < kQIters; ++it) {
+    const int idx = it * kThreads + threadIdx.x;
     if constexpr (!F::kBf16) {
 #pragma unroll
-      for (int x = 0; x < kWarps; ++x) q_top = max(q_top, q_max[x]);
-      q_mul = q_multiplier(q_top, q_inv);
+      for (int e = 0; e < 2; ++e)
+        qb[it][e] = pack_f16x2(__uint_as_float(qb[it][e] << 16) * q_mul,
+                               __uint_as_float(qb[it][e] & 0xffff0000u) * q_mul);
     }
+    if (idx < kQFrags)
+      *reinterpret_cast<uint2*>(smem + C::kQ + idx * 8) = make_uint2(qb[it][0], qb[it][1]);
+  }
+  if (a.parents && threadIdx.x < a.n_tokens) {
+    const int t = threadIdx.x, d = tree_depth(par, t), tl = t - t_first;
+    depth[t] = static_cast<int16_t>(d);
+    if (d == kBadParent) atomicOr(a.status, kStatusBadParent);
+    if (tl >= 0 && tl < C::kRows) {
+      uint32_t bits[kMaskWords];
 #pragma unroll
-    for (int it = 0; it < kQIters; ++it) {
-      const int idx = it * kThreads + threadIdx.x;
-      if constexpr (!F::kBf16) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          qb[it][e] = pack_f16x2(__uint_as_float(qb[it][e] << 16) * q_mul,
-                                 __uint_as_float(qb[it][e] & 0xffff0000u) * q_mul);
-      }
-      if (idx < kQFrags)
-        *reinterpret_cast<uint2*>(smem + C::kQ + idx * 8) = make_uint2(qb[it][0], qb[it][1]);
-    }
-    if (t < a.n_tokens) {
-      const int d = a.parents ? tree_depth(par, t) : t;
-      depth[t] = static_cast<int16_t>(d);
-      if (d == kBadParent) atomicOr(a.status, kStatusBadParent);
-      if (here) {
-        uint32_t bits[kMaskWords];
+      for (int i = 0; i < kMaskWords; ++i) bits[i] = 0u;
+      int x = t;
+      for (int e = 0; e <= d; ++e, x = par[x])
 #pragma unroll
         for (int i = 0; i < kMaskWords; ++i)
-          bits[i] = a.parents || t < 32 * i ? 0u
-                    : t >= 32 * i + 31       ? 0xffffffffu
-                                             : (2u << (t - 32 * i)) - 1u;
-        if (a.parents && d >= 0)
-          for (int x = t; x >= 0; x = par[x])
+          if ((x >> 5) == i) bits[i] |= 1u << (x & 31);
 #pragma unroll
-            for (int i = 0; i < kMaskWords; ++i)
-              if ((x >> 5) == i) bits[i] |= 1u << (x & 31);
-#pragma unroll
-        for (int i = 0; i < kMaskWords; ++i) mask[tl * kMaskWords + i] = bits[i];
-      }
+      for (int i = 0; i < kMaskWords; ++i) mask[tl * kMaskWords + i] = bits[i];
     }
   }
   __syncthreads();
+  auto depth_of = [&](int t) -> int { return a.parents ? depth[t] : t; };
 
   // this lane's rows: 8 n + 2 t4 + {0, 1}; their tokens (within the tile) and positions
   int tok[NT][2], pos[NT][2];
@@ -463,8 +465,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
     for (int e = 0; e < 2; ++e) {
       const int r = r0 + 8 * n + 2 * t4 + e;
       const int t = r < rows ? r / a.group : -1;
-      tok[n][e] = t < 0 || depth[t] < 0 ? -1 : t - t_first;
-      pos[n][e] = u.len + (t < 0 ? 0 : depth[t]);
+      const int d = t < 0 ? -1 : depth_of(t);
+      tok[n][e] = d < 0 ? -1 : t - t_first;
+      pos[n][e] = u.len + d;
       pos_hi = max(pos_hi, pos[n][e]);
     }
   if (VAR) pos_hi = __reduce_max_sync(0xffffffffu, pos_hi);
@@ -538,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int j = j0 + g + 8 * e, rel = j - u.len;
-        const int key_pos = rel < 0 ? j : u.len + (rel < a.n_tokens ? depth[rel] : 0);
+        const int key_pos = rel < 0 || rel >= a.n_tokens ? j : u.len + depth_of(rel);
         seen[e] = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -547,7 +550,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
             const int t = tok[n][x];
             bool see = t >= 0;
             if (see && rel >= 0)
-              see = rel < a.n_tokens && ((mask[t * kMaskWords + (rel >> 5)] >> (rel & 31)) & 1u);
+              see = a.parents ? rel < a.n_tokens &&
+                                    ((mask[t * kMaskWords + (rel >> 5)] >> (rel & 31)) & 1u)
+                              : rel <= t + t_first;
             if (VAR && a.window > 0) see = see && key_pos > pos[n][x] - a.window;
             if (!see) s[n][2 * e + x] = -INFINITY;
             seen[e] |= see;
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 #pragma unroll
           for (int sh = 4; sh < 32; sh <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
           if (m > m_ref[n][x] + kMoveLog2) {
-            const float alpha = exp2f(m_ref[n][x] - m);  // 0 from -inf
+            const float alpha = exp2_fast(m_ref[n][x] - m);  // 0 from -inf
             m_ref[n][x] = m;
             l[n][x] *= alpha;
 #pragma unroll
@@ -713,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 #pragma unroll
     for (int x = 0; x < kWarps; ++x) {
       const float2 v = ml[x * C::kRows + r];
-      const float f = exp2f(v.x - mu);  // 0 for a warp that saw none of the row's keys
+      const float f = exp2_fast(v.x - mu);  // 0 for a warp that saw none of the row's keys
       const float4 y = *reinterpret_cast<const float4*>(join + (x * C::kRows + r) * C::kJoinStride + ch);
       const float fo = f * unit[x];
       sum += v.y * f;
@@ -722,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
       acc.z += y.z * fo;
       acc.w += y.w * fo;
     }
-    if (depth[t] < 0) {  // a padding token's rows went along with the others
+    if (depth_of(t) < 0) {  // a padding token's rows went along with the others
       m = -INFINITY;
       sum = 0.f;
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -753,65 +758,68 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
   __shared__ float part_o[8][HD];
   __shared__ float2 part_ml[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (8 / kShare) + warp / kShare;
+  const int row = blockIdx.x * (8 / kShare) + warp / kShare;
   const int per_seq = a.n_tokens * a.n_heads;
-  const int64_t seq64 = row / per_seq;
+  const int seq = row / per_seq, rest = row - seq * per_seq;
+  const int t = rest / a.n_heads, h = rest - t * a.n_heads;
+  const int head = h / a.group, r = t * a.group + h - head * a.group;
+  const int tile = r / a.tile_rows;
+  const int per = a.c.n_kv_heads * a.row_tiles;
+  const int64_t stride = static_cast<int64_t>(per) * a.tile_rows;
   Unit u{};
-  if (seq64 < a.c.n_seqs) {
+  if (a.c.n_seqs == 1) {
+    only_unit(a, -1, u);
+  } else if (seq < a.c.n_seqs) {
     const Lane mine = lane_steps(a, lane);
-    find_unit(a, chunk_steps(a, lane, mine), -1, static_cast<int>(seq64), lane, mine, u);
+    find_unit(a, chunk_steps(a, lane, mine), -1, seq, lane, mine, u);
   }
+  // written by its block, or refused, or no such row
+  const bool live = seq < a.c.n_seqs && u.n_chunks > 1;
+  const int n_chunks = live ? u.n_chunks : 0;
+  const int64_t slot0 = (static_cast<int64_t>(u.base) * per + tile * a.c.n_kv_heads + head) *
+                            a.tile_rows + (r - tile * a.tile_rows) + (warp % kShare) * stride;
+  const float2* ml = a.ml_part + slot0;
+  const float* src = a.o_part + slot0 * HD + lane * kPer;
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
-  const bool live = u.n_chunks > 1;  // else written by its block, or refused, or no such row
-  const int seq = u.seq, rest = static_cast<int>(row - seq64 * per_seq);
-  const int t = rest / a.n_heads, h = rest - t * a.n_heads;
   float acc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
   float sum = 0.f, m = -INFINITY;
-  if (live) {
-    const int head = h / a.group, r = t * a.group + h - head * a.group;
-    const int tile = r / a.tile_rows;
-    const int per = a.c.n_kv_heads * a.row_tiles;
-    const int64_t first = (static_cast<int64_t>(u.base) * per + tile * a.c.n_kv_heads + head) *
-                              a.tile_rows + (r - tile * a.tile_rows);
-    const int64_t stride = static_cast<int64_t>(per) * a.tile_rows;
-    for (int x0 = warp % kShare; x0 < u.n_chunks; x0 += kBatch * kShare) {
-      float2 v[kBatch];
-      float y[kBatch][kPer];
+#pragma unroll 1
+  for (int x0 = warp % kShare; x0 < n_chunks; x0 += kBatch * kShare) {
+    float2 v[kBatch];
+    float y[kBatch][kPer];
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        const bool have = x0 + x * kShare < u.n_chunks;
-        const int64_t slot = first + (have ? x0 + x * kShare : x0) * stride;
-        v[x] = __ldcg(a.ml_part + slot);
-        if (!have) v[x] = make_float2(-INFINITY, 0.f);
-        const float* src = a.o_part + slot * HD + lane * kPer;
-        if constexpr (kPer == 4) {
-          const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-          y[x][0] = f.x, y[x][1] = f.y, y[x][2] = f.z, y[x][3] = f.w;
-        } else {
-          const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-          y[x][0] = f.x, y[x][1] = f.y;
-        }
+    for (int x = 0; x < kBatch; ++x) {
+      const bool have = x0 + x * kShare < n_chunks;
+      v[x] = have ? __ldcg(ml) : make_float2(-INFINITY, 0.f);
+      if constexpr (kPer == 4) {
+        const float4 f = have ? __ldcg(reinterpret_cast<const float4*>(src))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        y[x][0] = f.x, y[x][1] = f.y, y[x][2] = f.z, y[x][3] = f.w;
+      } else {
+        const float2 f = have ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
+        y[x][0] = f.x, y[x][1] = f.y;
       }
-      float m_new = m;
+      ml += kShare * stride;
+      src += kShare * stride * HD;
+    }
+    float m_new = m;
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) m_new = fmaxf(m_new, v[x].x);
-      const float mu = m_new == -INFINITY ? 0.f : m_new;
-      const float old = exp2f(m - mu);
-      m = m_new;
-      sum *= old;
+    for (int x = 0; x < kBatch; ++x) m_new = fmaxf(m_new, v[x].x);
+    const float mu = m_new == -INFINITY ? 0.f : m_new;
+    const float old = exp2_fast(m - mu);
+    m = m_new;
+    sum *= old;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] *= old;
+    for (int i = 0; i < kPer; ++i) acc[i] *= old;
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        if (x0 + x * kShare >= u.n_chunks) break;
-        const float f = exp2f(v[x].x - mu);
-        sum += v[x].y * f;
+    for (int x = 0; x < kBatch; ++x) {
+      const float f = exp2_fast(v[x].x - mu);  // 0 where there is none
+      sum += v[x].y * f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] += y[x][i] * f;
-      }
+      for (int i = 0; i < kPer; ++i) acc[i] += y[x][i] * f;
     }
   }
 #pragma unroll
@@ -828,7 +836,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
 #pragma unroll
   for (int x = 0; x < kShare; ++x) {
     const float2 v = part_ml[warp + x];
-    const float f = exp2f(v.x - mu);
+    const float f = exp2_fast(v.x - mu);
     sum += v.y * f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) acc[i] += part_o[warp + x][lane * kPer + i] * f;
@@ -955,6 +963,7 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
   if (t.ws && most_chunks > 1) {
     a.slots = s.slots;
     a.fit = s.fit;
+    a.per_chunk = 1.0f / static_cast<float>(s.slots / s.per);
     const int64_t most = max_units(s, c.n_seqs);
     grid = std::min(most, units * most_chunks);
     a.o_part = reinterpret_cast<float*>(t.ws);

@@ -30,6 +30,7 @@ struct Args {
   int tile_rows;                 // rows of one
   int slots;                     // blocks to spread the chunks over; 0: one chunk each
   int fit;                       // 1: choose chunks so that all units run at once
+  float per_chunk;               // n_seqs == 1: 1 / (chunks that fit the slots)
   int min_steps;                 // shortest chunk, in steps
   float* o_part;                 // [unit][tile_rows][hd], each kernel in its own order
   float2* ml_part;               // [unit][tile_rows]: (maximum, sum)
@@ -99,6 +100,27 @@ struct Unit {
   int seq, chunk, n_chunks, first, n_steps, len;  // steps [first, first + n_steps)
   int base;  // (chunk 0 of the sequence) among all chunks
 };
+
+// One sequence: its chunks by a few instructions, in every thread.
+__device__ __forceinline__ bool only_unit(const Args& a, int w, Unit& u) {
+  int first, len;
+  const int n = seq_steps(a, 0, first, len);
+  int c = n;
+  if (a.slots > 0) {
+    const int most = a.slots / (a.c.n_kv_heads * a.row_tiles);
+    c = static_cast<int>(static_cast<float>(n) * a.per_chunk) + 1;
+    if (static_cast<long long>(c) * most < n) ++c;  // (the quotient was rounded)
+    c = max(c, a.min_steps);
+  }
+  u.seq = 0;
+  u.len = len;
+  u.base = 0;
+  u.n_chunks = n == 0 ? 0 : static_cast<int>(static_cast<unsigned>(n - 1) / static_cast<unsigned>(c)) + 1;
+  u.chunk = max(w, 0);
+  u.first = first + u.chunk * c;
+  u.n_steps = min(c, n - u.chunk * c);
+  return u.chunk < u.n_chunks;
+}
 
 // The sequence and chunk of the w-th chunk overall (w < 0: of sequence `seq`,
 // whole range).  False past the last one.  By one warp; every lane returns it.

@@ -297,9 +297,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   grid_dep_launch();
   if (warp == 0) {
     Unit u{};
-    const Lane mine = lane_steps(a, lane);
-    const int c = chunk_steps(a, lane, mine);
-    const bool ok = find_unit(a, c, w, 0, lane, mine, u);
+    bool ok;
+    if (a.c.n_seqs == 1) {
+      ok = only_unit(a, w, u);
+    } else {
+      const Lane mine = lane_steps(a, lane);
+      ok = find_unit(a, chunk_steps(a, lane, mine), w, 0, lane, mine, u);
+    }
     if (lane == 0) {
       *shared_unit = u;
       *shared_ok = ok;
@@ -764,7 +768,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         float alpha = 1.f;
         if (m_ref == -INFINITY ? mx > -INFINITY : mx > kMoveLog2) {
           const float m_new = m_use + mx;
-          alpha = exp2f(m_ref - m_new);  // 0 from -inf
+          alpha = exp2_fast(m_ref - m_new);  // 0 from -inf
           m_ref = m_new;
           l *= alpha;
         }
@@ -866,8 +870,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const float2 x0 = ml[2 * (1 - s) * 128 + r];
       const float l_other = x0.y + ml[(2 * (1 - s) + 1) * 128 + r].y;
       const float m = fmaxf(m_ref, x0.x), mu = m == -INFINITY ? 0.f : m;
-      mine_f = exp2f(m_ref - mu);
-      other_f = exp2f(x0.x - mu);
+      mine_f = exp2_fast(m_ref - mu);
+      other_f = exp2_fast(x0.x - mu);
       // the first stream's share first, whichever thread adds
       l = s == 0 ? l * mine_f + l_other * other_f : l_other * other_f + l * mine_f;
       mine_f *= my_unit;
@@ -975,8 +979,12 @@ __global__ void __launch_bounds__(256) cache_join_tile_kernel(const __grid_const
   const int head = p % a.c.n_kv_heads, group_tile = p / a.c.n_kv_heads;
   if (threadIdx.x < 32) {
     Unit u{};
-    const Lane mine = lane_steps(a, lane);
-    find_unit(a, chunk_steps(a, lane, mine), -1, seq, lane, mine, u);
+    if (a.c.n_seqs == 1) {
+      only_unit(a, -1, u);
+    } else {
+      const Lane mine = lane_steps(a, lane);
+      find_unit(a, chunk_steps(a, lane, mine), -1, seq, lane, mine, u);
+    }
     if (lane == 0) shared_unit = u;
   }
   __syncthreads();
@@ -1012,7 +1020,7 @@ __global__ void __launch_bounds__(256) cache_join_tile_kernel(const __grid_const
 #pragma unroll
     for (int x = 0; x < kBatch; ++x) m_new = fmaxf(m_new, v[x].x);
     const float mu = m_new == -INFINITY ? 0.f : m_new;
-    const float old = exp2f(m - mu);
+    const float old = exp2_fast(m - mu);
     m = m_new;
     sum *= old;
 #pragma unroll
@@ -1020,7 +1028,7 @@ __global__ void __launch_bounds__(256) cache_join_tile_kernel(const __grid_const
 #pragma unroll
     for (int x = 0; x < kBatch; ++x) {
       if (x0 + x >= n_chunks) break;
-      const float f = exp2f(v[x].x - mu);
+      const float f = exp2_fast(v[x].x - mu);
       sum += v[x].y * f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
