@@ -9,7 +9,7 @@
 // the conversion to fp16 -- which needs every issue slot of the SM, so the
 // kernel is built to keep all of these running at once.
 //
-// One block of 896 threads per SM, two streams of 128 query rows, tiles of 64
+// One block of 640 threads per SM, two streams of 128 query rows, tiles of 64
 // keys: with more than 128 rows the streams are two row tiles that share every
 // K/V tile, else they are the even and the odd key tiles of one row tile.
 // While one stream's softmax runs, the tensor pipe works for the other, and
@@ -21,10 +21,9 @@
 //                stages): 16-byte asynchronous copies of cache rows; 8- and
 //                4-bit codes land in slots private to their thread, which
 //                turns them into the fp16 tile (no barrier in between)
-//   warps 12-27  softmax, two threads per query row with 32 of 64 scores each;
-//                exponentials against the row's reference maximum, which
-//                moves only when a score exceeds it by 2^8: two warps agree
-//                on that with one barrier, and exchange maxima only when it does
+//   warps 12-19  softmax, one thread per query row (so nothing is exchanged):
+//                64 scores at a time, exponentials against the row's reference
+//                maximum, which moves only when a score exceeds it by 2^8
 // The key's scales are applied to the scores (K) and to P (V): the tiles of 8-
 // and 4-bit rows hold the codes themselves, in fp16.
 //
@@ -51,13 +50,13 @@ constexpr int kKeys = 64;              // keys per tile
 constexpr int kTileRows = 128;         // query rows per stream
 constexpr int kLoadWarps = 4, kLoadThreads = 32 * kLoadWarps;  // of K, and of V
 constexpr int kFirstLoadWarp = 4, kFirstSoftmaxWarp = kFirstLoadWarp + 2 * kLoadWarps;
-constexpr int kSoftmaxThreads = 512;   // 2 streams x 2 threads per row x 128 rows
+constexpr int kSoftmaxThreads = 256;   // 2 streams x 128 rows
 constexpr int kTileThreads = 32 * kFirstSoftmaxWarp + kSoftmaxThreads;
 constexpr float kMoveLog2 = 8.0f;      // the reference maximum follows beyond a growth of 2^8
-// registers per thread: 72 at launch; 384 threads give up 24 each for the 512
-// softmax threads' 16 more
-constexpr int kLeanRegs = 48, kSoftmaxRegs = 88;
-static_assert(kTileThreads * 72 >= 384 * kLeanRegs + kSoftmaxThreads * kSoftmaxRegs,
+// registers per thread: 96 at launch; 384 threads give up 32 each for the 256
+// softmax threads' 48 more
+constexpr int kLeanRegs = 64, kSoftmaxRegs = 144;
+static_assert(kTileThreads * 96 >= 384 * kLeanRegs + kSoftmaxThreads * kSoftmaxRegs,
               "register split");
 
 template <int FMT, int HD>
@@ -93,9 +92,8 @@ struct TileCfg {
   static constexpr uint32_t kZeroSlot = kPieces * kLoadThreads * 4u;
   static constexpr uint32_t kMask = kZero + (FMT == PDS_KV_INT4 ? 2 * kRaw * kZeroSlot : 0u);
   static constexpr uint32_t kPar = kMask + kMaskWords * 256u * 4u;
-  static constexpr uint32_t kMax = kPar + kMaxDraftTokens * 4u;  // maxima of [stream][part][row]
-  static constexpr uint32_t kQMax = kMax + 4u * 128u * 4u;       // Q's maximum per warp
-  static constexpr uint32_t kUnitAt = kQMax + 64u;               // O's unit of each stream
+  static constexpr uint32_t kQMax = kPar + kMaxDraftTokens * 4u;  // Q's maximum per warp
+  static constexpr uint32_t kUnitAt = kQMax + 64u;                // O's unit of each stream
   static constexpr uint32_t kBar = kUnitAt + 16u;
   static constexpr int kNumBars = 1 + 2 * (kKStages + kVStages) + 14;
   static constexpr uint32_t kMisc = kBar + 8u * kNumBars;
@@ -182,18 +180,30 @@ __device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(d));
 }
-// Barrier `id` over `count` threads; whether any of them came with `flag`.
-__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t count, bool flag) {
-  uint32_t r;
+// 64 consecutive float32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_load64(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(flag))
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]),
+        "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]),
+        "=r"(r[63])
+      : "r"(taddr)
       : "memory");
-  return r != 0;
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ float max32(const float* v) {
   float a[11];
@@ -280,7 +290,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int s = 0; s < 2; ++s) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(bar_s_full(s, b), 1);
-        mbar_init(bar_p_full(s, b), 8);  // one arrival per softmax warp
+        mbar_init(bar_p_full(s, b), 4);  // one arrival per softmax warp
         mbar_init(bar_pv(s, b), 1);
       }
       mbar_init(bar_done(s), 1);
@@ -571,8 +581,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else {
     setmaxnreg_inc<kSoftmaxRegs>();
     const int tid = threadIdx.x - 32 * kFirstSoftmaxWarp;
-    const int s = tid >> 8;                       // stream
-    const int part = (tid >> 7) & 1;              // which 32 of 64 keys
+    const int s = tid >> 7;                       // stream
     const int r = tid & 127;                      // row of the stream's tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t to = tmem + lane_off + C::kTmO + s * 128u;
@@ -584,21 +593,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (ok) tc_fence_after();
     };
-    // Q: two threads per row of the (one or two) tiles, half a row each
+    // Q: one or two tiles, in pieces of half a row per thread and round
     if (n > 0) {
-      const int row = tid >> 1, R = r0 + row;
       constexpr int kPieces = HD / 16;
+      const int rounds = two_tiles ? 2 : 1;
       uint4 x[kPieces];
+      auto load = [&](int round) {
+        const int row = round * 128 + (tid >> 1), R = r0 + row;
 #pragma unroll
-      for (int c = 0; c < kPieces; ++c) x[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (R < rows && (two_tiles || row < 128)) {
-        const int t = R / a.group, i = R - t * a.group;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.q_stride +
-            (head * a.group + i) * HD) + (tid & 1) * kPieces;
+        for (int c = 0; c < kPieces; ++c) x[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (R < rows) {
+          const int t = R / a.group, i = R - t * a.group;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              a.q + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.q_stride +
+              (head * a.group + i) * HD) + (tid & 1) * kPieces;
 #pragma unroll
-        for (int c = 0; c < kPieces; ++c) x[c] = src[c];
-      }
+          for (int c = 0; c < kPieces; ++c) x[c] = src[c];
+        }
+      };
       float q_mul = 1.f;
       if constexpr (C::kQuant) {
         uint32_t top = 0u;
@@ -606,8 +618,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           top = max(top, max(finite_bits(__uint_as_float(w << 16)),
                              finite_bits(__uint_as_float(w & 0xffff0000u))));
         };
+#pragma unroll 1
+        for (int round = rounds - 1; round >= 0; --round) {  // (round 0 stays loaded)
+          load(round);
 #pragma unroll
-        for (int c = 0; c < kPieces; ++c) both(x[c].x), both(x[c].y), both(x[c].z), both(x[c].w);
+          for (int c = 0; c < kPieces; ++c) both(x[c].x), both(x[c].y), both(x[c].z), both(x[c].w);
+        }
         uint32_t* q_max = reinterpret_cast<uint32_t*>(smem + C::kQMax);
         top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) q_max[warp - kFirstSoftmaxWarp] = top;
@@ -616,7 +632,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         float inverse;
         q_mul = q_multiplier(top, inverse);
       }
-      if (two_tiles || row < 128) {
+#pragma unroll 1
+      for (int round = 0; round < rounds; ++round) {
+        if (!C::kQuant || round > 0) load(round);
 #pragma unroll
         for (int c = 0; c < kPieces; ++c) {
           uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
@@ -632,8 +650,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               w[e] = FMT == PDS_KV_INT4 ? pack_f16x2(f[e], f[e + 4])
                                         : pack_f16x2(f[2 * e], f[2 * e + 1]);
           }
-          st_shared_u4(sbase + C::kQ + (row >> 7) * C::kQTile +
-                           tile_at<128>(row & 127, (tid & 1) * kPieces + c),
+          st_shared_u4(sbase + C::kQ + round * C::kQTile +
+                           tile_at<128>(tid >> 1, (tid & 1) * kPieces + c),
                        w[0], w[1], w[2], w[3]);
         }
       }
@@ -656,7 +674,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       depth = tree_depth(par, tok);
       if (depth == kBadParent && row_live) atomicOr(a.status, kStatusBadParent);
     }
-    if (part == 0) {
+    {
       uint32_t bits[kMaskWords];
 #pragma unroll
       for (int i = 0; i < kMaskWords; ++i) bits[i] = 0u;
@@ -678,93 +696,80 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
 #pragma unroll
-      for (int i = 0; i < kMaskWords; ++i) mask[i * 256] = bits[i];
+      for (int i = 0; i < kMaskWords; ++i) mask[i * 256] = bits[i];  // (read by this thread alone)
     }
-    named_bar_sync(1, kSoftmaxThreads);
     const int lo = VAR && a.window > 0 ? len + depth - a.window + 1 : 0;
 
     const bool warp_live = r0 + (two_tiles ? s * kTileRows : 0) + (warp & 3) * 32 < rows;
     const float sc = a.scale_log2, cap = VAR ? a.cap * a.scale_log2 : 0.f;  // powers of two
-    const uint32_t pair_bar = 2u + s * 4u + (warp & 3);  // the two warps of these 32 rows
-    float* xch_max = reinterpret_cast<float*>(smem + C::kMax);
     float m_ref = -INFINITY, l = 0.f;
     uint32_t v_exp = kMinScaleExp;  // O's unit: the exponent of the largest V scale so far
     const int n_mine = s == 0 ? n_tiles0 : n_tiles1;
     const int tile_step = two_tiles ? 1 : 2;
     int slot = two_tiles ? 0 : s;                     // of the tile's scale words
-    int key0 = (u.first + slot) * kKeys + part * 32;  // this thread's first key of the tile
-    const uint32_t words0 = sbase + C::kWords + part * 128u;
-    // keys below the one and from the other on are hidden from some rows
+    int key0 = (u.first + slot) * kKeys;              // the tile's first key
+    // tiles from a key below the one, or above the other, on hold rows that are
+    // hidden from some
     const int hide_lo = VAR && a.window > 0 ? len + a.n_tokens - a.window : 0;
-    const int hide_hi = len - 32;
-    // Both warps of a row pass its barriers for every tile, even after a wait
-    // has given up (ok false: the work is skipped), so neither is left waiting.
+    const int hide_hi = len - kKeys;
     for (int i = 0; i < n_mine; ++i) {
       const int b = i & 1;
-      const uint32_t words = words0 + slot * C::kWordSlot;
+      const uint32_t words = sbase + C::kWords + slot * C::kWordSlot;
       const int key = key0;
       slot += tile_step;
       if (slot >= C::kWordTiles) slot -= C::kWordTiles;
       key0 += tile_step * kKeys;
       wait(bar_s_full(s, b), (i >> 1) & 1);
+      if (!ok) break;
       if (!warp_live) {
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bar_p_full(s, b));
+        if (lane == 0) mbar_arrive(bar_p_full(s, b));
         continue;
       }
       const uint32_t ts = tmem + lane_off + C::kTmS + s * 128u + b * 64u;
       const bool partial = key > hide_hi || key < hide_lo;
-      uint32_t vis = 0xffffffffu;
-      if (partial) vis = visible32(key, len, lo, mask);
-      float z[32];
-      // scores less the reference, in powers of two; again if the reference moves
+      uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
+      if (partial) {
+        vis[0] = visible32(key, len, lo, mask);
+        vis[1] = visible32(key + 32, len, lo, mask);
+      }
       uint32_t unit = v_exp;
-      if constexpr (C::kQuant) unit = lds32(words - part * 128u + 512u);
-      bool again = false;  // the same in both warps of the row
-      for (;;) {
+      if constexpr (C::kQuant) unit = lds32(words + 512u);
+      float z[kKeys];
+      // scores less the reference, in powers of two; again if the reference moves
+      for (bool again = false;; again = true) {
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // masked scores give 0
-        float mx = -INFINITY;
-        if (ok) {
-          tmem_load32(ts + part * 32u, z);
-          if (VAR && cap > 0.f) {
+        tmem_load64(ts, z);
+        if (VAR && cap > 0.f) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              float f = sc;
-              if constexpr (C::kQuant) f = __uint_as_float(lds32(words + x * 4));
-              // c tanh(z / c) = c - 2 c / (2^(2 log2(e) z / c) + 1)
-              const float y = z[x] * f;
-              const float e = exp2_fast(y * (2.0f * 1.4426950408889634f / cap));
-              z[x] = cap - __fdividef(2.0f * cap, e + 1.0f) - m_use;
-            }
-          } else if constexpr (C::kQuant) {
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              const float4 f = ld_shared_f4(words + x * 16);
-              fma2_pair(z[4 * x], z[4 * x + 1], f.x, f.y, -m_use);
-              fma2_pair(z[4 * x + 2], z[4 * x + 3], f.z, f.w, -m_use);
-            }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 16; ++x) fma2(z[2 * x], z[2 * x + 1], sc, -m_use);
+          for (int x = 0; x < kKeys; ++x) {
+            float f = sc;
+            if constexpr (C::kQuant) f = __uint_as_float(lds32(words + x * 4));
+            // c tanh(z / c) = c - 2 c / (2^(2 log2(e) z / c) + 1)
+            const float y = z[x] * f;
+            const float e = exp2_fast(y * (2.0f * 1.4426950408889634f / cap));
+            z[x] = cap - __fdividef(2.0f * cap, e + 1.0f) - m_use;
           }
-          if (partial) {
+        } else if constexpr (C::kQuant) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!((vis >> x) & 1u)) z[x] = -INFINITY;
+          for (int x = 0; x < kKeys / 4; ++x) {
+            const float4 f = ld_shared_f4(words + x * 16);
+            fma2_pair(z[4 * x], z[4 * x + 1], f.x, f.y, -m_use);
+            fma2_pair(z[4 * x + 2], z[4 * x + 3], f.z, f.w, -m_use);
           }
-          mx = max32(z);
+        } else {
+#pragma unroll
+          for (int x = 0; x < kKeys / 2; ++x) fma2(z[2 * x], z[2 * x + 1], sc, -m_use);
         }
-        if (again) {
-          named_bar_sync(pair_bar, 64);  // both have read their scores once more
-          break;
+        if (partial) {
+#pragma unroll
+          for (int x = 0; x < kKeys; ++x)
+            if (!((vis[x >> 5] >> (x & 31)) & 1u)) z[x] = -INFINITY;
         }
-        // (past this barrier both warps have read their scores: P may go over them)
+        if (again) break;
+        const float mx = fmaxf(max32(z), max32(z + 32));
         const bool move = (m_ref == -INFINITY ? mx > -INFINITY : mx > kMoveLog2) || unit != v_exp;
-        if (!named_bar_or(pair_bar, 64, ok && move)) break;
-        again = true;
-        xch_max[(2 * s + part) * 128 + r] = mx;
-        named_bar_sync(pair_bar, 64);
-        mx = fmaxf(mx, xch_max[(2 * s + 1 - part) * 128 + r]);
+        if (!__any_sync(0xffffffffu, move)) break;
         float alpha = 1.f;
         if (m_ref == -INFINITY ? mx > -INFINITY : mx > kMoveLog2) {
           const float m_new = m_use + mx;
@@ -779,50 +784,48 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (i > 0) {
           // O at rest: the product of the tile before has completed
           wait(bar_pv(s, b ^ 1), ((i - 1) >> 1) & 1);
-          if (ok) {
+          if (!ok) break;
 #pragma unroll 1
-            for (int c = 0; c < HD / 32; ++c) {
-              float o[16];
-              const uint32_t at = to + part * (HD / 2) + c * 16;
-              tmem_load16(at, o);
+          for (int c = 0; c < HD / 16; ++c) {
+            float o[16];
+            tmem_load16(to + c * 16, o);
 #pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] *= alpha;
-              tmem_store16(at, o);
-            }
+            for (int x = 0; x < 16; ++x) o[x] *= alpha;
+            tmem_store16(to + c * 16, o);
           }
         }
       }
-      if (!ok) continue;
+      if (!ok) break;
 #pragma unroll
-      for (int x = 0; x < 32; ++x) z[x] = exp2_fast(z[x]);
+      for (int x = 0; x < kKeys; ++x) z[x] = exp2_fast(z[x]);
       float sum[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) sum[x] = z[x];
 #pragma unroll
-      for (int x = 1; x < 4; ++x)
+      for (int x = 1; x < kKeys / 8; ++x)
 #pragma unroll
         for (int y = 0; y < 4; ++y)
           add2(sum[2 * y], sum[2 * y + 1], z[8 * x + 2 * y], z[8 * x + 2 * y + 1]);
       l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
       if constexpr (C::kQuant) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
+        for (int x = 0; x < kKeys / 4; ++x) {
           const float4 f = ld_shared_f4(words + 256u + x * 16);
           mul2(z[4 * x], z[4 * x + 1], f.x, f.y);
           mul2(z[4 * x + 2], z[4 * x + 3], f.z, f.w);
         }
         if (partial) {  // a hidden row may have any scale, a NaN too
 #pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (!((vis >> x) & 1u)) z[x] = 0.f;
+          for (int x = 0; x < kKeys; ++x)
+            if (!((vis[x >> 5] >> (x & 31)) & 1u)) z[x] = 0.f;
         }
       }
-      float pk[16];
+      float pk[32];
 #pragma unroll
-      for (int x = 0; x < 16; ++x)
+      for (int x = 0; x < 32; ++x)
         pk[x] = __uint_as_float(C::kQuant ? pack_f16x2(z[2 * x], z[2 * x + 1])
                                           : pack_bf16x2(z[2 * x], z[2 * x + 1]));
-      tmem_store16(ts + part * 16u, pk);
+      tmem_store32(ts, pk);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_p_full(s, b));
@@ -833,52 +836,48 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       wait(bar_done(0), 0);
       wait(bar_done(1), 0);
     }
-    // Sums of the two threads of a row (and, where the streams hold the same
-    // rows over different keys, of both streams), in a fixed order.  In that
-    // case each stream takes half of the columns and gives the other half
-    // away.  Every product is done: the spaces of Q and K are free.
-    float2* ml = reinterpret_cast<float2*>(smem + C::kK);  // [stream][part][row]
-    ml[(2 * s + part) * 128 + r] = make_float2(m_ref, l);
+    // Where the streams hold the same rows over different keys, each takes half
+    // of the columns and gives the other half away.  Every product is done: the
+    // spaces of Q and K are free.
+    float2* ml = reinterpret_cast<float2*>(smem + C::kK);  // [stream][row]
+    ml[s * 128 + r] = make_float2(m_ref, l);
     // (a stream's warps all have the same unit, but for those without rows)
     float* unit_of = reinterpret_cast<float*>(smem + C::kUnitAt);
     const float my_unit = C::kQuant && n_mine > 0 ? v_inverse(v_exp) : 1.f;
-    if ((tid & 255) == 0) unit_of[s] = my_unit;
+    if (r == 0) unit_of[s] = my_unit;
     const uint32_t xch = sbase + C::kQ;
     const uint32_t mine_at = static_cast<uint32_t>(r) * (HD * 2);
     auto xch_at = [&](int c4) {  // float4 c4 of the row's given half, spread over the banks
       return mine_at + (static_cast<uint32_t>(c4 ^ (r & (HD / 8 - 1))) << 4);
     };
     if (!two_tiles && ok && warp_live) {
-      const int give = (s == 0 ? HD / 2 : 0) + part * (HD / 4);
 #pragma unroll 1
-      for (int c = 0; c < HD / 64; ++c) {
+      for (int c = 0; c < HD / 32; ++c) {
         float o[16];
-        tmem_load16(to + give + c * 16, o);
+        tmem_load16(to + (s == 0 ? HD / 2 : 0) + c * 16, o);
         const bool none = n_mine == 0;  // its accumulator was never written
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          st_shared_f4(xch + s * (64u * HD * 4u) + xch_at(part * (HD / 16) + 4 * c + x),
+          st_shared_f4(xch + s * (64u * HD * 4u) + xch_at(4 * c + x),
                        none ? make_float4(0.f, 0.f, 0.f, 0.f)
                             : make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
       }
     }
     named_bar_sync(1, kSoftmaxThreads);
     float mine_f = my_unit, other_f = 0.f;  // factors of this stream's O and of the other's
-    int c0 = part * (HD / 2), c1 = c0 + HD / 2;  // this thread's columns
-    l = ml[2 * s * 128 + r].y + ml[(2 * s + 1) * 128 + r].y;
+    int c0 = 0, c1 = HD;                    // this thread's columns
     if (!two_tiles) {
-      const float2 x0 = ml[2 * (1 - s) * 128 + r];
-      const float l_other = x0.y + ml[(2 * (1 - s) + 1) * 128 + r].y;
+      const float2 x0 = ml[(1 - s) * 128 + r];
       const float m = fmaxf(m_ref, x0.x), mu = m == -INFINITY ? 0.f : m;
       mine_f = exp2_fast(m_ref - mu);
       other_f = exp2_fast(x0.x - mu);
       // the first stream's share first, whichever thread adds
-      l = s == 0 ? l * mine_f + l_other * other_f : l_other * other_f + l * mine_f;
+      l = s == 0 ? l * mine_f + x0.y * other_f : x0.y * other_f + l * mine_f;
       mine_f *= my_unit;
       other_f *= unit_of[1 - s];
       m_ref = m;
-      c0 = s * (HD / 2) + part * (HD / 4);
-      c1 = c0 + HD / 4;
+      c0 = s * (HD / 2);
+      c1 = c0 + HD / 2;
     }
     if (ok && warp_live && n > 0) {
       const bool pad = depth < 0, whole = u.n_chunks == 1;
@@ -954,7 +953,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     : make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
         }
       }
-      if (row_live && !whole && part == 0 && (two_tiles || s == 0))
+      if (row_live && !whole && (two_tiles || s == 0))
         a.ml_part[static_cast<int64_t>(blockIdx.x) * a.tile_rows + half * 128 + r] =
             pad ? make_float2(-INFINITY, 0.f) : make_float2(m_ref, l);
     }
