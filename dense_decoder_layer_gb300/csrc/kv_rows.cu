@@ -54,21 +54,26 @@ __device__ __forceinline__ void unit_channels(int u, int rot_dim, int layout, in
   }
 }
 
-// (cos, sin) * mscale of the row's pairs into shared memory.  The angle is a
-// fixed-point fraction of a turn: position times a 64-bit fraction, modulo
-// 2^64, is the exact remainder modulo whole turns, so no position loses
-// accuracy and no 64-bit floating point is needed (its rate on this chip is
-// a hundredth of float32's).
+// (cos, sin) * mscale of pair i at position pos.  The angle is a fixed-point
+// fraction of a turn: position times a 64-bit fraction, modulo 2^64, is the
+// exact remainder modulo whole turns, so no position loses accuracy and no
+// 64-bit floating point is needed (its rate on this chip is a hundredth of
+// float32's).  What the conversion of the fraction's upper half to float32
+// rounds off (below 2^-25 of a turn) turns the pair by a first-order step.
+__device__ __forceinline__ float2 pair_turn(const RopeTurns& r, int i, int64_t pos) {
+  const uint64_t turn = static_cast<uint64_t>(pos) * r.turns[i];
+  // signed: [-1/2, 1/2) of a turn; in half turns [-1, 1)
+  const int32_t hi = static_cast<int32_t>(turn >> 32);
+  const float f = __int2float_rn(hi);
+  const float rest = static_cast<float>(hi - static_cast<int32_t>(fminf(f, 2147483520.0f)));
+  constexpr float kHalfTurn = 4.656612873077393e-10f;  // 2^-31
+  float s, c;
+  sincospif(fminf(f, 2147483520.0f) * kHalfTurn, &s, &c);
+  const float d = rest * (kHalfTurn * 3.14159265358979f);
+  return make_float2((c - s * d) * r.mscale, (s + c * d) * r.mscale * r.sign);
+}
 __device__ __forceinline__ void fill_table(float2* table, const RopeTurns& r, int64_t pos) {
-  for (int i = threadIdx.x; i < r.rot_dim / 2; i += blockDim.x) {
-    const uint64_t turn = static_cast<uint64_t>(pos) * r.turns[i];
-    // signed: [-1/2, 1/2) of a turn; in half turns [-1, 1)
-    const float half_turns =
-        static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    table[i] = make_float2(c * r.mscale, s * r.mscale * r.sign);
-  }
+  for (int i = threadIdx.x; i < r.rot_dim / 2; i += blockDim.x) table[i] = pair_turn(r, i, pos);
 }
 
 // Turn the pairs of unit u (table in shared memory); a unit past rot_dim stays.
@@ -91,26 +96,26 @@ __device__ __forceinline__ void rotate_unit(Vec16& v, int u, const RopeTurns& r,
   }
 }
 
-// One block per row (and slice of its units): the first unit's loads go out
-// before the table is made.
-__global__ void __launch_bounds__(kRowThreads) rope_kernel(const uint16_t* x, uint16_t* y, int heads,
-                                                           int hd, int64_t x_stride,
+// One block per ROWS rows (and slice of their units): a thread's units of all of
+// them are loaded before the table is made and while it is.  Four rows per block
+// when there are many (128 bytes per thread in flight; with one, a block's table
+// and barrier cost as much as its data: 8192 rows of 32 x 128 took 33.5 us), one
+// when there are few and latency counts.
+template <int ROWS>
+__global__ void __launch_bounds__(kRowThreads) rope_kernel(const uint16_t* x, uint16_t* y, int rows,
+                                                           int heads, int hd, int64_t x_stride,
                                                            int64_t y_stride,
                                                            const int32_t* __restrict__ positions,
                                                            int start_pos,
                                                            const __grid_constant__ RopeTurns r) {
-  __shared__ float2 table[kMaxTurnPairs];
-  const int row = blockIdx.x;
+  __shared__ float2 table[ROWS * kMaxTurnPairs];
+  const int row0 = blockIdx.x * ROWS;
   const int per_head = hd >> 4, units = heads * per_head;
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
-  const int64_t pos = positions ? static_cast<int64_t>(positions[row])
-                                : static_cast<int64_t>(start_pos) + row;
-  const uint16_t* xr = x + row * x_stride;
-  uint16_t* yr = y + row * y_stride;
   const int step = blockDim.x * gridDim.y;
   int u = blockIdx.y * blockDim.x + threadIdx.x;
-  uint4 wa = {}, wb = {};
+  uint4 wa[ROWS], wb[ROWS];
   int off_a = 0, off_b = 0, uu = 0;
   auto load = [&]() {
     const int h = u / per_head;
@@ -119,19 +124,36 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const uint16_t* x, ui
     unit_channels(uu, r.rot_dim, r.layout, a, b);
     off_a = h * hd + a;
     off_b = h * hd + b;
-    wa = *reinterpret_cast<const uint4*>(xr + off_a);
-    wb = *reinterpret_cast<const uint4*>(xr + off_b);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (ROWS > 1 && row0 + i >= rows) continue;
+      const uint16_t* xr = x + (row0 + i) * x_stride;
+      wa[i] = *reinterpret_cast<const uint4*>(xr + off_a);
+      wb[i] = *reinterpret_cast<const uint4*>(xr + off_b);
+    }
   };
   if (u < units) load();
-  fill_table(table, r, pos);
+  const int pairs = r.rot_dim / 2;
+  for (int i = threadIdx.x; i < ROWS * pairs; i += blockDim.x) {
+    const int k = ROWS > 1 ? i / pairs : 0, row = row0 + k;
+    if (ROWS > 1 && row >= rows) break;
+    const int64_t pos = positions ? static_cast<int64_t>(positions[row])
+                                  : static_cast<int64_t>(start_pos) + row;
+    table[k * kMaxTurnPairs + i - k * pairs] = pair_turn(r, i - k * pairs, pos);
+  }
   __syncthreads();
   while (u < units) {
-    Vec16 v;
-    widen8(wa, v.x);
-    widen8(wb, v.x + 8);
-    rotate_unit(v, uu, r, table);
-    *reinterpret_cast<uint4*>(yr + off_a) = narrow8(v.x);
-    *reinterpret_cast<uint4*>(yr + off_b) = narrow8(v.x + 8);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (ROWS > 1 && row0 + i >= rows) break;
+      Vec16 v;
+      widen8(wa[i], v.x);
+      widen8(wb[i], v.x + 8);
+      rotate_unit(v, uu, r, table + i * kMaxTurnPairs);
+      uint16_t* yr = y + (row0 + i) * y_stride;
+      *reinterpret_cast<uint4*>(yr + off_a) = narrow8(v.x);
+      *reinterpret_cast<uint4*>(yr + off_b) = narrow8(v.x + 8);
+    }
     u += step;
     if (u < units) load();
   }
@@ -315,49 +337,69 @@ __global__ void __launch_bounds__(kRowThreads)
   const int64_t j0 = at_lens ? len : first_row;          // cache row of output row 0
   const int64_t live = at_lens ? rows : min(static_cast<int64_t>(rows), len - j0);
   const int n = static_cast<int>(min(static_cast<int64_t>(kReadRows), live - r0));
-  const int per_row = c.n_kv_heads * kPerHead;
-  for (int u = threadIdx.x; u < n * per_row; u += blockDim.x) {
-    const int r = u / per_row, w = u - r * per_row;
-    const int h = w / kPerHead, ch = (w - h * kPerHead) * 16;
-    const int64_t j = j0 + r0 + r;
-    const char* p = src + j * c.row_stride + h * c.head_stride;
-    uint4 lo, hi;
-    if constexpr (FMT == PDS_KV_BF16) {
-      lo = *reinterpret_cast<const uint4*>(p + 2 * ch);
-      hi = *reinterpret_cast<const uint4*>(p + 2 * ch + 16);
-    } else {
-      const uint32_t word =
-          scales[(static_cast<int64_t>(s) * c.n_kv_heads + h) * c.capacity + j];
-      float x[16];
-      if constexpr (FMT == PDS_KV_E4M3) {
-        const uint4 q = *reinterpret_cast<const uint4*>(p + ch);
-        const uint32_t qs[4] = {q.x, q.y, q.z, q.w};
-        const float scale = __uint_as_float(word);
+  // four units per thread in flight
+  const int per_row = c.n_kv_heads * kPerHead, total = n * per_row;
+  constexpr int kFlight = 4;
+  for (int u0 = threadIdx.x; u0 < total; u0 += kFlight * kRowThreads) {
+    uint4 qa[kFlight], qb[kFlight];
+    uint32_t word[kFlight];
+    int64_t to[kFlight];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
-              static_cast<__nv_fp8x2_storage_t>(qs[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-          const float2 f = __half22float2(__half2(hr));
-          x[2 * i] = f.x * scale;
-          x[2 * i + 1] = f.y * scale;
-        }
+    for (int i = 0; i < kFlight; ++i) {
+      const int u = u0 + i * kRowThreads;
+      to[i] = -1;
+      if (u >= total) continue;
+      const int r = u / per_row, w = u - r * per_row;
+      const int h = w / kPerHead, ch = (w - h * kPerHead) * 16;
+      const int64_t j = j0 + r0 + r;
+      const char* p = src + j * c.row_stride + h * c.head_stride;
+      to[i] = ((static_cast<int64_t>(s) * rows + r0 + r) * c.n_kv_heads + h) * HD + ch;
+      if constexpr (FMT == PDS_KV_BF16) {
+        qa[i] = *reinterpret_cast<const uint4*>(p + 2 * ch);
+        qb[i] = *reinterpret_cast<const uint4*>(p + 2 * ch + 16);
+      } else if constexpr (FMT == PDS_KV_E4M3) {
+        qa[i] = *reinterpret_cast<const uint4*>(p + ch);
       } else {
         const uint2 q = *reinterpret_cast<const uint2*>(p + ch / 2);
-        const float scale = __uint_as_float(word & 0xffff0000u);
-        const int z = word & 15;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int n4 = ((i < 8 ? q.x : q.y) >> (4 * (i & 7))) & 15;
-          x[i] = static_cast<float>(n4 - z) * scale;
-        }
+        qa[i].x = q.x;
+        qa[i].y = q.y;
       }
-      lo = narrow8(x);
-      hi = narrow8(x + 8);
+      if constexpr (FMT != PDS_KV_BF16)
+        word[i] = scales[(static_cast<int64_t>(s) * c.n_kv_heads + h) * c.capacity + j];
     }
-    uint4* dst = reinterpret_cast<uint4*>(
-        out + ((static_cast<int64_t>(s) * rows + r0 + r) * c.n_kv_heads + h) * HD + ch);
-    dst[0] = lo;
-    dst[1] = hi;
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      if (to[i] < 0) continue;
+      uint4 lo = qa[i], hi = qb[i];
+      if constexpr (FMT != PDS_KV_BF16) {
+        float x[16];
+        if constexpr (FMT == PDS_KV_E4M3) {
+          const uint32_t qs[4] = {qa[i].x, qa[i].y, qa[i].z, qa[i].w};
+          const float scale = __uint_as_float(word[i]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+                static_cast<__nv_fp8x2_storage_t>(qs[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
+            const float2 f = __half22float2(__half2(hr));
+            x[2 * e] = f.x * scale;
+            x[2 * e + 1] = f.y * scale;
+          }
+        } else {
+          const float scale = __uint_as_float(word[i] & 0xffff0000u);
+          const int z = word[i] & 15;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int n4 = ((e < 8 ? qa[i].x : qa[i].y) >> (4 * (e & 7))) & 15;
+            x[e] = static_cast<float>(n4 - z) * scale;
+          }
+        }
+        lo = narrow8(x);
+        hi = narrow8(x + 8);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(out + to[i]);
+      dst[0] = lo;
+      dst[1] = hi;
+    }
   }
 }
 
@@ -375,6 +417,8 @@ cudaError_t by_format(int format, int hd, F&& f) {
   }
 }
 
+constexpr int kManyRows = 2048;
+
 int round_threads(int units) {  // a block that covers the units, whole warps
   return units >= kRowThreads ? kRowThreads : (units + 31) / 32 * 32;
 }
@@ -386,12 +430,15 @@ cudaError_t launch_rope(const RopeTurns& r, const uint16_t* x, uint16_t* y, int 
                         int start_pos, cudaStream_t st) {
   const int units = heads * (hd / 16);
   const int threads = round_threads(units);
-  // few rows: the row's units are spread over several blocks
-  const int slices = rows >= 256 ? 1 : (units + threads - 1) / threads;
-  return launch_after(rope_kernel, dim3(rows, std::min(slices, 65535)), threads, 0, st, x, y, heads,
-                      hd, x_stride, y_stride, positions, start_pos, r);
+  const int slices = std::min((units + threads - 1) / threads, 65535);
+  // many rows: enough blocks of four to fill the GPU several times
+  if (rows >= kManyRows)
+    return launch_after(rope_kernel<4>, dim3((rows + 3) / 4), threads, 0, st, x, y, rows, heads, hd,
+                        x_stride, y_stride, positions, start_pos, r);
+  // few: the units of a row are spread over several blocks
+  return launch_after(rope_kernel<1>, dim3(rows, slices), threads, 0, st, x, y, rows, heads, hd,
+                      x_stride, y_stride, positions, start_pos, r);
 }
-
 cudaError_t launch_cache_write(const CacheView& c, int format, int hd, const RopeTurns& r,
                                const uint16_t* k, const uint16_t* v, int n_tokens,
                                int64_t k_stride, int64_t v_stride, const int32_t* parents,
