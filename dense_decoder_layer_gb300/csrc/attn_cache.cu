@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
     const int r = r0 + 8 * n + (l >> 2);
     qb[it][0] = qb[it][1] = 0u;
     if (idx < kQFrags && r < rows) {
-      const int t = r / a.group, i = r - t * a.group;
+      const int t = token_of(a, r), i = r - t * a.group;
       const uint16_t* src = a.q + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.q_stride +
                             (head * a.group + i) * HD;
       const int ch = F::q_channel(ks, l & 3);
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
     if (lane == 0) q_max[warp] = q_top;
   }
   // a tree's depths, and the ancestor sets of this tile's tokens
-  const int t_first = r0 / a.group;
+  const int t_first = token_of(a, r0);
   if (a.parents && threadIdx.x < a.n_tokens)
     par[threadIdx.x] = a.parents[static_cast<int64_t>(u.seq) * a.n_tokens + threadIdx.x];
   __syncthreads();
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = r0 + 8 * n + 2 * t4 + e;
-      const int t = r < rows ? r / a.group : -1;
+      const int t = r < rows ? token_of(a, r) : -1;
       const int d = t < 0 ? -1 : depth_of(t);
       tok[n][e] = d < 0 ? -1 : t - t_first;
       pos[n][e] = u.len + d;
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
   for (int idx = threadIdx.x; idx < C::kRows * (HD / 4); idx += kThreads) {
     const int r = idx / (HD / 4), ch = (idx - r * (HD / 4)) * 4;
     if (r0 + r >= rows) break;
-    const int t = (r0 + r) / a.group, i = r0 + r - t * a.group;
+    const int t = token_of(a, r0 + r), i = r0 + r - t * a.group;
     float m = -INFINITY;
 #pragma unroll
     for (int x = 0; x < kWarps; ++x) m = fmaxf(m, ml[x * C::kRows + r].x);
@@ -881,7 +881,7 @@ Shape make_shape(int format, int hd, int n_seqs, int n_tokens, int n_heads, int 
   s.per = n_kv_heads * s.row_tiles;
   const int64_t units = static_cast<int64_t>(n_seqs) * s.per;
   const int resident = num_sms * (s.tiles ? 1 : blocks_per_sm(format, hd, s.nt));
-  s.fit = 2 * units <= resident;
+  s.fit = units <= resident;
   s.slots = s.fit ? resident : 2 * resident;
   return s;
 }
@@ -943,6 +943,7 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
   a.n_tokens = t.n_tokens;
   a.n_heads = t.n_heads;
   a.group = t.n_heads / c.n_kv_heads;
+  a.per_group = 1.0f / static_cast<float>(a.group);
   a.max_len = t.max_len;
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(t.head_dim));
   a.cap = t.softcap > 0.f ? t.softcap * sqrtf(static_cast<float>(t.head_dim)) : 0.f;

@@ -21,6 +21,7 @@ struct Args {
   int64_t q_stride, o_stride;
   const int32_t* parents;
   int n_tokens, n_heads, group;  // group: query heads per kv head
+  float per_group;               // 1 / group
   int max_len;
   float scale_log2;              // log2(e) / sqrt(hd)
   float cap;                     // softcap in units of q.k (0: none)
@@ -51,6 +52,12 @@ __device__ __forceinline__ int seq_steps(const Args& a, int s, int& first, int& 
   // the first row any token can see: a root's, at position len
   if (a.window > 0 && len - a.window + 1 > 0) first = (len - a.window + 1) / a.step;
   return (len + a.n_tokens + a.step - 1) / a.step - first;
+}
+
+// Token of query row R = t group + i: R is below 2^21 (256 tokens, 8192 heads), so
+// the rounded product is off by less than half of 1 / group.
+__device__ __forceinline__ int token_of(const Args& a, int R) {
+  return static_cast<int>((static_cast<float>(R) + 0.5f) * a.per_group);
 }
 
 __device__ __forceinline__ unsigned warp_sum_uint(unsigned v) {
@@ -85,8 +92,8 @@ __device__ __forceinline__ int chunk_steps(const Args& a, int lane, const Lane& 
   total = warp_sum(total);
   int c = max(a.min_steps, static_cast<int>(__fdividef(total * per, static_cast<float>(a.slots))));
   // Sequences' last chunks are short: lengthen until the units fit the slots.
-  // There are at most half as many (sequence, head, tile) as slots, so twice
-  // this length always fits: some 16 rounds of a sixteenth at the very most.
+  // One chunk per sequence always fits; the length grows by a sixteenth a round,
+  // and past the longest sequence there is nothing left to grow for.
   const unsigned most = static_cast<unsigned>(a.slots / per);
   for (;;) {
     unsigned chunks = static_cast<unsigned>(mine.n + c - 1) / static_cast<unsigned>(c);

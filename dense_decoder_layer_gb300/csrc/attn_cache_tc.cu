@@ -593,51 +593,52 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (ok) tc_fence_after();
     };
-    // Q: one or two tiles, in pieces of half a row per thread and round
+    // Q: half a row of each of the (one or two) tiles per thread, all loads at once
     if (n > 0) {
       constexpr int kPieces = HD / 16;
-      const int rounds = two_tiles ? 2 : 1;
-      uint4 x[kPieces];
-      auto load = [&](int round) {
-        const int row = round * 128 + (tid >> 1), R = r0 + row;
+      uint4 x[2][kPieces];
 #pragma unroll
-        for (int c = 0; c < kPieces; ++c) x[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (R < rows) {
-          const int t = R / a.group, i = R - t * a.group;
+      for (int tile = 0; tile < 2; ++tile) {
+        const int R = r0 + tile * kTileRows + (tid >> 1);
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c) x[tile][c] = make_uint4(0u, 0u, 0u, 0u);
+        if (R < rows && (tile == 0 || two_tiles)) {
+          const int t = token_of(a, R), i = R - t * a.group;
           const uint4* src = reinterpret_cast<const uint4*>(
               a.q + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.q_stride +
               (head * a.group + i) * HD) + (tid & 1) * kPieces;
 #pragma unroll
-          for (int c = 0; c < kPieces; ++c) x[c] = src[c];
+          for (int c = 0; c < kPieces; ++c) x[tile][c] = src[c];
         }
-      };
+      }
       float q_mul = 1.f;
       if constexpr (C::kQuant) {
+        // largest finite |value| of a pair of bf16, by their bits
         uint32_t top = 0u;
         auto both = [&](uint32_t w) {
           top = max(top, max(finite_bits(__uint_as_float(w << 16)),
                              finite_bits(__uint_as_float(w & 0xffff0000u))));
         };
-#pragma unroll 1
-        for (int round = rounds - 1; round >= 0; --round) {  // (round 0 stays loaded)
-          load(round);
 #pragma unroll
-          for (int c = 0; c < kPieces; ++c) both(x[c].x), both(x[c].y), both(x[c].z), both(x[c].w);
-        }
+        for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+          for (int c = 0; c < kPieces; ++c)
+            both(x[tile][c].x), both(x[tile][c].y), both(x[tile][c].z), both(x[tile][c].w);
         uint32_t* q_max = reinterpret_cast<uint32_t*>(smem + C::kQMax);
         top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) q_max[warp - kFirstSoftmaxWarp] = top;
         named_bar_sync(1, kSoftmaxThreads);
+#pragma unroll
         for (int c = 0; c < kSoftmaxThreads / 32; ++c) top = max(top, q_max[c]);
         float inverse;
         q_mul = q_multiplier(top, inverse);
       }
-#pragma unroll 1
-      for (int round = 0; round < rounds; ++round) {
-        if (!C::kQuant || round > 0) load(round);
+#pragma unroll
+      for (int tile = 0; tile < 2; ++tile) {
+        if (tile == 1 && !two_tiles) break;
 #pragma unroll
         for (int c = 0; c < kPieces; ++c) {
-          uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+          uint32_t w[4] = {x[tile][c].x, x[tile][c].y, x[tile][c].z, x[tile][c].w};
           if constexpr (C::kQuant) {
             float f[8];
 #pragma unroll
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               w[e] = FMT == PDS_KV_INT4 ? pack_f16x2(f[e], f[e + 4])
                                         : pack_f16x2(f[2 * e], f[2 * e + 1]);
           }
-          st_shared_u4(sbase + C::kQ + round * C::kQTile +
+          st_shared_u4(sbase + C::kQ + tile * C::kQTile +
                            tile_at<128>(tid >> 1, (tid & 1) * kPieces + c),
                        w[0], w[1], w[2], w[3]);
         }
@@ -663,7 +664,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // column of the mask table, and the first cached row it sees
     const int R = r0 + (two_tiles ? s * kTileRows : 0) + r;
     const bool row_live = R < rows;
-    const int tok = row_live ? R / a.group : 0;
+    const int tok = row_live ? token_of(a, R) : 0;
     int32_t* par = reinterpret_cast<int32_t*>(smem + C::kPar);
     uint32_t* mask = reinterpret_cast<uint32_t*>(smem + C::kMask) + s * 128 + r;
     if (n > 0 && a.parents && tid < a.n_tokens)
@@ -852,13 +853,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     if (!two_tiles && ok && warp_live) {
 #pragma unroll 1
-      for (int c = 0; c < HD / 32; ++c) {
-        float o[16];
-        tmem_load16(to + (s == 0 ? HD / 2 : 0) + c * 16, o);
+      for (int c = 0; c < HD / 64; ++c) {
+        float o[32];
+        tmem_load32(to + (s == 0 ? HD / 2 : 0) + c * 32, o);
         const bool none = n_mine == 0;  // its accumulator was never written
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          st_shared_f4(xch + s * (64u * HD * 4u) + xch_at(4 * c + x),
+        for (int x = 0; x < 8; ++x)
+          st_shared_f4(xch + s * (64u * HD * 4u) + xch_at(8 * c + x),
                        none ? make_float4(0.f, 0.f, 0.f, 0.f)
                             : make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
       }
@@ -889,13 +890,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       float4* out = reinterpret_cast<float4*>(a.o_part) +
                     (static_cast<int64_t>(blockIdx.x) * (a.tile_rows / 128) + half) * (HD / 4) * 128;
 #pragma unroll 1
-      for (int c = c0; c < c1; c += 16) {
-        float o[16];
-        tmem_load16(to + c, o);
+      for (int c = c0; c < c1; c += 32) {
+        float o[32];
+        tmem_load32(to + c, o);
         if (!two_tiles) {
           const bool none = n_mine == 0;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
+          for (int x = 0; x < 8; ++x) {
             const float4 y = ld_shared_f4(xch + (1 - s) * (64u * HD * 4u) +
                                           xch_at((c - s * (HD / 2)) / 4 + x));
             const float v[4] = {y.x, y.y, y.z, y.w};
@@ -907,14 +908,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         } else if (C::kQuant) {
 #pragma unroll
-          for (int x = 0; x < 16; ++x) o[x] *= mine_f;
+          for (int x = 0; x < 32; ++x) o[x] *= mine_f;
         }
         if constexpr (FMT == PDS_KV_INT4) {  // the channels back in their order
-          float y[16];
+          float y[32];
 #pragma unroll
-          for (int x = 0; x < 16; ++x) y[x] = o[(x & 8) + ((x & 3) << 1) + ((x >> 2) & 1)];
+          for (int x = 0; x < 32; ++x) y[x] = o[(x & 24) + ((x & 3) << 1) + ((x >> 2) & 1)];
 #pragma unroll
-          for (int x = 0; x < 16; ++x) o[x] = y[x];
+          for (int x = 0; x < 32; ++x) o[x] = y[x];
         }
         if constexpr (!C::kQuant) {
           if (*poison && row_live) {  // what the loaders took out, for the rows that see it
@@ -930,7 +931,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                       a.c.v + u.seq * a.c.seq_stride + head * a.c.head_stride +
                       (key0 + 32 * g + x) * a.c.row_stride) + c;
 #pragma unroll
-                  for (int e = 0; e < 16; ++e)
+                  for (int e = 0; e < 32; ++e)
                     if ((v[e] & 0x7f80u) == 0x7f80u) o[e] += bf16_to_f32(v[e]);
                 }
               }
@@ -939,15 +940,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         if (!row_live) continue;
         if (whole) {
-          uint32_t y[8];
+          uint32_t y[16];
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
+          for (int x = 0; x < 16; ++x)
             y[x] = pad ? 0u : pack_bf16x2(o[2 * x] * inv, o[2 * x + 1] * inv);
-          reinterpret_cast<uint4*>(dst + c)[0] = make_uint4(y[0], y[1], y[2], y[3]);
-          reinterpret_cast<uint4*>(dst + c)[1] = make_uint4(y[4], y[5], y[6], y[7]);
-        } else {
 #pragma unroll
           for (int x = 0; x < 4; ++x)
+            reinterpret_cast<uint4*>(dst + c)[x] =
+                make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
             out[(c / 4 + x) * 128 + r] =
                 pad ? make_float4(0.f, 0.f, 0.f, 0.f)
                     : make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
@@ -1039,7 +1042,7 @@ __global__ void __launch_bounds__(256) cache_join_tile_kernel(const __grid_const
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-  const int t = R / a.group, i = R - t * a.group;
+  const int t = token_of(a, R), i = R - t * a.group;
   uint16_t* dst = a.o + (static_cast<int64_t>(seq) * a.n_tokens + t) * a.o_stride +
                   (head * a.group + i) * HD + c4 * 4;
   *reinterpret_cast<uint4*>(dst) =

@@ -651,8 +651,8 @@ pds_status pds_attention_tree(const pds_cache* cache, const uint16_t* q, uint16_
   if (n_tokens < 1 || n_heads < 1) return fail(PDS_EINVAL, "pds_attention_tree: bad size");
   if (!(softcap >= 0.f) || !std::isfinite(softcap) || window < 0 || max_len < 0)
     return fail(PDS_EINVAL, "pds_attention_tree: softcap, window and max_len must be >= 0");
-  if (n_heads % cache->n_kv_heads || n_heads > (1 << 20))
-    return fail(PDS_DECLINED, "declined: pds_attention_tree needs H % Hkv == 0");
+  if (n_heads % cache->n_kv_heads || n_heads > 8192)
+    return fail(PDS_DECLINED, "declined: pds_attention_tree needs H % Hkv == 0, H <= 8192");
   if (n_tokens > pds::kMaxDraftTokens)
     return fail(PDS_DECLINED, "declined: pds_attention_tree takes at most 256 tokens");
   if (n_tokens > cache->capacity)
