@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
       }
       if (blockIdx.x == 0) {  // report lengths that do not fit
         bool bad = false;
+#pragma unroll 1
         for (int s = lane; s < a.c.n_seqs; s += 32) bad |= lane_steps(a, s).n == 0;
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kStatusBadLength);
       }
@@ -863,7 +864,7 @@ constexpr int kTileMinRows = 33;
 struct Shape {
   bool tiles;            // the tensor-core kernel
   int nt;                // the warp kernel's column tiles
-  int step, tile_rows;   // keys of a step, query rows of a block
+  int step_shift, tile_rows;  // log2 of a step's keys, query rows of a block
   int row_tiles, per;    // blocks of rows per kv head, and per sequence
   int slots, fit;
 };
@@ -875,7 +876,7 @@ Shape make_shape(int format, int hd, int n_seqs, int n_tokens, int n_heads, int 
   const int rows = n_tokens * (n_heads / n_kv_heads);
   s.tiles = rows >= kTileMinRows;
   s.nt = column_tiles(rows);
-  s.step = s.tiles ? 64 : kStep;
+  s.step_shift = s.tiles ? 6 : 4;
   s.tile_rows = s.tiles ? (rows <= 128 ? 128 : 256) : 8 * s.nt;
   s.row_tiles = (rows + s.tile_rows - 1) / s.tile_rows;
   s.per = n_kv_heads * s.row_tiles;
@@ -950,14 +951,14 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
   a.window = t.window;
   a.row_tiles = s.row_tiles;
   a.tile_rows = s.tile_rows;
-  a.step = s.step;
+  a.step_shift = s.step_shift;
   a.min_steps = s.tiles ? 4 : 2 * kWarps;
   a.status = t.status;
   // a window's keys, with whole steps at both ends
-  const int64_t prefix = t.window > 0 ? std::min<int64_t>(t.max_len, int64_t{t.window} + 2 * s.step)
+  const int64_t prefix = t.window > 0 ? std::min<int64_t>(t.max_len, int64_t{t.window} + (2 << s.step_shift))
                                       : t.max_len;
   const int64_t span = prefix + t.n_tokens;
-  const int64_t least = static_cast<int64_t>(a.step) * a.min_steps;
+  const int64_t least = static_cast<int64_t>(a.min_steps) << a.step_shift;
   const int64_t most_chunks = (span + least - 1) / least;
   const int64_t units = static_cast<int64_t>(c.n_seqs) * s.per;
   int64_t grid = units;

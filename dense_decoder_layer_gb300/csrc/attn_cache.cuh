@@ -26,7 +26,7 @@ struct Args {
   float scale_log2;              // log2(e) / sqrt(hd)
   float cap;                     // softcap in units of q.k (0: none)
   int window;
-  int step;                      // keys of a step
+  int step_shift;                // log2 of the keys of a step
   int row_tiles;                 // blocks of query rows per (sequence, kv head)
   int tile_rows;                 // rows of one
   int slots;                     // blocks to spread the chunks over; 0: one chunk each
@@ -43,15 +43,15 @@ struct Args {
 // Units: (chunk of a sequence) x (kv head, row tile), the latter fastest, so
 // that blocks running together read neighbouring heads of the same rows.
 
-// Steps of sequence s: [first, first + n) in units of a.step keys; n = 0 for a
+// Steps of sequence s: [first, first + n) in units of 2^step_shift keys; n = 0 for a
 // length that does not fit.
 __device__ __forceinline__ int seq_steps(const Args& a, int s, int& first, int& len) {
   len = a.c.lens[s];
   first = 0;
   if (len < 0 || len > a.max_len) return 0;
   // the first row any token can see: a root's, at position len
-  if (a.window > 0 && len - a.window + 1 > 0) first = (len - a.window + 1) / a.step;
-  return (len + a.n_tokens + a.step - 1) / a.step - first;
+  if (a.window > 0 && len - a.window + 1 > 0) first = (len - a.window + 1) >> a.step_shift;
+  return ((len + a.n_tokens - 1) >> a.step_shift) + 1 - first;
 }
 
 // Token of query row R = t group + i: R is below 2^21 (256 tokens, 8192 heads), so
@@ -81,6 +81,7 @@ __device__ __forceinline__ int chunk_steps(const Args& a, int lane, const Lane& 
   const int per = a.c.n_kv_heads * a.row_tiles;
   if (!a.fit) {
     long long total = mine.n;
+#pragma unroll 1
     for (int s = lane + 32; s < a.c.n_seqs; s += 32) total += lane_steps(a, s).n;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -88,6 +89,7 @@ __device__ __forceinline__ int chunk_steps(const Args& a, int lane, const Lane& 
     return max(a.min_steps, static_cast<int>((total * per + a.slots - 1) / a.slots));
   }
   float total = static_cast<float>(mine.n);
+#pragma unroll 1
   for (int s = lane + 32; s < a.c.n_seqs; s += 32) total += static_cast<float>(lane_steps(a, s).n);
   total = warp_sum(total);
   int c = max(a.min_steps, static_cast<int>(__fdividef(total * per, static_cast<float>(a.slots))));
@@ -95,8 +97,10 @@ __device__ __forceinline__ int chunk_steps(const Args& a, int lane, const Lane& 
   // One chunk per sequence always fits; the length grows by a sixteenth a round,
   // and past the longest sequence there is nothing left to grow for.
   const unsigned most = static_cast<unsigned>(a.slots / per);
+#pragma unroll 1
   for (;;) {
     unsigned chunks = static_cast<unsigned>(mine.n + c - 1) / static_cast<unsigned>(c);
+#pragma unroll 1
     for (int s = lane + 32; s < a.c.n_seqs; s += 32) chunks += (lane_steps(a, s).n + c - 1) / c;
     if (warp_sum_uint(chunks) <= most) return c;
     c += max(1, c >> 4);
@@ -134,6 +138,7 @@ __device__ __forceinline__ bool only_unit(const Args& a, int w, Unit& u) {
 __device__ __forceinline__ bool find_unit(const Args& a, int c, int w, int seq, int lane, const Lane& mine,
                           Unit& u) {
   int base = 0;
+#pragma unroll 1
   for (int s0 = 0; s0 < a.c.n_seqs; s0 += 32) {
     const Lane l = s0 == 0 ? mine : lane_steps(a, s0 + lane);
     const int chunks = l.n == 0 ? 0 : (l.n - 1) / c + 1;
@@ -283,7 +288,7 @@ __device__ __forceinline__ bool not_finite2(uint32_t w) {  // either bf16 of a p
 
 }  // namespace cacheattn
 
-// The tensor-core kernel and its join (attn_cache_tc.cu): a.step is 64 keys,
+// The tensor-core kernel and its join (attn_cache_tc.cu): a step is 64 keys,
 // a.tile_rows 128 or 256 query rows per block, one block per SM.
 cudaError_t launch_tile_attention(const cacheattn::Args& a, int format, int hd, int64_t grid,
                                   cudaStream_t st);

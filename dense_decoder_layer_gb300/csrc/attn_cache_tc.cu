@@ -242,6 +242,29 @@ __device__ __forceinline__ bool part_hidden(const Args& a, int key0, int keys, i
   return key0 + keys > len || (a.window > 0 && key0 < len + a.n_tokens - a.window);
 }
 
+// The bounded wait of a converged warp; every lane returns the same.  Short on
+// purpose: a block runs most of its code once and has to fetch it first, some
+// hundred cycles per 128 bytes, and this appears in twenty places.
+__device__ __forceinline__ bool warp_wait(bool ok, uint32_t bar, uint32_t parity,
+                                          volatile int* abort_flag, uint32_t* status) {
+  if (__all_sync(0xffffffffu, ok && sm100::mbar_try_wait(bar, parity))) return true;
+  if (ok) {
+    const uint64_t t0 = sm100::global_timer_ns();
+    ok = false;
+    do {
+      if (sm100::mbar_try_wait(bar, parity)) {
+        ok = true;
+        break;
+      }
+    } while (!*abort_flag && sm100::global_timer_ns() - t0 < sm100::kWaitLimitNs);
+    if (!ok) {
+      *abort_flag = 1;
+      atomicOr(status, kStatusTimeout);
+    }
+  }
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
 template <int FMT, int HD, bool VAR>
 __global__ void __launch_bounds__(kTileThreads, 1)
     cache_attn_tile_kernel(const __grid_constant__ Args a) {
@@ -320,6 +343,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     if (blockIdx.x == 0) {  // report lengths that do not fit
       bool bad = false;
+#pragma unroll 1
       for (int s = lane; s < a.c.n_seqs; s += 32) bad |= lane_steps(a, s).n == 0;
       if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kStatusBadLength);
     }
@@ -349,8 +373,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const bool leader = lane == 0;
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity, abort_flag, a.status)) != 0;
-        return ok;
+        return ok = warp_wait(ok, bar, parity, abort_flag, a.status);
       };
       const uint32_t q = ((sbase + C::kQ + (two_tiles ? s * C::kQTile : 0u)) >> 4) | kKMajorLo;
       const uint32_t scores_at = tmem + C::kTmS + s * 128u, o_at = tmem + C::kTmO + s * 128u;
@@ -366,7 +389,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (!wait(bar_k_full(k_st), k_phase)) break;
           tc_fence_after();
           const uint32_t k = ((sbase + C::kK + k_st * C::kTile) >> 4) | kKMajorLo;
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < HD / 16; ++x)
             mma_ss(leader, scores_at + b * 64u, q + kmajor_step<128>(x), k + kmajor_step<64>(x),
                    kIdS, x > 0);
@@ -381,7 +404,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tc_fence_after();
           const uint32_t v = ((sbase + C::kV + v_st * C::kTile) >> 4) | kVLo;
           const uint32_t p_at = scores_at + (e & 1) * 64u;
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < kKeys / 16; ++x)
             mma_ts(leader, o_at, p_at + x * 8u, v + v_step(x), kIdPV, e > 0 || x > 0);
           mma_commit(leader, bar_pv(s, e & 1));
@@ -391,7 +414,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       mma_commit(leader, bar_done(s));
       int dummy = 0;
-      mbar_wait(bar_done(s), 0, &dummy, a.status);
+      warp_wait(true, bar_done(s), 0, &dummy, a.status);
     }
   } else if (warp < kFirstSoftmaxWarp) {
     setmaxnreg_dec<kLeanRegs>();
@@ -399,8 +422,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int tid = (threadIdx.x - 32 * kFirstLoadWarp) & (kLoadThreads - 1);
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      ok = ok && mbar_wait(bar, parity, abort_flag, a.status);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = warp_wait(ok, bar, parity, abort_flag, a.status);
     };
     auto arrive = [&](uint32_t bar) {
       fence_proxy_async_smem();
@@ -492,6 +514,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (++st_done == stages) st_done = 0;
       }
     } else {
+#pragma unroll 1
       for (int t = 0; t < C::kRaw; ++t) issue(t, raw0 + t * C::kUnit, t);
       int st = 0, slot = 0;
       uint32_t phase = 1, v_exp = kMinScaleExp;
@@ -500,6 +523,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         wait(bar_q, 0);
         uint32_t top = 0u;
         const uint32_t* q_max = reinterpret_cast<const uint32_t*>(smem + C::kQMax);
+#pragma unroll 1
         for (int x = 0; x < kSoftmaxThreads / 32; ++x) top = max(top, q_max[x]);
         float inverse;
         q_multiplier(top, inverse);
@@ -587,73 +611,64 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t to = tmem + lane_off + C::kTmO + s * 128u;
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (!__all_sync(0xffffffffu, ok && mbar_try_wait(bar, parity))) {
-        ok = ok && mbar_wait(bar, parity, abort_flag, a.status);
-        ok = __all_sync(0xffffffffu, ok);
-      }
+      ok = warp_wait(ok, bar, parity, abort_flag, a.status);
       if (ok) tc_fence_after();
     };
-    // Q: half a row of each of the (one or two) tiles per thread, all loads at once
+    // Q into its (one or two) tiles, in 8-channel pieces; fp16 where the rows are
+    // codes: each thread then converts the pieces it has copied, in place.
+    // (Loops rolled by four: this runs once, and fetching its code costs as
+    // much as its latencies.)
     if (n > 0) {
-      constexpr int kPieces = HD / 16;
-      uint4 x[2][kPieces];
-#pragma unroll
-      for (int tile = 0; tile < 2; ++tile) {
-        const int R = r0 + tile * kTileRows + (tid >> 1);
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c) x[tile][c] = make_uint4(0u, 0u, 0u, 0u);
-        if (R < rows && (tile == 0 || two_tiles)) {
-          const int t = token_of(a, R), i = R - t * a.group;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.q_stride +
-              (head * a.group + i) * HD) + (tid & 1) * kPieces;
-#pragma unroll
-          for (int c = 0; c < kPieces; ++c) x[tile][c] = src[c];
-        }
+      constexpr int kPieces = HD / 8;
+      const int pieces = (two_tiles ? 2 : 1) * 128 * kPieces;
+      auto place = [&](int i) {
+        return sbase + C::kQ + (i / (128 * kPieces)) * C::kQTile +
+               tile_at<128>((i / kPieces) & 127, i % kPieces);
+      };
+#pragma unroll 4
+      for (int i = tid; i < pieces; i += kSoftmaxThreads) {
+        const int R = r0 + i / kPieces;
+        const bool live = R < rows;  // rows past the last are zero
+        const int t = live ? token_of(a, R) : 0, h = live ? R - t * a.group : 0;
+        copy16(place(i), a.q + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.q_stride +
+                             (head * a.group + h) * HD + (i % kPieces) * 8, live);
       }
-      float q_mul = 1.f;
+      copies_commit();
+      copies_wait<0>();
       if constexpr (C::kQuant) {
-        // largest finite |value| of a pair of bf16, by their bits
-        uint32_t top = 0u;
-        auto both = [&](uint32_t w) {
-          top = max(top, max(finite_bits(__uint_as_float(w << 16)),
-                             finite_bits(__uint_as_float(w & 0xffff0000u))));
-        };
+        uint32_t top = 0u;  // bits of the largest finite |value|
+#pragma unroll 4
+        for (int i = tid; i < pieces; i += kSoftmaxThreads) {
+          const uint4 x = lds128(place(i));
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int tile = 0; tile < 2; ++tile)
-#pragma unroll
-          for (int c = 0; c < kPieces; ++c)
-            both(x[tile][c].x), both(x[tile][c].y), both(x[tile][c].z), both(x[tile][c].w);
+          for (int e = 0; e < 4; ++e)
+            top = max(top, max(finite_bits(__uint_as_float(w[e] << 16)),
+                               finite_bits(__uint_as_float(w[e] & 0xffff0000u))));
+        }
         uint32_t* q_max = reinterpret_cast<uint32_t*>(smem + C::kQMax);
         top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) q_max[warp - kFirstSoftmaxWarp] = top;
         named_bar_sync(1, kSoftmaxThreads);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < kSoftmaxThreads / 32; ++c) top = max(top, q_max[c]);
         float inverse;
-        q_mul = q_multiplier(top, inverse);
-      }
+        const float q_mul = q_multiplier(top, inverse);
+#pragma unroll 4
+        for (int i = tid; i < pieces; i += kSoftmaxThreads) {
+          const uint4 x = lds128(place(i));
+          uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          float f[8];
 #pragma unroll
-      for (int tile = 0; tile < 2; ++tile) {
-        if (tile == 1 && !two_tiles) break;
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c) {
-          uint32_t w[4] = {x[tile][c].x, x[tile][c].y, x[tile][c].z, x[tile][c].w};
-          if constexpr (C::kQuant) {
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              f[2 * e] = __uint_as_float(w[e] << 16) * q_mul;
-              f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u) * q_mul;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = FMT == PDS_KV_INT4 ? pack_f16x2(f[e], f[e + 4])
-                                        : pack_f16x2(f[2 * e], f[2 * e + 1]);
+          for (int e = 0; e < 4; ++e) {
+            f[2 * e] = __uint_as_float(w[e] << 16) * q_mul;
+            f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u) * q_mul;
           }
-          st_shared_u4(sbase + C::kQ + tile * C::kQTile +
-                           tile_at<128>(tid >> 1, (tid & 1) * kPieces + c),
-                       w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = FMT == PDS_KV_INT4 ? pack_f16x2(f[e], f[e + 4])
+                                      : pack_f16x2(f[2 * e], f[2 * e + 1]);
+          st_shared_u4(place(i), w[0], w[1], w[2], w[3]);
         }
       }
       fence_proxy_async_smem();
@@ -853,13 +868,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     if (!two_tiles && ok && warp_live) {
 #pragma unroll 1
-      for (int c = 0; c < HD / 64; ++c) {
-        float o[32];
-        tmem_load32(to + (s == 0 ? HD / 2 : 0) + c * 32, o);
+      for (int c = 0; c < HD / 32; ++c) {
+        float o[16];
+        tmem_load16(to + (s == 0 ? HD / 2 : 0) + c * 16, o);
         const bool none = n_mine == 0;  // its accumulator was never written
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-          st_shared_f4(xch + s * (64u * HD * 4u) + xch_at(8 * c + x),
+        for (int x = 0; x < 4; ++x)
+          st_shared_f4(xch + s * (64u * HD * 4u) + xch_at(4 * c + x),
                        none ? make_float4(0.f, 0.f, 0.f, 0.f)
                             : make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
       }
@@ -890,13 +905,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       float4* out = reinterpret_cast<float4*>(a.o_part) +
                     (static_cast<int64_t>(blockIdx.x) * (a.tile_rows / 128) + half) * (HD / 4) * 128;
 #pragma unroll 1
-      for (int c = c0; c < c1; c += 32) {
-        float o[32];
-        tmem_load32(to + c, o);
+      for (int c = c0; c < c1; c += 16) {
+        float o[16];
+        tmem_load16(to + c, o);
         if (!two_tiles) {
           const bool none = n_mine == 0;
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
+          for (int x = 0; x < 4; ++x) {
             const float4 y = ld_shared_f4(xch + (1 - s) * (64u * HD * 4u) +
                                           xch_at((c - s * (HD / 2)) / 4 + x));
             const float v[4] = {y.x, y.y, y.z, y.w};
@@ -908,14 +923,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         } else if (C::kQuant) {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] *= mine_f;
+          for (int x = 0; x < 16; ++x) o[x] *= mine_f;
         }
         if constexpr (FMT == PDS_KV_INT4) {  // the channels back in their order
-          float y[32];
+          float y[16];
 #pragma unroll
-          for (int x = 0; x < 32; ++x) y[x] = o[(x & 24) + ((x & 3) << 1) + ((x >> 2) & 1)];
+          for (int x = 0; x < 16; ++x) y[x] = o[(x & 8) + ((x & 3) << 1) + ((x >> 2) & 1)];
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = y[x];
+          for (int x = 0; x < 16; ++x) o[x] = y[x];
         }
         if constexpr (!C::kQuant) {
           if (*poison && row_live) {  // what the loaders took out, for the rows that see it
@@ -931,7 +946,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                       a.c.v + u.seq * a.c.seq_stride + head * a.c.head_stride +
                       (key0 + 32 * g + x) * a.c.row_stride) + c;
 #pragma unroll
-                  for (int e = 0; e < 32; ++e)
+                  for (int e = 0; e < 16; ++e)
                     if ((v[e] & 0x7f80u) == 0x7f80u) o[e] += bf16_to_f32(v[e]);
                 }
               }
@@ -940,17 +955,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         if (!row_live) continue;
         if (whole) {
-          uint32_t y[16];
+          uint32_t y[8];
 #pragma unroll
-          for (int x = 0; x < 16; ++x)
+          for (int x = 0; x < 8; ++x)
             y[x] = pad ? 0u : pack_bf16x2(o[2 * x] * inv, o[2 * x + 1] * inv);
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
+          for (int x = 0; x < 2; ++x)
             reinterpret_cast<uint4*>(dst + c)[x] =
                 make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]);
         } else {
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
+          for (int x = 0; x < 4; ++x)
             out[(c / 4 + x) * 128 + r] =
                 pad ? make_float4(0.f, 0.f, 0.f, 0.f)
                     : make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
