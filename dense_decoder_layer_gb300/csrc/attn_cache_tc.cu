@@ -242,6 +242,19 @@ __device__ __forceinline__ bool part_hidden(const Args& a, int key0, int keys, i
   return key0 + keys > len || (a.window > 0 && key0 < len + a.n_tokens - a.window);
 }
 
+// mbar_try_wait that may sleep up to `ns` (a hint) before it answers no: a warp
+// that polls takes issue slots from those that work.
+__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
 // The bounded wait of a converged warp; every lane returns the same.  Short on
 // purpose: a block runs most of its code once and has to fetch it first, some
 // hundred cycles per 128 bytes, and this appears in twenty places.
@@ -252,7 +265,7 @@ __device__ __forceinline__ bool warp_wait(bool ok, uint32_t bar, uint32_t parity
     const uint64_t t0 = sm100::global_timer_ns();
     ok = false;
     do {
-      if (sm100::mbar_try_wait(bar, parity)) {
+      if (mbar_try_wait_for(bar, parity, 100000u)) {
         ok = true;
         break;
       }
@@ -620,31 +633,47 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // much as its latencies.)
     if (n > 0) {
       constexpr int kPieces = HD / 8;
-      const int pieces = (two_tiles ? 2 : 1) * 128 * kPieces;
-      auto place = [&](int i) {
-        return sbase + C::kQ + (i / (128 * kPieces)) * C::kQTile +
-               tile_at<128>((i / kPieces) & 127, i % kPieces);
+      constexpr int kStep = kSoftmaxThreads / kPieces;  // rows from one piece of a thread to its next
+      static_assert(kStep % 8 == 0, "a thread's pieces are swizzled alike");
+      const int q_rows = two_tiles ? 256 : 128, row0 = tid / kPieces, col = tid % kPieces;
+      const uint32_t at0 = sbase + C::kQ + tile_at<128>(row0, col);
+      auto place = [&](int row) {  // of this thread's piece of row `row`
+        return at0 + static_cast<uint32_t>(row >> 7) * C::kQTile +
+               static_cast<uint32_t>((row & 127) - row0) * 128u;
       };
+      const uint16_t* src = a.q + static_cast<int64_t>(u.seq) * a.n_tokens * a.q_stride +
+                            head * a.group * HD + col * 8;
 #pragma unroll 4
-      for (int i = tid; i < pieces; i += kSoftmaxThreads) {
-        const int R = r0 + i / kPieces;
+      for (int row = row0; row < q_rows; row += kStep) {
+        const int R = r0 + row;
         const bool live = R < rows;  // rows past the last are zero
         const int t = live ? token_of(a, R) : 0, h = live ? R - t * a.group : 0;
-        copy16(place(i), a.q + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.q_stride +
-                             (head * a.group + h) * HD + (i % kPieces) * 8, live);
+        copy16(place(row), src + t * a.q_stride + h * HD, live);
       }
       copies_commit();
       copies_wait<0>();
       if constexpr (C::kQuant) {
-        uint32_t top = 0u;  // bits of the largest finite |value|
+        // bits of the largest |value|, two at a time; over again without the
+        // infinities and NaN if there are any
+        uint32_t pair = 0u;
 #pragma unroll 4
-        for (int i = tid; i < pieces; i += kSoftmaxThreads) {
-          const uint4 x = lds128(place(i));
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        for (int row = row0; row < q_rows; row += kStep) {
+          const uint4 x = lds128(place(row));
+          pair = __vmaxu2(pair, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                         __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+        }
+        uint32_t top = max(pair & 0xffffu, pair >> 16) << 16;
+        if (__any_sync(0xffffffffu, top >= 0x7f800000u)) {
+          top = 0u;
+#pragma unroll 1
+          for (int row = row0; row < q_rows; row += kStep) {
+            const uint4 x = lds128(place(row));
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            top = max(top, max(finite_bits(__uint_as_float(w[e] << 16)),
-                               finite_bits(__uint_as_float(w[e] & 0xffff0000u))));
+            for (int e = 0; e < 4; ++e)
+              top = max(top, max(finite_bits(__uint_as_float(w[e] << 16)),
+                                 finite_bits(__uint_as_float(w[e] & 0xffff0000u))));
+          }
         }
         uint32_t* q_max = reinterpret_cast<uint32_t*>(smem + C::kQMax);
         top = __reduce_max_sync(0xffffffffu, top);
@@ -655,8 +684,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         float inverse;
         const float q_mul = q_multiplier(top, inverse);
 #pragma unroll 4
-        for (int i = tid; i < pieces; i += kSoftmaxThreads) {
-          const uint4 x = lds128(place(i));
+        for (int row = row0; row < q_rows; row += kStep) {
+          const uint4 x = lds128(place(row));
           uint32_t w[4] = {x.x, x.y, x.z, x.w};
           float f[8];
 #pragma unroll
@@ -668,7 +697,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int e = 0; e < 4; ++e)
             w[e] = FMT == PDS_KV_INT4 ? pack_f16x2(f[e], f[e + 4])
                                       : pack_f16x2(f[2 * e], f[2 * e + 1]);
-          st_shared_u4(place(i), w[0], w[1], w[2], w[3]);
+          st_shared_u4(place(row), w[0], w[1], w[2], w[3]);
         }
       }
       fence_proxy_async_smem();
