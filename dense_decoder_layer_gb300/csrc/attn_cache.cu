@@ -110,6 +110,17 @@ struct Fmt {
     return (r >> 2) * 128 + ((((r & 3) * 2 + c) ^ (((r >> 2) & 1) << 1)) << 4);
   }
 
+  // A step's copy: piece x of a lane is row kRowsPerPiece x + lane / kChunks, chunk
+  // lane % kChunks.  From one piece to the next its place moves by a constant,
+  // but for the bits of V's permutation that depend on x alone.
+  static constexpr int kRowsPerPiece = 32 / kChunks;
+  static constexpr int kPieces = kStep / kRowsPerPiece;
+  static constexpr uint32_t kPieceBytes = kRowsPerPiece * kRow;
+  static constexpr uint32_t v_piece_xor(int x) {
+    return FMT == PDS_KV_BF16 ? (HD == 128 ? (x & 3) << 5 : (x & 1) << 6)
+                              : kRow == 128 ? (x & 1) << 6 : 0;
+  }
+
   // The contraction runs over the head's channels in an order that lets a lane
   // read its share of a key's row with wide loads: in step ks the lane's quarter
   // t4 has the channels ch .. ch + 3 from this one on (4-bit rows: ch, ch + 4
@@ -345,35 +356,47 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 
   // this warp's steps: u.first + warp, + kWarps, ...
   const uint32_t ring = smem_addr(smem) + C::kRing + warp * C::kStages * F::kStage;
-  const char* k_base = a.c.k + u.seq * a.c.seq_stride + head * a.c.head_stride;
-  const char* v_base = a.c.v + u.seq * a.c.seq_stride + head * a.c.head_stride;
   const int64_t word0 = (static_cast<int64_t>(u.seq) * a.c.n_kv_heads + head) * a.c.capacity;
   const int n_mine = u.n_steps > warp ? (u.n_steps - warp - 1) / kWarps + 1 : 0;
-  auto fetch = [&](int i) {  // step i of this warp into stage i % kStages
-    if (i < n_mine) {
-      const int j0 = (u.first + warp + i * kWarps) * kStep;
-      const uint32_t st = ring + (i % C::kStages) * F::kStage;
+  // where this lane's pieces of the next step to fetch come from and go to
+  int row = (u.first + warp) * kStep + lane / F::kChunks;
+  const char* seq_k = a.c.k + u.seq * a.c.seq_stride + head * a.c.head_stride;
+  const char* seq_v = a.c.v + u.seq * a.c.seq_stride + head * a.c.head_stride;
+  int64_t off = row * a.c.row_stride + (lane % F::kChunks) * 16;
+  const int64_t piece_off = F::kRowsPerPiece * a.c.row_stride;
+  const uint32_t k_to = F::k_at(lane / F::kChunks, lane % F::kChunks);
+  const uint32_t v_to = F::kSlice + F::v_at(lane / F::kChunks, lane % F::kChunks);
+  int word_row = (u.first + warp) * kStep + (lane & 15);  // of this lane's scale word
+  const uint32_t* words = (lane < 16 ? a.c.k_scale : a.c.v_scale) + word0;
+  int fetched = 0;
+  uint32_t fetch_to = ring;
+  auto fetch = [&]() {  // the next step of this warp, into the next stage
+    if (fetched < n_mine) {
+      int64_t o = off;
 #pragma unroll
-      for (int x = 0; x < (kStep * F::kChunks + 31) / 32; ++x) {
-        const int idx = x * 32 + lane;
-        const int r = idx / F::kChunks, ch = idx - r * F::kChunks;
-        const bool live = j0 + r < end;
-        // a row past the end is not read: its address is that of the last one
-        const int64_t off = static_cast<int64_t>(live ? j0 + r : end - 1) * a.c.row_stride + ch * 16;
-        copy16(st + F::k_at(r, ch), k_base + off, live);
-        copy16(st + F::kSlice + F::v_at(r, ch), v_base + off, live);
+      for (int x = 0; x < F::kPieces; ++x) {
+        // a row past the end is not read: it is given the sequence's first address
+        const bool live = row + x * F::kRowsPerPiece < end;
+        const int64_t from = live ? o : 0;
+        copy16(fetch_to + x * F::kPieceBytes + k_to, seq_k + from, live);
+        copy16(fetch_to + x * F::kPieceBytes + (v_to ^ F::v_piece_xor(x)), seq_v + from, live);
+        o += piece_off;
       }
-      if constexpr (FMT != PDS_KV_BF16) {
-        const int r = lane & 15;
-        const bool live = j0 + r < end;
-        const uint32_t* src = (lane < 16 ? a.c.k_scale : a.c.v_scale) + word0;
-        copy4(st + 2 * F::kSlice + lane * 4, src + (live ? j0 + r : end - 1), live);
+      if constexpr (!F::kBf16) {
+        const bool live = word_row < end;
+        copy4(fetch_to + 2 * F::kSlice + lane * 4, words + (live ? word_row : 0), live);
+        word_row += kWarps * kStep;
       }
+      row += kWarps * kStep;
+      off += kWarps * kStep * a.c.row_stride;
+      ++fetched;
+      fetch_to += F::kStage;
+      if (fetch_to == ring + C::kStages * F::kStage) fetch_to = ring;
     }
     copies_commit();
   };
 #pragma unroll 1
-  for (int i = 0; i < C::kStages - 1; ++i) fetch(i);
+  for (int i = 0; i < C::kStages - 1; ++i) fetch();
 
   // Q as B fragments, in the contraction's channel order; rows past the last are zero
   constexpr int kQFrags = F::kKSteps * NT * 32;
@@ -488,12 +511,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 
   uint32_t v_exp = kMinScaleExp;  // exponent of the largest V scale so far: O's unit
   const uint32_t q_frag = smem_addr(smem) + C::kQ;
-  for (int i = 0; i < n_mine; ++i) {
+  uint32_t st = ring;  // the step's stage
+  int j0 = (u.first + warp) * kStep;
+  for (int i = 0; i < n_mine; ++i, j0 += kWarps * kStep) {
+    if (i > 0) st = st + F::kStage == ring + C::kStages * F::kStage ? ring : st + F::kStage;
     copies_wait<C::kStages - 2>();
     __syncwarp();
-    fetch(i + C::kStages - 1);  // into the stage that step i - 1 has been read from
-    const uint32_t st = ring + (i % C::kStages) * F::kStage;
-    const int j0 = (u.first + warp + i * kWarps) * kStep;
+    fetch();  // into the stage that the step before has been read from
 
     // scale words of this lane's keys: g, g + 8 (rows of S^T), and the zero
     // points that the operands need
