@@ -299,7 +299,11 @@ struct Cfg {
   // the warps' O rows are joined in the space of the ring
   static constexpr int kJoinStride = HD + 4;
   static constexpr int kJoin = kWarps * kRows * kJoinStride * 4;
-  static constexpr int kSmem = kRing + (kRingBytes > kJoin ? kRingBytes : kJoin);
+  // behind them, the block's rows for the other blocks of its cluster: O, (maximum, sum)
+  static constexpr int kShare = kRing + kJoin;
+  static constexpr int kShareMl = kShare + kRows * HD * 4;
+  static constexpr int kJoinEnd = kShareMl + kRows * 8;
+  static constexpr int kSmem = kRing + kRingBytes > kJoinEnd ? kRing + kRingBytes : kJoinEnd;
   static_assert(kSmem * kBlocks <= 228 * 1024 - 1024 * kBlocks, "shared memory per SM");
 };
 
@@ -320,12 +324,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
   int* shared_ok = reinterpret_cast<int*>(smem + C::kMisc + 48);
 
   const int per = a.c.n_kv_heads * a.row_tiles;
-  const int w = blockIdx.x / per, p = blockIdx.x - w * per;
+  const int chunk_unit = a.cluster > 1 ? blockIdx.x / a.cluster : blockIdx.x;
+  const int w = chunk_unit / per, p = chunk_unit - w * per;
   const int head = p % a.c.n_kv_heads, tile = p / a.c.n_kv_heads;
   sm100::grid_dep_wait();  // everything below reads what earlier kernels wrote
   sm100::grid_dep_launch();
   Unit u{};
-  if (a.c.n_seqs == 1) {
+  if (a.cluster > 1) {  // sequence w, in as many chunks as the cluster has blocks
+    int first;
+    const int n = seq_steps(a, w, first, u.len);
+    if (n == 0) {  // (all of the cluster's blocks leave)
+      if (p == 0 && threadIdx.x == 0) atomicOr(a.status, kStatusBadLength);
+      return;
+    }
+    const int c = (n + a.cluster - 1) / a.cluster, rank = blockIdx.x - chunk_unit * a.cluster;
+    u.seq = w;
+    u.n_chunks = a.cluster;
+    u.first = first + rank * c;
+    u.n_steps = max(0, min(c, n - rank * c));
+  } else if (a.c.n_seqs == 1) {
     const bool ok = only_unit(a, w, u);
     if (blockIdx.x == 0 && threadIdx.x == 0 && u.n_chunks == 0)
       atomicOr(a.status, kStatusBadLength);
@@ -757,7 +774,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
       sum = 0.f;
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    if (whole) {
+    if (a.cluster > 1) {
+      *reinterpret_cast<float4*>(smem + C::kShare + (r * HD + ch) * 4) = acc;
+      if (ch == 0) *reinterpret_cast<float2*>(smem + C::kShareMl + r * 8) = make_float2(m, sum);
+    } else if (whole) {
       const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // a row that sees nothing is zero
       uint16_t* dst = a.o + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.o_stride +
                       (head * a.group + i) * HD + ch;
@@ -769,6 +789,38 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
       if (ch == 0) a.ml_part[slot] = make_float2(m, sum);
     }
   }
+  if (a.cluster <= 1) return;
+  // The chunks of the cluster's blocks, in order: every block takes a share of
+  // the rows' pieces and reads the others' over distributed shared memory.
+  sm100::cluster_sync();
+  const uint32_t share = smem_addr(smem) + C::kShare, share_ml = smem_addr(smem) + C::kShareMl;
+  const int live_rows = min(rows - r0, C::kRows);
+  for (int idx = (blockIdx.x - chunk_unit * a.cluster) * kThreads + threadIdx.x;
+       idx < live_rows * (HD / 4); idx += a.cluster * kThreads) {
+    const int r = idx / (HD / 4), ch = (idx - r * (HD / 4)) * 4;
+    float m = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = 0; x < a.cluster; ++x) {
+      const float2 v = sm100::ld_cluster_f2(sm100::mapa_shared(share_ml + r * 8, x));
+      const float4 y = sm100::ld_cluster_f4(sm100::mapa_shared(share + (r * HD + ch) * 4, x));
+      const float m_new = fmaxf(m, v.x), mu = m_new == -INFINITY ? 0.f : m_new;
+      const float old = exp2_fast(m - mu), f = exp2_fast(v.x - mu);
+      m = m_new;
+      sum = sum * old + v.y * f;
+      acc.x = acc.x * old + y.x * f;
+      acc.y = acc.y * old + y.y * f;
+      acc.z = acc.z * old + y.z * f;
+      acc.w = acc.w * old + y.w * f;
+    }
+    const int t = token_of(a, r0 + r), i = r0 + r - t * a.group;
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    uint16_t* dst = a.o + (static_cast<int64_t>(u.seq) * a.n_tokens + t) * a.o_stride +
+                    (head * a.group + i) * HD + ch;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  }
+  sm100::cluster_sync();  // nobody leaves while its rows may still be read
 }
 
 // Four warps per (sequence, token, head) row: warp i joins chunks i, i + 4, ...,
@@ -882,6 +934,15 @@ int blocks_per_sm(int format, int hd, int nt) {  // Cfg::kBlocks
   return nt == kMaxTiles || (format == PDS_KV_BF16 && hd == 128) ? 1 : 2;
 }
 
+// Few short ranges: their chunks are the blocks of a cluster, which join them over
+// distributed shared memory, one launch instead of two and no workspace.  Up to
+// this many blocks, and this many chunks of the shortest length between them:
+// beyond, the two launches spread the keys over more SMs.  us with and without
+// clusters: 1 token, bf16, 1000 keys 5.6/6.3, 2048 5.9/6.2, 4000 7.2/6.9 (but a
+// launch less to issue), 8000 9.9/8.9; 4 sequences, int4, 1000 5.9/8.0, 4000 10.7/13.1.
+constexpr int kMaxCluster = 8;
+constexpr int kClusterChunks = 16;
+
 // More query rows per kv head than this go to the tensor-core kernel.
 constexpr int kTileMinRows = 33;
 
@@ -927,8 +988,8 @@ cudaError_t launch(const Args& a, int64_t grid, cudaStream_t st) {
   const cudaError_t ce = kernel_smem_attr(
       reinterpret_cast<const void*>(cache_attn_kernel<FMT, HD, NT, VAR>), C::kSmem);
   if (ce != cudaSuccess) return ce;
-  return launch_after(cache_attn_kernel<FMT, HD, NT, VAR>, dim3(static_cast<unsigned>(grid)),
-                      kThreads, C::kSmem, st, a);
+  return launch_after_cluster(cache_attn_kernel<FMT, HD, NT, VAR>,
+                              dim3(static_cast<unsigned>(grid)), kThreads, C::kSmem, a.cluster, st, a);
 }
 
 template <int FMT, int HD>
@@ -990,7 +1051,13 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
   const int64_t most_chunks = (span + least - 1) / least;
   const int64_t units = static_cast<int64_t>(c.n_seqs) * s.per;
   int64_t grid = units;
-  if (t.ws && most_chunks > 1) {
+  int cluster = 1;
+  while (cluster < kMaxCluster && cluster < most_chunks) cluster *= 2;
+  a.cluster = 1;
+  if (!s.tiles && cluster > 1 && most_chunks <= kClusterChunks && units * cluster <= s.slots) {
+    a.cluster = cluster;
+    grid = units * cluster;
+  } else if (t.ws && most_chunks > 1) {
     a.slots = s.slots;
     a.fit = s.fit;
     a.per_chunk = 1.0f / static_cast<float>(s.slots / s.per);

@@ -33,6 +33,7 @@ struct Args {
   int fit;                       // 1: choose chunks so that all units run at once
   float per_chunk;               // n_seqs == 1: 1 / (chunks that fit the slots)
   int min_steps;                 // shortest chunk, in steps
+  int cluster;                   // > 1: every sequence in this many chunks, one cluster's blocks
   float* o_part;                 // [unit][tile_rows][hd], each kernel in its own order
   float2* ml_part;               // [unit][tile_rows]: (maximum, sum)
   uint32_t* status;

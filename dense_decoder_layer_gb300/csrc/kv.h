@@ -59,20 +59,30 @@ struct TreeAttnCall {
 // memory.  Every kernel of the decoding path does and lets its successor begin
 // early in turn: a decode step is a row of kernels of a few microseconds, of
 // which a launch that waits for the end of its predecessor is a large part.
+// The grid in clusters of `cluster` blocks along x.
 template <typename... Params, typename... Given>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
-                         cudaStream_t st, Given&&... args) {
+cudaError_t launch_after_cluster(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                                 int cluster, cudaStream_t st, Given&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+template <typename... Params, typename... Given>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                         cudaStream_t st, Given&&... args) {
+  return launch_after_cluster(kernel, grid, threads, smem, 1, st, args...);
 }
 
 cudaError_t launch_rope(const RopeTurns& r, const uint16_t* x, uint16_t* y, int rows, int heads,

@@ -518,13 +518,13 @@ pds_status pds_cache_read(const pds_cache* cache, int32_t first_row, int32_t row
  *  q, o     bf16, token t of sequence s at element (s n_tokens + t) * q_stride
  *           (o_stride), [n_heads, head_dim] each (0: packed; multiples of 8).
  *           o may not overlap q.
- *  n_tokens 1 .. 256; n_heads a multiple of n_kv_heads.
+ *  n_tokens 1 .. 256; n_heads a multiple of n_kv_heads, at most 8192.
  *  max_len  an upper bound of lens known on the host, or 0 (the capacity less
  *           n_tokens); sizes the launch, not the result's meaning.  A longer
  *           sequence is refused as one that does not fit.
  *  workspace  >= pds_attention_tree_workspace_bytes(...) bytes, so that key
- *           ranges are split over all SMs, or NULL and 0 (every range on one
- *           SM).  Its content on entry does not matter; calls that may run at
+ *           ranges are split over all SMs, or NULL and 0 (long ranges stay on
+ *           one SM each).  Its content on entry does not matter; calls that may run at
  *           the same time need one each.  How ranges are split, and so the
  *           rounding of the result, depends on whether there is one, on
  *           max_len and on lens; the same call on the same inputs gives the
