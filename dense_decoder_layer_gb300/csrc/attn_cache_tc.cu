@@ -52,7 +52,7 @@ constexpr int kLoadWarps = 4, kLoadThreads = 32 * kLoadWarps;  // of K, and of V
 constexpr int kFirstLoadWarp = 4, kFirstSoftmaxWarp = kFirstLoadWarp + 2 * kLoadWarps;
 constexpr int kSoftmaxThreads = 256;   // 2 streams x 128 rows
 constexpr int kTileThreads = 32 * kFirstSoftmaxWarp + kSoftmaxThreads;
-constexpr float kMoveLog2 = 8.0f;      // the reference maximum follows beyond a growth of 2^8
+constexpr float kMoveSum = 256.0f;     // a tile's weights sum to more: the reference moves
 // registers per thread: 96 at launch; 384 threads give up 32 each for the 256
 // softmax threads' 48 more
 constexpr int kLeanRegs = 64, kSoftmaxRegs = 144;
@@ -95,7 +95,7 @@ struct TileCfg {
   static constexpr uint32_t kQMax = kPar + kMaxDraftTokens * 4u;  // Q's maximum per warp
   static constexpr uint32_t kUnitAt = kQMax + 64u;                // O's unit of each stream
   static constexpr uint32_t kBar = kUnitAt + 16u;
-  static constexpr int kNumBars = 1 + 2 * (kKStages + kVStages) + 14;
+  static constexpr int kNumBars = 2 + 2 * (kKStages + kVStages) + 14;
   static constexpr uint32_t kMisc = kBar + 8u * kNumBars;
   static constexpr size_t kSmem = 1024 + kMisc + 96;
   static_assert(kSmem <= 232448, "shared memory per block");
@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto bar_k_empty = [&](int st) { return bar0 + 8u * (1 + C::kKStages + st); };
   auto bar_v_full = [&](int st) { return bar0 + 8u * (1 + 2 * C::kKStages + st); };
   auto bar_v_empty = [&](int st) { return bar0 + 8u * (1 + 2 * C::kKStages + C::kVStages + st); };
+  const uint32_t bar_q_max = bar0 + 8u * (C::kNumBars - 1);  // (8- and 4-bit rows) Q's maximum
   constexpr int kBar2 = 1 + 2 * (C::kKStages + C::kVStages);
   // per stream s and score buffer b = i & 1 of its tile i, phase i >> 1: the
   // scores are there / P is there / O += P V has completed (a barrier per
@@ -320,6 +321,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const bool two_tiles = rows - r0 > kTileRows;  // the streams are row tiles, else key halves
   if (threadIdx.x == 0) {
     mbar_init(bar_q, kSoftmaxThreads / 32);
+    mbar_init(bar_q_max, kSoftmaxThreads / 32);
     for (int i = 0; i < C::kKStages; ++i) {
       mbar_init(bar_k_full(i), kLoadWarps);
       mbar_init(bar_k_empty(i), two_tiles ? 2 : 1);
@@ -500,10 +502,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       copies_commit();
     };
     if constexpr (!C::kQuant) {
-      // a tile is handed over once the next one's copy has been issued
+      // a tile is handed over once the copies of the next two have been issued
       int st = 0, st_done = 0;
       uint32_t phase = 1;  // of the stage's release; the first round passes at once
-      for (int t = 0; t <= n && ok; ++t) {
+      for (int t = 0; t <= n + 1 && ok; ++t) {
         if (t < n) {
           if (t >= stages) wait(empty0 + 8u * st, phase);
           issue(t, tiles_at + st * C::kTile, 0);
@@ -511,9 +513,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         } else {
           copies_commit();
         }
-        if (t == 0) continue;
-        copies_wait<1>();
-        if (is_v && part_hidden(a, (u.first + t - 1) * kKeys, kKeys, len)) {
+        if (t < 2) continue;
+        copies_wait<2>();
+        if (is_v && part_hidden(a, (u.first + t - 2) * kKeys, kKeys, len)) {
           // Rows that some query rows must not see: an infinity or a NaN would
           // reach them through a zero weight.  It is taken out here and added
           // to the rows that do see it at the end.
@@ -545,8 +547,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       int st = 0, slot = 0;
       uint32_t phase = 1, v_exp = kMinScaleExp;
       float k_factor = a.scale_log2;
-      if (!is_v && n > 0) {  // Q's multiplier, once Q is there
-        wait(bar_q, 0);
+      if (!is_v && n > 0) {  // Q's multiplier, once its maximum is there
+        wait(bar_q_max, 0);
         uint32_t top = 0u;
         const uint32_t* q_max = reinterpret_cast<const uint32_t*>(smem + C::kQMax);
 #pragma unroll 1
@@ -690,7 +692,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         uint32_t* q_max = reinterpret_cast<uint32_t*>(smem + C::kQMax);
         top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) q_max[warp - kFirstSoftmaxWarp] = top;
+        if (lane == 0) {
+          q_max[warp - kFirstSoftmaxWarp] = top;
+          mbar_arrive(bar_q_max);
+        }
         named_bar_sync(1, kSoftmaxThreads);
 #pragma unroll 1
         for (int c = 0; c < kSoftmaxThreads / 32; ++c) top = max(top, q_max[c]);
@@ -794,8 +799,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       uint32_t unit = v_exp;
       if constexpr (C::kQuant) unit = lds32(words + 512u);
       float z[kKeys];
-      // scores less the reference, in powers of two; again if the reference moves
-      for (bool again = false;; again = true) {
+      // Scores less the reference, in powers of two, and their exponentials.  The
+      // maximum is only taken where the row has no reference yet or its weights
+      // have outgrown the old one, which their sum tells.
+      bool move = __any_sync(0xffffffffu, m_ref == -INFINITY || unit != v_exp);
+      float grown;
+      for (;;) {
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // masked scores give 0
         tmem_load64(ts, z);
         if (VAR && cap > 0.f) {
@@ -824,12 +833,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int x = 0; x < kKeys; ++x)
             if (!((vis[x >> 5] >> (x & 31)) & 1u)) z[x] = -INFINITY;
         }
-        if (again) break;
+        if (!move) {
+#pragma unroll
+          for (int x = 0; x < kKeys; ++x) z[x] = exp2_fast(z[x]);
+          float sum[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) sum[x] = z[x];
+#pragma unroll
+          for (int x = 1; x < kKeys / 8; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              add2(sum[2 * y], sum[2 * y + 1], z[8 * x + 2 * y], z[8 * x + 2 * y + 1]);
+          grown = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+          move = __any_sync(0xffffffffu, grown > kMoveSum);
+          if (!move) break;
+          continue;
+        }
+        move = false;
         const float mx = fmaxf(max32(z), max32(z + 32));
-        const bool move = (m_ref == -INFINITY ? mx > -INFINITY : mx > kMoveLog2) || unit != v_exp;
-        if (!__any_sync(0xffffffffu, move)) break;
         float alpha = 1.f;
-        if (m_ref == -INFINITY ? mx > -INFINITY : mx > kMoveLog2) {
+        if (m_ref == -INFINITY ? mx > -INFINITY : mx > 0.f) {
           const float m_new = m_use + mx;
           alpha = exp2_fast(m_ref - m_new);  // 0 from -inf
           m_ref = m_new;
@@ -854,17 +877,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if (!ok) break;
-#pragma unroll
-      for (int x = 0; x < kKeys; ++x) z[x] = exp2_fast(z[x]);
-      float sum[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) sum[x] = z[x];
-#pragma unroll
-      for (int x = 1; x < kKeys / 8; ++x)
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          add2(sum[2 * y], sum[2 * y + 1], z[8 * x + 2 * y], z[8 * x + 2 * y + 1]);
-      l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+      l += grown;
       if constexpr (C::kQuant) {
 #pragma unroll
         for (int x = 0; x < kKeys / 4; ++x) {
