@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // maximum is only taken where the row has no reference yet or its weights
       // have outgrown the old one, which their sum tells.
       bool move = __any_sync(0xffffffffu, m_ref == -INFINITY || unit != v_exp);
-      float grown;
+      float grown, pk[kKeys / 2];
       for (;;) {
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // masked scores give 0
         tmem_load64(ts, z);
@@ -834,20 +834,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (!((vis[x >> 5] >> (x & 31)) & 1u)) z[x] = -INFINITY;
         }
         if (!move) {
-#pragma unroll
-          for (int x = 0; x < kKeys; ++x) z[x] = exp2_fast(z[x]);
           float sum[8];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) sum[x] = z[x];
+          for (int x = 0; x < 8; ++x) sum[x] = 0.f;
 #pragma unroll
-          for (int x = 1; x < kKeys / 8; ++x)
+          for (int x = 0; x < kKeys / 8; ++x) {
+            float* y = z + 8 * x;
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              add2(sum[2 * y], sum[2 * y + 1], z[8 * x + 2 * y], z[8 * x + 2 * y + 1]);
+            for (int e = 0; e < 8; ++e) y[e] = exp2_fast(y[e]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) add2(sum[2 * e], sum[2 * e + 1], y[2 * e], y[2 * e + 1]);
+            if constexpr (!C::kQuant) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                pk[4 * x + e] = __uint_as_float(pack_bf16x2(y[2 * e], y[2 * e + 1]));
+            }
+          }
           grown = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
           move = __any_sync(0xffffffffu, grown > kMoveSum);
-          if (!move) break;
-          continue;
+          if (move) continue;
+          break;
         }
         move = false;
         const float mx = fmaxf(max32(z), max32(z + 32));
@@ -890,12 +896,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int x = 0; x < kKeys; ++x)
             if (!((vis[x >> 5] >> (x & 31)) & 1u)) z[x] = 0.f;
         }
-      }
-      float pk[32];
 #pragma unroll
-      for (int x = 0; x < 32; ++x)
-        pk[x] = __uint_as_float(C::kQuant ? pack_f16x2(z[2 * x], z[2 * x + 1])
-                                          : pack_bf16x2(z[2 * x], z[2 * x + 1]));
+        for (int x = 0; x < kKeys / 2; ++x)
+          pk[x] = __uint_as_float(pack_f16x2(z[2 * x], z[2 * x + 1]));
+      }
       tmem_store32(ts, pk);
       tc_fence_before();
       __syncwarp();
