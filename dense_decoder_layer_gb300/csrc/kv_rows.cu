@@ -72,8 +72,14 @@ __device__ __forceinline__ float2 pair_turn(const RopeTurns& r, int i, int64_t p
   const float d = rest * (kHalfTurn * 3.14159265358979f);
   return make_float2((c - s * d) * r.mscale, (s + c * d) * r.mscale * r.sign);
 }
+// Where pair i is in a table: the same pair of neighbouring units side by side, so
+// that the lanes of a head read neighbouring banks.
+__device__ __forceinline__ int turn_at(const RopeTurns& r, int i) {
+  return (i & 7) * (r.rot_dim >> 4) + (i >> 3);
+}
 __device__ __forceinline__ void fill_table(float2* table, const RopeTurns& r, int64_t pos) {
-  for (int i = threadIdx.x; i < r.rot_dim / 2; i += blockDim.x) table[i] = pair_turn(r, i, pos);
+  for (int i = threadIdx.x; i < r.rot_dim / 2; i += blockDim.x)
+    table[turn_at(r, i)] = pair_turn(r, i, pos);
 }
 
 // Turn the pairs of unit u (table in shared memory); a unit past rot_dim stays.
@@ -82,7 +88,7 @@ __device__ __forceinline__ void rotate_unit(Vec16& v, int u, const RopeTurns& r,
   if (16 * u >= r.rot_dim) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float2 cs = table[8 * u + i];
+    const float2 cs = table[i * (r.rot_dim >> 4) + u];
     const bool neox = r.layout == PDS_ROPE_NEOX;
     const float p = neox ? v.x[i] : v.x[2 * i], q = neox ? v.x[8 + i] : v.x[2 * i + 1];
     const float y0 = p * cs.x - q * cs.y, y1 = p * cs.y + q * cs.x;
@@ -97,10 +103,10 @@ __device__ __forceinline__ void rotate_unit(Vec16& v, int u, const RopeTurns& r,
 }
 
 // One block per ROWS rows (and slice of their units): a thread's units of all of
-// them are loaded before the table is made and while it is.  Four rows per block
-// when there are many (128 bytes per thread in flight; with one, a block's table
-// and barrier cost as much as its data: 8192 rows of 32 x 128 took 33.5 us), one
-// when there are few and latency counts.
+// them are loaded before the table is made and while it is.  Two rows per block
+// when there are many (us for 8192 / 2048 rows of 32 x 128 with one, two and four:
+// 24.4/5.7, 22.0/5.1, 24.6/5.8; one waits more for its table, four leave fewer
+// blocks per SM), one when there are few and latency counts.
 template <int ROWS>
 __global__ void __launch_bounds__(kRowThreads) rope_kernel(const uint16_t* x, uint16_t* y, int rows,
                                                            int heads, int hd, int64_t x_stride,
@@ -139,7 +145,7 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const uint16_t* x, ui
     if (ROWS > 1 && row >= rows) break;
     const int64_t pos = positions ? static_cast<int64_t>(positions[row])
                                   : static_cast<int64_t>(start_pos) + row;
-    table[k * kMaxTurnPairs + i - k * pairs] = pair_turn(r, i - k * pairs, pos);
+    table[k * kMaxTurnPairs + turn_at(r, i - k * pairs)] = pair_turn(r, i - k * pairs, pos);
   }
   __syncthreads();
   while (u < units) {
@@ -311,7 +317,9 @@ __global__ void __launch_bounds__(kRowThreads)
 
 // A block takes kReadRows rows (all heads) of one sequence's K or V: the scale
 // words of a head are adjacent rows, so a block uses most of each sector of
-// them that it fetches.
+// them that it fetches.  A thread's 16 channels are two pieces of 8, half a head
+// apart, so that a warp's stores lie side by side: 8 x 8192 rows of e4m3, 407 MB,
+// take 60.9 us (6.7 TB/s; with 16 adjacent channels 69.5), 8192 rows 9.5.
 constexpr int kReadRows = 16;
 
 template <int FMT, int HD>
@@ -350,19 +358,20 @@ __global__ void __launch_bounds__(kRowThreads)
       to[i] = -1;
       if (u >= total) continue;
       const int r = u / per_row, w = u - r * per_row;
-      const int h = w / kPerHead, ch = (w - h * kPerHead) * 16;
+      const int h = w / kPerHead, ch = (w - h * kPerHead) * 8;
       const int64_t j = j0 + r0 + r;
       const char* p = src + j * c.row_stride + h * c.head_stride;
       to[i] = ((static_cast<int64_t>(s) * rows + r0 + r) * c.n_kv_heads + h) * HD + ch;
       if constexpr (FMT == PDS_KV_BF16) {
         qa[i] = *reinterpret_cast<const uint4*>(p + 2 * ch);
-        qb[i] = *reinterpret_cast<const uint4*>(p + 2 * ch + 16);
+        qb[i] = *reinterpret_cast<const uint4*>(p + HD + 2 * ch);
       } else if constexpr (FMT == PDS_KV_E4M3) {
-        qa[i] = *reinterpret_cast<const uint4*>(p + ch);
+        const uint2 lo = *reinterpret_cast<const uint2*>(p + ch);
+        const uint2 hi = *reinterpret_cast<const uint2*>(p + HD / 2 + ch);
+        qa[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
       } else {
-        const uint2 q = *reinterpret_cast<const uint2*>(p + ch / 2);
-        qa[i].x = q.x;
-        qa[i].y = q.y;
+        qa[i].x = *reinterpret_cast<const uint32_t*>(p + ch / 2);
+        qa[i].y = *reinterpret_cast<const uint32_t*>(p + HD / 4 + ch / 2);
       }
       if constexpr (FMT != PDS_KV_BF16)
         word[i] = scales[(static_cast<int64_t>(s) * c.n_kv_heads + h) * c.capacity + j];
@@ -396,9 +405,8 @@ __global__ void __launch_bounds__(kRowThreads)
         lo = narrow8(x);
         hi = narrow8(x + 8);
       }
-      uint4* dst = reinterpret_cast<uint4*>(out + to[i]);
-      dst[0] = lo;
-      dst[1] = hi;
+      *reinterpret_cast<uint4*>(out + to[i]) = lo;
+      *reinterpret_cast<uint4*>(out + to[i] + HD / 2) = hi;
     }
   }
 }
@@ -431,9 +439,9 @@ cudaError_t launch_rope(const RopeTurns& r, const uint16_t* x, uint16_t* y, int 
   const int units = heads * (hd / 16);
   const int threads = round_threads(units);
   const int slices = std::min((units + threads - 1) / threads, 65535);
-  // many rows: enough blocks of four to fill the GPU several times
+  // many rows: enough blocks of two to fill the GPU
   if (rows >= kManyRows)
-    return launch_after(rope_kernel<4>, dim3((rows + 3) / 4), threads, 0, st, x, y, rows, heads, hd,
+    return launch_after(rope_kernel<2>, dim3((rows + 1) / 2), threads, 0, st, x, y, rows, heads, hd,
                         x_stride, y_stride, positions, start_pos, r);
   // few: the units of a row are spread over several blocks
   return launch_after(rope_kernel<1>, dim3(rows, slices), threads, 0, st, x, y, rows, heads, hd,
