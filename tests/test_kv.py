@@ -216,3 +216,11 @@ def test_yarn_keeps_fast_pairs_and_interpolates_slow_ones():
     t = np.random.default_rng(0).standard_normal((3, 2, 128))
     back = D.rotate(D.rotate(t, [1, 5, 70000], y), [1, 5, 70000], y, inverse=True)
     np.testing.assert_allclose(back, t, atol=1e-9)
+
+
+@needs_lib
+def test_more_heads_than_the_attention_takes_are_declined():
+    lib, c = pds.load(), _cache()
+    assert lib.pds_attention_tree(c, PTR, PTR, 1, 8194, 0, 0, None, 0.0, 0, 0, None, 0,
+                                  None) == pds.PDS_DECLINED
+    assert lib.pds_attention_tree_workspace_bytes(c, 1, 8194) == 0
