@@ -1057,7 +1057,7 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
   if (!s.tiles && cluster > 1 && most_chunks <= kClusterChunks && units * cluster <= s.slots) {
     a.cluster = cluster;
     grid = units * cluster;
-  } else if (t.ws && most_chunks > 1) {
+  } else if (t.ws && most_chunks > 1 && s.per < s.slots) {  // (else a range per SM at least)
     a.slots = s.slots;
     a.fit = s.fit;
     a.per_chunk = 1.0f / static_cast<float>(s.slots / s.per);

@@ -29,7 +29,8 @@ struct Args {
   int step_shift;                // log2 of the keys of a step
   int row_tiles;                 // blocks of query rows per (sequence, kv head)
   int tile_rows;                 // rows of one
-  int slots;                     // blocks to spread the chunks over; 0: one chunk each
+  int slots;                     // blocks to spread the chunks over, more than n_kv_heads x
+                                 // row_tiles; 0: one chunk each
   int fit;                       // 1: choose chunks so that all units run at once
   float per_chunk;               // n_seqs == 1: 1 / (chunks that fit the slots)
   int min_steps;                 // shortest chunk, in steps
@@ -87,7 +88,8 @@ __device__ __forceinline__ int chunk_steps(const Args& a, int lane, const Lane& 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     // at most slots + (sequences x per) units: every chunk but a sequence's last is whole
-    return max(a.min_steps, static_cast<int>((total * per + a.slots - 1) / a.slots));
+    return static_cast<int>(
+        min(1LL << 30, max(static_cast<long long>(a.min_steps), (total * per + a.slots - 1) / a.slots)));
   }
   float total = static_cast<float>(mine.n);
 #pragma unroll 1
@@ -136,8 +138,8 @@ __device__ __forceinline__ bool only_unit(const Args& a, int w, Unit& u) {
 
 // The sequence and chunk of the w-th chunk overall (w < 0: of sequence `seq`,
 // whole range).  False past the last one.  By one warp; every lane returns it.
-__device__ __forceinline__ bool find_unit(const Args& a, int c, int w, int seq, int lane, const Lane& mine,
-                          Unit& u) {
+__device__ __forceinline__ bool find_unit(const Args& a, int c, int w, int seq, int lane,
+                                          const Lane& mine, Unit& u) {
   int base = 0;
 #pragma unroll 1
   for (int s0 = 0; s0 < a.c.n_seqs; s0 += 32) {

@@ -237,3 +237,25 @@ def test_keys_alone_or_values_alone_are_read(fmt):
         assert pds.load().pds_cache_read(cache.c, 3, 30, *ptr, stream) == pds.PDS_OK
         cache.sync()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("fmt,n,t,h,hkv,hd,length", [
+    ("bf16", 1, 256, 256, 16, 64, 300), ("e4m3", 1, 256, 200, 50, 64, 700),
+    ("int4", 1, 1, 400, 400, 64, 600), ("bf16", 2, 2, 340, 340, 64, 900),
+    ("e4m3", 2, 200, 160, 8, 128, 400)])
+def test_more_heads_and_rows_than_run_at_once(fmt, n, t, h, hkv, hd, length):
+    """One sequence alone fills the GPU more than once: its ranges are not cut."""
+    kv = _kv()
+    rng = np.random.default_rng(h)
+    lens = [length, length // 3][:n]
+    cache, k64, v64 = _filled(kv, rng, fmt, n, length + t + 2, hkv, hd, lens)
+    q, q64 = _normal(rng, n, t, h, hd)
+    o = cache.attend(q)
+    cache.sync()
+    # the last kv head and the first, and within them two query heads
+    g = h // hkv
+    for kvh in (0, hkv - 1):
+        heads = [kvh * g, kvh * g + g - 1] if g > 1 else [kvh * g]
+        part = slice(kvh, kvh + 1)
+        _check(o[:, :, heads], q64[:, :, heads], k64[:, :, part], v64[:, :, part], lens)
+    assert torch.equal(o, cache.attend(q))
