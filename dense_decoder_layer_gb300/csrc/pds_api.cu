@@ -545,7 +545,7 @@ pds_status launched(const char* fn, cudaError_t ce) {
 
 pds_status pds_rope(const pds_rope_spec* spec, const uint16_t* x, uint16_t* y, int32_t rows,
                     int32_t n_heads, int32_t head_dim, int64_t x_stride, int64_t y_stride,
-                    const int32_t* positions, int32_t start_pos, int32_t inverse, void* stream) {
+                    const int32_t* positions, int32_t start_pos, int32_t inverse, void* stream) try {
   if (!spec || !x || !y) return fail(PDS_EINVAL, "pds_rope: NULL operand");
   if (rows < 1 || n_heads < 1 || head_dim < 1) return fail(PDS_EINVAL, "pds_rope: bad size");
   if (head_dim % 16 || head_dim > 256 || n_heads > (1 << 20))
@@ -567,12 +567,14 @@ pds_status pds_rope(const pds_rope_spec* spec, const uint16_t* x, uint16_t* y, i
   return launched("pds_rope", pds::launch_rope(turns, x, y, rows, n_heads, head_dim, x_stride,
                                                y_stride, positions, start_pos,
                                                static_cast<cudaStream_t>(stream)));
+} catch (...) {  // a message could not be allocated
+  return PDS_ENOMEM;
 }
 
 pds_status pds_cache_write(const pds_cache* cache, const pds_rope_spec* spec, const uint16_t* k,
                            const uint16_t* v, int32_t n_tokens, int64_t k_stride,
                            int64_t v_stride, const int32_t* parents, const int32_t* positions,
-                           void* stream) {
+                           void* stream) try {
   pds::CacheView view;
   pds_status rc = make_view("pds_cache_write", cache, &view);
   if (rc != PDS_OK) return rc;
@@ -601,10 +603,12 @@ pds_status pds_cache_write(const pds_cache* cache, const pds_rope_spec* spec, co
                   pds::launch_cache_write(view, cache->format, cache->head_dim, turns, k, v,
                                           n_tokens, k_stride, v_stride, parents, positions, status,
                                           static_cast<cudaStream_t>(stream)));
+} catch (...) {  // a message could not be allocated
+  return PDS_ENOMEM;
 }
 
 pds_status pds_cache_read(const pds_cache* cache, int32_t first_row, int32_t rows,
-                          uint16_t* k_out, uint16_t* v_out, void* stream) {
+                          uint16_t* k_out, uint16_t* v_out, void* stream) try {
   pds::CacheView view;
   pds_status rc = make_view("pds_cache_read", cache, &view);
   if (rc != PDS_OK) return rc;
@@ -621,12 +625,14 @@ pds_status pds_cache_read(const pds_cache* cache, int32_t first_row, int32_t row
   return launched("pds_cache_read",
                   pds::launch_cache_read(view, cache->format, cache->head_dim, first_row, rows,
                                          k_out, v_out, status, static_cast<cudaStream_t>(stream)));
+} catch (...) {  // a message could not be allocated
+  return PDS_ENOMEM;
 }
 
 size_t pds_attention_tree_workspace_bytes(const pds_cache* cache, int32_t n_tokens,
                                           int32_t n_heads) {
   if (!cache || n_tokens < 1 || n_tokens > pds::kMaxDraftTokens || n_heads < 1 ||
-      cache->n_seqs < 1 || cache->n_seqs > 4096 || cache->n_kv_heads < 1 ||
+      n_heads > 8192 || cache->n_seqs < 1 || cache->n_seqs > 4096 || cache->n_kv_heads < 1 ||
       n_heads % cache->n_kv_heads || (cache->head_dim != 64 && cache->head_dim != 128))
     return 0;
   int dev = 0, sms = 0;
@@ -643,7 +649,7 @@ pds_status pds_attention_tree(const pds_cache* cache, const uint16_t* q, uint16_
                               int32_t n_tokens, int32_t n_heads, int64_t q_stride,
                               int64_t o_stride, const int32_t* parents, float softcap,
                               int32_t window, int32_t max_len, void* workspace,
-                              size_t workspace_bytes, void* stream) {
+                              size_t workspace_bytes, void* stream) try {
   pds::TreeAttnCall a{};
   pds_status rc = make_view("pds_attention_tree", cache, &a.cache);
   if (rc != PDS_OK) return rc;
@@ -691,6 +697,8 @@ pds_status pds_attention_tree(const pds_cache* cache, const uint16_t* q, uint16_
   rc = pds::tree_attention(a, static_cast<cudaStream_t>(stream), &err);
   if (rc != PDS_OK) return fail(rc, err);
   return PDS_OK;
+} catch (...) {  // a message could not be allocated
+  return PDS_ENOMEM;
 }
 
 }  // extern "C"
