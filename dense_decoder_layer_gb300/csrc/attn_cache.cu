@@ -29,6 +29,13 @@
 // Chunks write unnormalised rows and (maximum, sum) to the workspace; a second
 // kernel joins them in chunk order.  The chunk length is made from the
 // sequences' lengths on the device (they change between replays of a graph).
+//
+// Measured (32/8 heads of 128; replayed graphs, so without the host's part), one
+// token of 16 sequences of 4096 rows: bf16 44.5 us (6.0 TB/s), e4m3 29.7 (4.7),
+// 4-bit 31.3 (2.3): bf16 is bound by HBM, the others by the conversion's
+// instructions (the ALU pipe is the busiest, 38% and 56%) on the SMs that hold
+// two of the 256 blocks.  24/8 heads, one token over 2048 bf16 rows: 5.9 us, of
+// which some 4 are a launch, fetching the code and one round of loads.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -826,7 +833,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 // Four warps per (sequence, token, head) row: warp i joins chunks i, i + 4, ...,
 // and the first joins the four, in order.  The schedule is made while the
 // chunks are still being computed (lens were complete before those began), the
-// loads come after.
+// loads come after.  Bound by latency (lengths, schedule, one or two rounds of
+// loads): 5 us alone for 24 rows of 19 chunks, of which 2 to 3 remain behind the chunks.
 template <int HD>
 __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ Args a) {
   constexpr int kShare = 4;        // warps of a row
@@ -943,7 +951,10 @@ int blocks_per_sm(int format, int hd, int nt) {  // Cfg::kBlocks
 constexpr int kMaxCluster = 8;
 constexpr int kClusterChunks = 16;
 
-// More query rows per kv head than this go to the tensor-core kernel.
+// From this many query rows per kv head on, the tcgen05 kernel.  us here and there
+// for 8 sequences of 4096 rows, 24 rows: bf16 33.6/30.6, e4m3 33.3/35.9, 4-bit
+// 33.9/35.0; one sequence of 8192: 14.3/17.1, 14.1/18.1, 14.6/18.0.  36 rows (two
+// row tiles here): 45.5/31.2, 48.8/37.2, 53.4/36.2.
 constexpr int kTileMinRows = 33;
 
 struct Shape {
@@ -1041,6 +1052,8 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
   a.row_tiles = s.row_tiles;
   a.tile_rows = s.tile_rows;
   a.step_shift = s.step_shift;
+  // Two steps per warp, four tiles: with half 8 x 600 4-bit rows take 8.7 us
+  // instead of 7.0, with double one token over 600 e4m3 rows 5.8 instead of 4.8.
   a.min_steps = s.tiles ? 4 : 2 * kWarps;
   a.status = t.status;
   // a window's keys, with whole steps at both ends

@@ -73,7 +73,8 @@ __device__ __forceinline__ float2 pair_turn(const RopeTurns& r, int i, int64_t p
   return make_float2((c - s * d) * r.mscale, (s + c * d) * r.mscale * r.sign);
 }
 // Where pair i is in a table: the same pair of neighbouring units side by side, so
-// that the lanes of a head read neighbouring banks.
+// that the lanes of a head read neighbouring banks (with the pairs in order 8192
+// rows of 32 x 128 took 29.6 us instead of 24.6, four rows to a block).
 __device__ __forceinline__ int turn_at(const RopeTurns& r, int i) {
   return (i & 7) * (r.rot_dim >> 4) + (i >> 3);
 }
@@ -184,7 +185,9 @@ constexpr float kMinScale = 1.17549435e-38f;  // smaller scales are stored as 0
 
 // One block per new token: its Hkv K rows, then its Hkv V rows.  The loads of
 // the thread's first unit do not depend on the sequence's length, so they go
-// out before lens and the parents are read.
+// out before lens and the parents are read.  2048 tokens of 8 x 128, rotated and
+// stored as e4m3, 12.8 MB, take 7 us from Python, 8 single tokens as 4-bit 5: both
+// latency (loads, the turns, a head's extrema, stores) behind the host's call.
 template <int FMT, int HD>
 __global__ void __launch_bounds__(kRowThreads)
     cache_write_kernel(const __grid_constant__ CacheView c, const __grid_constant__ RopeTurns r,
