@@ -349,6 +349,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
     u.n_chunks = a.cluster;
     u.first = first + rank * c;
     u.n_steps = max(0, min(c, n - rank * c));
+  } else if (a.slots == 0) {
+    if (!whole_unit(a, w, u)) {
+      if (p == 0 && threadIdx.x == 0) atomicOr(a.status, kStatusBadLength);
+      return;
+    }
   } else if (a.c.n_seqs == 1) {
     const bool ok = only_unit(a, w, u);
     if (blockIdx.x == 0 && threadIdx.x == 0 && u.n_chunks == 0)

@@ -79,7 +79,6 @@ __device__ __forceinline__ Lane lane_steps(const Args& a, int s) {
 
 // Steps per chunk (the same for every sequence), by one warp.
 __device__ __forceinline__ int chunk_steps(const Args& a, int lane, const Lane& mine) {
-  if (a.slots == 0) return 1 << 30;
   const int per = a.c.n_kv_heads * a.row_tiles;
   if (!a.fit) {
     long long total = mine.n;
@@ -119,13 +118,10 @@ struct Unit {
 __device__ __forceinline__ bool only_unit(const Args& a, int w, Unit& u) {
   int first, len;
   const int n = seq_steps(a, 0, first, len);
-  int c = n;
-  if (a.slots > 0) {
-    const int most = a.slots / (a.c.n_kv_heads * a.row_tiles);
-    c = static_cast<int>(static_cast<float>(n) * a.per_chunk) + 1;
-    if (static_cast<long long>(c) * most < n) ++c;  // (the quotient was rounded)
-    c = max(c, a.min_steps);
-  }
+  const int most = a.slots / (a.c.n_kv_heads * a.row_tiles);
+  int c = static_cast<int>(static_cast<float>(n) * a.per_chunk) + 1;
+  if (static_cast<long long>(c) * most < n) ++c;  // (the quotient was rounded)
+  c = max(c, a.min_steps);
   u.seq = 0;
   u.len = len;
   u.base = 0;
@@ -134,6 +130,16 @@ __device__ __forceinline__ bool only_unit(const Args& a, int w, Unit& u) {
   u.first = first + u.chunk * c;
   u.n_steps = min(c, n - u.chunk * c);
   return u.chunk < u.n_chunks;
+}
+
+// Uncut sequences (slots == 0): the w-th is unit w, whether its length fits or not.
+// With the search below, which passes over the sequences 32 at a time, 1024
+// sequences of 200 e4m3 rows (8/2 heads) took 86 us instead of 39.
+__device__ __forceinline__ bool whole_unit(const Args& a, int w, Unit& u) {
+  u.seq = w;
+  u.n_steps = seq_steps(a, w, u.first, u.len);
+  u.n_chunks = u.n_steps > 0;
+  return u.n_chunks != 0;
 }
 
 // The sequence and chunk of the w-th chunk overall (w < 0: of sequence `seq`,

@@ -364,7 +364,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp == 0) {
     Unit u{};
     bool ok;
-    if (a.c.n_seqs == 1) {
+    if (a.slots == 0) {
+      ok = whole_unit(a, w, u);
+      if (!ok && p == 0 && lane == 0) atomicOr(a.status, kStatusBadLength);
+    } else if (a.c.n_seqs == 1) {
       ok = only_unit(a, w, u);
     } else {
       const Lane mine = lane_steps(a, lane);
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       *shared_unit = u;
       *shared_ok = ok;
     }
-    if (blockIdx.x == 0) {  // report lengths that do not fit
+    if (a.slots > 0 && blockIdx.x == 0) {  // report lengths that do not fit
       bool bad = false;
 #pragma unroll 1
       for (int s = lane; s < a.c.n_seqs; s += 32) bad |= lane_steps(a, s).n == 0;

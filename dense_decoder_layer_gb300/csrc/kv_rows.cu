@@ -58,19 +58,34 @@ __device__ __forceinline__ void unit_channels(int u, int rot_dim, int layout, in
 // fraction of a turn: position times a 64-bit fraction, modulo 2^64, is the
 // exact remainder modulo whole turns, so no position loses accuracy and no
 // 64-bit floating point is needed (its rate on this chip is a hundredth of
-// float32's).  What the conversion of the fraction's upper half to float32
-// rounds off (below 2^-25 of a turn) turns the pair by a first-order step.
+// float32's).  The nearest quarter turn comes off as an integer; what is left, at
+// most an eighth, becomes an angle xh + xl (Dekker's products), and sine and
+// cosine are their Taylor series with the rounding errors of the leading terms
+// added to the small ones: off by little more than their own last rounding.
 __device__ __forceinline__ float2 pair_turn(const RopeTurns& r, int i, int64_t pos) {
   const uint64_t turn = static_cast<uint64_t>(pos) * r.turns[i];
-  // signed: [-1/2, 1/2) of a turn; in half turns [-1, 1)
-  const int32_t hi = static_cast<int32_t>(turn >> 32);
+  const uint32_t quarter = static_cast<uint32_t>((turn + (1ull << 61)) >> 62) & 3u;
+  const int64_t rest = static_cast<int64_t>(turn - (static_cast<uint64_t>(quarter) << 62));
+  const int32_t hi = static_cast<int32_t>(rest >> 32);  // below 2^29
   const float f = __int2float_rn(hi);
-  const float rest = static_cast<float>(hi - static_cast<int32_t>(fminf(f, 2147483520.0f)));
-  constexpr float kHalfTurn = 4.656612873077393e-10f;  // 2^-31
-  float s, c;
-  sincospif(fminf(f, 2147483520.0f) * kHalfTurn, &s, &c);
-  const float d = rest * (kHalfTurn * 3.14159265358979f);
-  return make_float2((c - s * d) * r.mscale, (s + c * d) * r.mscale * r.sign);
+  const float low = static_cast<float>(hi - static_cast<int32_t>(f)) +
+                    __uint2float_rn(static_cast<uint32_t>(rest)) * 2.3283064365386963e-10f;
+  // 2 pi 2^-32 as the sum of two float32
+  constexpr double kTurn = 6.283185307179586476925 / 4294967296.0;
+  constexpr float kTurnHi = static_cast<float>(kTurn);
+  constexpr float kTurnLo = static_cast<float>(kTurn - static_cast<double>(kTurnHi));
+  const float xh = f * kTurnHi;
+  const float xl = __fmaf_rn(f, kTurnHi, -xh) + (f * kTurnLo + low * kTurnHi);
+  const float h = xh * xh, h_err = __fmaf_rn(xh, xh, -h);
+  const float one = 1.0f - 0.5f * h, one_err = (1.0f - one) - 0.5f * h;
+  const float odd = h * (-1.0f / 6 + h * (1.0f / 120 + h * (-1.0f / 5040 + h * (1.0f / 362880 -
+                                                                                h * (1.0f / 39916800)))));
+  const float even = h * h * (1.0f / 24 + h * (-1.0f / 720 + h * (1.0f / 40320 - h * (1.0f / 3628800))));
+  const float s = xh + (xh * odd + xl * one);
+  const float c = one + (one_err + (even - (0.5f * h_err + xl * xh)));
+  const float cc = quarter & 1u ? s : c, ss = quarter & 1u ? c : s;
+  const bool neg_c = quarter == 1u || quarter == 2u, neg_s = quarter >= 2u;
+  return make_float2((neg_c ? -cc : cc) * r.mscale, (neg_s ? -ss : ss) * r.mscale * r.sign);
 }
 // Where pair i is in a table: the same pair of neighbouring units side by side, so
 // that the lanes of a head read neighbouring banks (with the pairs in order 8192

@@ -259,3 +259,28 @@ def test_more_heads_and_rows_than_run_at_once(fmt, n, t, h, hkv, hd, length):
         part = slice(kvh, kvh + 1)
         _check(o[:, :, heads], q64[:, :, heads], k64[:, :, part], v64[:, :, part], lens)
     assert torch.equal(o, cache.attend(q))
+
+
+def test_turns_are_correct_to_float32():
+    """A key that is 1 in one channel becomes (cos, sin): the e4m3 row's scale is the larger of
+    the two, at least 2^-1/2, over 448.  0.76 units in the last place of a value below 1 are
+    1.08 2^-24 of it, the division rounds once more: in all below 2.25 2^-24."""
+    kv = _kv()
+    rng = np.random.default_rng(61)
+    t, hd = 250, 64
+    k = torch.zeros(1, t, hd // 2, hd, dtype=torch.bfloat16, device="cuda")
+    for i in range(hd // 2):
+        k[:, :, i, i] = 1.0
+    pos = rng.integers(0, 2 ** 31, t)
+    pos[:20] = np.arange(20)
+    cache = kv.KvCache("e4m3", 1, t, hd // 2, hd)
+    spec = kv.RopeSpec(5.0e5, hd)
+    cache.write(k, k, rope=spec, positions=_i32(pos[None]))
+    cache.sync()
+    angle = np.outer(pos.astype(np.longdouble), D.scaled_inv_freq(hd, 5.0e5).astype(np.longdouble))
+    want = np.maximum(np.abs(np.cos(angle)), np.abs(np.sin(angle))) / 448
+    got = cache.k_scale[0].T.cpu().numpy().astype(np.float64)
+    err = np.abs(got / want - 1)
+    near = pos < 2 ** 16  # there the float64 frequencies themselves are exact enough
+    assert np.all(err[near] <= 2.25 * 2.0 ** -24)
+    assert np.all(err <= 2.25 * 2.0 ** -24 + 2.0 ** 31 * 2.0 ** -52)
