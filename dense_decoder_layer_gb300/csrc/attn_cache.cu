@@ -359,6 +359,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
     if (blockIdx.x == 0 && threadIdx.x == 0 && u.n_chunks == 0)
       atomicOr(a.status, kStatusBadLength);
     if (!ok) return;
+  } else if (!a.fit) {
+    const Share h = block_share(a, smem + C::kRing);  // (the ring is not in use yet)
+    const bool ok = w < a.c.n_seqs ? first_unit(a, h, w, u)
+                                   : later_unit(a, h, w - a.c.n_seqs, lane, u);
+    if (!ok) {
+      if (w < a.c.n_seqs && p == 0 && threadIdx.x == 0) atomicOr(a.status, kStatusBadLength);
+      return;
+    }
+    __syncthreads();  // the ring may be filled
   } else {
     if (warp == 0) {
       const Lane mine = lane_steps(a, lane);
@@ -859,6 +868,10 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
   Unit u{};
   if (a.c.n_seqs == 1) {
     only_unit(a, -1, u);
+  } else if (!a.fit) {
+    __shared__ unsigned long long scratch[kShareScratch / 8];
+    const Share h = block_share(a, scratch);
+    if (h.any && seq < a.c.n_seqs) chunks_of(a, h, seq, lane, u);
   } else if (seq < a.c.n_seqs) {
     const Lane mine = lane_steps(a, lane);
     find_unit(a, chunk_steps(a, lane, mine), -1, seq, lane, mine, u);
@@ -866,10 +879,9 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
   // written by its block, or refused, or no such row
   const bool live = seq < a.c.n_seqs && u.n_chunks > 1;
   const int n_chunks = live ? u.n_chunks : 0;
-  const int64_t slot0 = (static_cast<int64_t>(u.base) * per + tile * a.c.n_kv_heads + head) *
-                            a.tile_rows + (r - tile * a.tile_rows) + (warp % kShare) * stride;
-  const float2* ml = a.ml_part + slot0;
-  const float* src = a.o_part + slot0 * HD + lane * kPer;
+  // of chunk x: the first apart from the others where there are many sequences
+  const int64_t slot0 = (static_cast<int64_t>(tile) * a.c.n_kv_heads + head) * a.tile_rows +
+                        (r - tile * a.tile_rows);
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
   float acc[kPer];
@@ -882,8 +894,11 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
     float y[kBatch][kPer];
 #pragma unroll
     for (int x = 0; x < kBatch; ++x) {
-      const bool have = x0 + x * kShare < n_chunks;
-      v[x] = have ? __ldcg(ml) : make_float2(-INFINITY, 0.f);
+      const int at = x0 + x * kShare;
+      const bool have = at < n_chunks;
+      const int64_t slot = slot0 + (at == 0 ? u.base : u.more + at) * stride;
+      const float* src = a.o_part + slot * HD + lane * kPer;
+      v[x] = have ? __ldcg(a.ml_part + slot) : make_float2(-INFINITY, 0.f);
       if constexpr (kPer == 4) {
         const float4 f = have ? __ldcg(reinterpret_cast<const float4*>(src))
                               : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -892,8 +907,6 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
         const float2 f = have ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
         y[x][0] = f.x, y[x][1] = f.y;
       }
-      ml += kShare * stride;
-      src += kShare * stride * HD;
     }
     float m_new = m;
 #pragma unroll

@@ -31,7 +31,8 @@ struct Args {
   int tile_rows;                 // rows of one
   int slots;                     // blocks to spread the chunks over, more than n_kv_heads x
                                  // row_tiles; 0: one chunk each
-  int fit;                       // 1: choose chunks so that all units run at once
+  int fit;                       // 1: choose chunks so that all units run at once; 0: there are
+                                 // more sequences than that
   float per_chunk;               // n_seqs == 1: 1 / (chunks that fit the slots)
   int min_steps;                 // shortest chunk, in steps
   int cluster;                   // > 1: every sequence in this many chunks, one cluster's blocks
@@ -77,19 +78,10 @@ __device__ __forceinline__ Lane lane_steps(const Args& a, int s) {
   return l;
 }
 
-// Steps per chunk (the same for every sequence), by one warp.
+// Steps per chunk (the same for every sequence) where all units run at once, by
+// one warp.
 __device__ __forceinline__ int chunk_steps(const Args& a, int lane, const Lane& mine) {
   const int per = a.c.n_kv_heads * a.row_tiles;
-  if (!a.fit) {
-    long long total = mine.n;
-#pragma unroll 1
-    for (int s = lane + 32; s < a.c.n_seqs; s += 32) total += lane_steps(a, s).n;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    // at most slots + (sequences x per) units: every chunk but a sequence's last is whole
-    return static_cast<int>(
-        min(1LL << 30, max(static_cast<long long>(a.min_steps), (total * per + a.slots - 1) / a.slots)));
-  }
   float total = static_cast<float>(mine.n);
 #pragma unroll 1
   for (int s = lane + 32; s < a.c.n_seqs; s += 32) total += static_cast<float>(lane_steps(a, s).n);
@@ -111,7 +103,7 @@ __device__ __forceinline__ int chunk_steps(const Args& a, int lane, const Lane& 
 
 struct Unit {
   int seq, chunk, n_chunks, first, n_steps, len;  // steps [first, first + n_steps)
-  int base;  // (chunk 0 of the sequence) among all chunks
+  int base, more;  // among all chunks: the sequence's first is `base`, its k-th more + k
 };
 
 // One sequence: its chunks by a few instructions, in every thread.
@@ -124,7 +116,7 @@ __device__ __forceinline__ bool only_unit(const Args& a, int w, Unit& u) {
   c = max(c, a.min_steps);
   u.seq = 0;
   u.len = len;
-  u.base = 0;
+  u.base = u.more = 0;
   u.n_chunks = n == 0 ? 0 : static_cast<int>(static_cast<unsigned>(n - 1) / static_cast<unsigned>(c)) + 1;
   u.chunk = max(w, 0);
   u.first = first + u.chunk * c;
@@ -164,7 +156,7 @@ __device__ __forceinline__ bool find_unit(const Args& a, int c, int w, int seq, 
       const int src = __ffs(hit) - 1;
       u.seq = s0 + src;
       u.n_chunks = __shfl_sync(0xffffffffu, chunks, src);
-      u.base = __shfl_sync(0xffffffffu, excl, src);
+      u.base = u.more = __shfl_sync(0xffffffffu, excl, src);
       u.len = __shfl_sync(0xffffffffu, l.len, src);
       const int f = __shfl_sync(0xffffffffu, l.first, src), m = __shfl_sync(0xffffffffu, l.n, src);
       u.chunk = w >= 0 ? w - u.base : 0;
@@ -175,6 +167,105 @@ __device__ __forceinline__ bool find_unit(const Args& a, int c, int w, int seq, 
     base = __shfl_sync(0xffffffffu, base + incl, 31);
   }
   return false;
+}
+
+// More sequences than run at once: only those longer than an average block's
+// share are cut, at the share.  Blocks 0 .. n_seqs have the first chunks, at once
+// and without a search (the lengths' sum apart); the others, of which there are
+// never more than fit the slots, follow.  (Found by a search over all sequences
+// the first chunks of 256 sequences of 1000 e4m3 rows, 32/8 heads, took 136 us.)
+struct Share {
+  int c;     // steps of a chunk
+  bool any;  // whether any sequence is longer
+};
+constexpr int kShareScratch = 64 * 12;  // bytes of shared memory, 8-byte aligned
+// By all threads of a block, with one barrier.
+__device__ __forceinline__ Share block_share(const Args& a, void* scratch) {
+  unsigned long long* sums = static_cast<unsigned long long*>(scratch);
+  unsigned* longest = reinterpret_cast<unsigned*>(sums + 64);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  unsigned long long sum = 0;
+  unsigned most = 0;
+#pragma unroll 1
+  for (int s = threadIdx.x; s < a.c.n_seqs; s += blockDim.x) {
+    const unsigned n = static_cast<unsigned>(lane_steps(a, s).n);
+    sum += n;
+    most = max(most, n);
+  }
+  auto reduce = [&]() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    most = __reduce_max_sync(0xffffffffu, most);
+  };
+  reduce();
+  if (lane == 0) {
+    sums[warp] = sum;
+    longest[warp] = most;
+  }
+  __syncthreads();
+  sum = lane < warps ? sums[lane] : 0ull;
+  most = lane < warps ? longest[lane] : 0u;
+  reduce();
+  // at most (slots + sequences x per) units: with c >= total per / slots (to within
+  // 2^-22) the sum of floor((n - 1) / c) is at most slots / per
+  const float share = __fdiv_rn(__fmul_rn(static_cast<float>(sum),
+                                          static_cast<float>(a.c.n_kv_heads * a.row_tiles)),
+                                static_cast<float>(a.slots));
+  const int c = max(a.min_steps, static_cast<int>(fminf(share, 1073741824.f)) + 1);
+  return Share{c, most > static_cast<unsigned>(c)};
+}
+// Chunk 0 of sequence w.
+__device__ __forceinline__ bool first_unit(const Args& a, const Share& h, int w, Unit& u) {
+  u.seq = w;
+  const int n = seq_steps(a, w, u.first, u.len);
+  u.n_chunks = n == 0 ? 0 : (n - 1) / h.c + 1;
+  u.n_steps = min(n, h.c);
+  return n != 0;
+}
+// The e-th of the chunks behind the first ones, by one warp.
+__device__ __forceinline__ bool later_unit(const Args& a, const Share& h, int e, int lane, Unit& u) {
+  if (!h.any) return false;
+  int base = 0;
+#pragma unroll 1
+  for (int s0 = 0; s0 < a.c.n_seqs; s0 += 32) {
+    const Lane l = lane_steps(a, s0 + lane);
+    const int chunks = l.n == 0 ? 0 : (l.n - 1) / h.c;
+    int incl = chunks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const int excl = base + incl - chunks;
+    const unsigned hit = __ballot_sync(0xffffffffu, e >= excl && e < excl + chunks);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const int k = e - __shfl_sync(0xffffffffu, excl, src) + 1;
+      const int f = __shfl_sync(0xffffffffu, l.first, src), n = __shfl_sync(0xffffffffu, l.n, src);
+      u.seq = s0 + src;
+      u.n_chunks = __shfl_sync(0xffffffffu, chunks, src) + 1;
+      u.len = __shfl_sync(0xffffffffu, l.len, src);
+      u.first = f + k * h.c;
+      u.n_steps = min(h.c, n - k * h.c);
+      return true;
+    }
+    base = __shfl_sync(0xffffffffu, base + incl, 31);
+  }
+  return false;
+}
+// Where the chunks of sequence `seq` are, by one warp.
+__device__ __forceinline__ void chunks_of(const Args& a, const Share& h, int seq, int lane, Unit& u) {
+  first_unit(a, h, seq, u);
+  u.base = seq;
+  u.more = 0;
+  if (u.n_chunks <= 1) return;
+  unsigned before = 0;
+#pragma unroll 1
+  for (int s = lane; s < seq; s += 32) {
+    const int n = lane_steps(a, s).n;
+    before += n == 0 ? 0 : (n - 1) / h.c;
+  }
+  u.more = a.c.n_seqs + static_cast<int>(warp_sum_uint(before)) - 1;
 }
 
 // ------------------------------------------------------------ instructions

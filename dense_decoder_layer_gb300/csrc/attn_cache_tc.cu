@@ -361,12 +361,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   grid_dep_wait();  // everything below reads what earlier kernels wrote
   grid_dep_launch();
+  const bool many = a.slots > 0 && a.c.n_seqs > 1 && !a.fit;
+  Share share{};
+  if (many) share = block_share(a, smem + C::kK);  // (nothing is there yet)
   if (warp == 0) {
     Unit u{};
     bool ok;
-    if (a.slots == 0) {
-      ok = whole_unit(a, w, u);
+    if (a.slots == 0 || (many && w < a.c.n_seqs)) {
+      ok = many ? first_unit(a, share, w, u) : whole_unit(a, w, u);
       if (!ok && p == 0 && lane == 0) atomicOr(a.status, kStatusBadLength);
+    } else if (many) {
+      ok = later_unit(a, share, w - a.c.n_seqs, lane, u);
     } else if (a.c.n_seqs == 1) {
       ok = only_unit(a, w, u);
     } else {
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       *shared_unit = u;
       *shared_ok = ok;
     }
-    if (a.slots > 0 && blockIdx.x == 0) {  // report lengths that do not fit
+    if (a.slots > 0 && !many && blockIdx.x == 0) {  // report lengths that do not fit
       bool bad = false;
 #pragma unroll 1
       for (int s = lane; s < a.c.n_seqs; s += 32) bad |= lane_steps(a, s).n == 0;
@@ -1070,10 +1075,22 @@ __global__ void __launch_bounds__(256) cache_join_tile_kernel(const __grid_const
   const int per = a.c.n_kv_heads * a.row_tiles;
   const int seq = blockIdx.x / per, p = blockIdx.x - seq * per;
   const int head = p % a.c.n_kv_heads, group_tile = p / a.c.n_kv_heads;
+  Share share{};
+  if (a.c.n_seqs > 1 && !a.fit) {
+    __shared__ unsigned long long scratch[kShareScratch / 8];
+    share = block_share(a, scratch);
+    if (!share.any) {
+      sm100::grid_dep_wait();
+      sm100::grid_dep_launch();
+      return;
+    }
+  }
   if (threadIdx.x < 32) {
     Unit u{};
     if (a.c.n_seqs == 1) {
       only_unit(a, -1, u);
+    } else if (!a.fit) {
+      chunks_of(a, share, seq, lane, u);
     } else {
       const Lane mine = lane_steps(a, lane);
       find_unit(a, chunk_steps(a, lane, mine), -1, seq, lane, mine, u);
@@ -1081,17 +1098,16 @@ __global__ void __launch_bounds__(256) cache_join_tile_kernel(const __grid_const
     if (lane == 0) shared_unit = u;
   }
   __syncthreads();
-  const int n_chunks = shared_unit.n_chunks, base = shared_unit.base;
+  const int n_chunks = shared_unit.n_chunks, base = shared_unit.base, more = shared_unit.more;
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
   const int r = threadIdx.x & 127, half = blockIdx.z;
   const int c4 = (blockIdx.y * 2 + (threadIdx.x >> 7)) * 2;  // of the row's float4 pieces
   const int R = group_tile * a.tile_rows + half * 128 + r, rows = a.n_tokens * a.group;
   if (n_chunks <= 1 || R >= rows) return;  // written by its block, or refused
-  const int64_t unit0 = static_cast<int64_t>(base) * per + p;
-  const float2* ml = a.ml_part + unit0 * a.tile_rows + half * 128 + r;
+  const float2* ml = a.ml_part + static_cast<int64_t>(p) * a.tile_rows + half * 128 + r;
   const float4* src = reinterpret_cast<const float4*>(a.o_part) +
-                      ((unit0 * (a.tile_rows / 128) + half) * (HD / 4) + c4) * 128 + r;
+                      ((static_cast<int64_t>(p) * (a.tile_rows / 128) + half) * (HD / 4) + c4) * 128 + r;
   const int64_t ml_step = static_cast<int64_t>(per) * a.tile_rows;
   const int64_t o_step = static_cast<int64_t>(per) * (a.tile_rows / 128) * (HD / 4) * 128;
   constexpr int kBatch = 6;  // chunks whose loads are in flight together
@@ -1104,7 +1120,8 @@ __global__ void __launch_bounds__(256) cache_join_tile_kernel(const __grid_const
     float4 y[kBatch][2];
 #pragma unroll
     for (int x = 0; x < kBatch; ++x) {
-      const int64_t at = x0 + x < n_chunks ? x0 + x : x0;
+      const int k = x0 + x < n_chunks ? x0 + x : x0;
+      const int64_t at = k == 0 ? base : more + k;
       v[x] = __ldcg(ml + at * ml_step);
       y[x][0] = __ldcg(src + at * o_step);
       y[x][1] = __ldcg(src + at * o_step + 128);

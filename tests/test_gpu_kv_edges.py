@@ -284,3 +284,44 @@ def test_turns_are_correct_to_float32():
     near = pos < 2 ** 16  # there the float64 frequencies themselves are exact enough
     assert np.all(err[near] <= 2.25 * 2.0 ** -24)
     assert np.all(err <= 2.25 * 2.0 ** -24 + 2.0 ** 31 * 2.0 ** -52)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int4"])
+@pytest.mark.parametrize("n,t,h,hkv,hd,window", [(170, 1, 4, 2, 64, 0), (80, 3, 8, 4, 128, 0),
+                                                 (45, 20, 8, 4, 64, 0), (400, 1, 1, 1, 128, 0),
+                                                 (90, 9, 8, 4, 64, 500)])
+def test_a_few_long_sequences_among_many(fmt, n, t, h, hkv, hd, window):
+    """More sequences than run at once: the long ones are cut, the one that does not fit is not
+    served, the others are right."""
+    from dense_decoder_layer_gb300 import pds
+    kv = _kv()
+    rng = np.random.default_rng(n)
+    cap = 5000
+    lens = rng.integers(0, 60, n)
+    lens[[1, n - 3]] = 4900, 2777
+    lens[n // 2] = 5000 - t
+    bad = n // 3
+    lens[bad] = cap - t + 1
+    lens = lens.tolist()
+    cache = kv.KvCache(fmt, n, cap, hkv, hd)
+    k, k64 = _normal(rng, 1, cap, hkv, hd)
+    v, v64 = _normal(rng, 1, cap, hkv, hd)
+    cache.write(k.expand(n, -1, -1, -1).contiguous(), v.expand(n, -1, -1, -1).contiguous())
+    if fmt != "bf16":
+        k64, v64 = (D.dequantise(_codes(x[:1], fmt), np.swapaxes(_words(w[:1]), 1, 2), fmt)
+                    for x, w in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+    cache.lens.copy_(_i32(lens))
+    q, q64 = _normal(rng, n, t, h, hd)
+    out = torch.full_like(q, 9.0)
+    cache.attend(q, out=out, window=window)
+    with pytest.raises(pds.PdsError):
+        cache.sync()
+    assert (out[bad] == 9.0).all()
+    k64, v64 = (np.broadcast_to(x, (n, *x.shape[1:])) for x in (k64, v64))
+    _check(out, q64, k64, v64, lens, window=window,
+           seqs=[0, 1, bad - 1, bad + 1, n // 2, n - 3, n - 2, n - 1])
+    again = torch.full_like(q, 9.0)
+    cache.attend(q, out=again, window=window)
+    assert torch.equal(out, again)
+    with pytest.raises(pds.PdsError):
+        cache.sync()
