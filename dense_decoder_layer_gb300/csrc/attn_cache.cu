@@ -857,100 +857,116 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
   __shared__ float part_o[8][HD];
   __shared__ float2 part_ml[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x * (8 / kShare) + warp / kShare;
   const int per_seq = a.n_tokens * a.n_heads;
-  const int seq = row / per_seq, rest = row - seq * per_seq;
-  const int t = rest / a.n_heads, h = rest - t * a.n_heads;
-  const int head = h / a.group, r = t * a.group + h - head * a.group;
-  const int tile = r / a.tile_rows;
   const int per = a.c.n_kv_heads * a.row_tiles;
   const int64_t stride = static_cast<int64_t>(per) * a.tile_rows;
-  Unit u{};
-  if (a.c.n_seqs == 1) {
-    only_unit(a, -1, u);
-  } else if (!a.fit) {
+  Share share{};
+  const bool many = a.c.n_seqs > 1 && !a.fit;
+  if (many) {
     __shared__ unsigned long long scratch[kShareScratch / 8];
-    const Share h = block_share(a, scratch);
-    if (h.any && seq < a.c.n_seqs) chunks_of(a, h, seq, lane, u);
-  } else if (seq < a.c.n_seqs) {
-    const Lane mine = lane_steps(a, lane);
-    find_unit(a, chunk_steps(a, lane, mine), -1, seq, lane, mine, u);
+    share = block_share(a, scratch);
+    if (!share.any) {  // (the wait still: what follows may count on the chunks too)
+      sm100::grid_dep_wait();
+      sm100::grid_dep_launch();
+      return;
+    }
   }
-  // written by its block, or refused, or no such row
-  const bool live = seq < a.c.n_seqs && u.n_chunks > 1;
-  const int n_chunks = live ? u.n_chunks : 0;
-  // of chunk x: the first apart from the others where there are many sequences
-  const int64_t slot0 = (static_cast<int64_t>(tile) * a.c.n_kv_heads + head) * a.tile_rows +
-                        (r - tile * a.tile_rows);
-  sm100::grid_dep_wait();
-  sm100::grid_dep_launch();
-  float acc[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-  float sum = 0.f, m = -INFINITY;
+  const int pairs = static_cast<int>((static_cast<int64_t>(a.c.n_seqs) * per_seq + 1) / 2);
 #pragma unroll 1
-  for (int x0 = warp % kShare; x0 < n_chunks; x0 += kBatch * kShare) {
-    float2 v[kBatch];
-    float y[kBatch][kPer];
+  for (int blk = blockIdx.x; blk < pairs; blk += gridDim.x) {
+    const int row = blk * (8 / kShare) + warp / kShare;
+    const int seq = row / per_seq, rest = row - seq * per_seq;
+    const int t = rest / a.n_heads, h = rest - t * a.n_heads;
+    const int head = h / a.group, r = t * a.group + h - head * a.group;
+    const int tile = r / a.tile_rows;
+    Unit u{};
+    if (a.c.n_seqs == 1) {
+      only_unit(a, -1, u);
+    } else if (many) {
+      if (seq < a.c.n_seqs) chunks_of(a, share, seq, lane, u);
+    } else if (seq < a.c.n_seqs) {
+      const Lane mine = lane_steps(a, lane);
+      find_unit(a, chunk_steps(a, lane, mine), -1, seq, lane, mine, u);
+    }
+    // written by its block, or refused, or no such row
+    const bool live = seq < a.c.n_seqs && u.n_chunks > 1;
+    const int n_chunks = live ? u.n_chunks : 0;
+    // of chunk x: the first apart from the others where there are many sequences
+    const int64_t slot0 = (static_cast<int64_t>(tile) * a.c.n_kv_heads + head) * a.tile_rows +
+                          (r - tile * a.tile_rows);
+    sm100::grid_dep_wait();
+    sm100::grid_dep_launch();
+    float acc[kPer];
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      const int at = x0 + x * kShare;
-      const bool have = at < n_chunks;
-      const int64_t slot = slot0 + (at == 0 ? u.base : u.more + at) * stride;
-      const float* src = a.o_part + slot * HD + lane * kPer;
-      v[x] = have ? __ldcg(a.ml_part + slot) : make_float2(-INFINITY, 0.f);
-      if constexpr (kPer == 4) {
-        const float4 f = have ? __ldcg(reinterpret_cast<const float4*>(src))
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-        y[x][0] = f.x, y[x][1] = f.y, y[x][2] = f.z, y[x][3] = f.w;
-      } else {
-        const float2 f = have ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
-        y[x][0] = f.x, y[x][1] = f.y;
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+    float sum = 0.f, m = -INFINITY;
+#pragma unroll 1
+    for (int x0 = warp % kShare; x0 < n_chunks; x0 += kBatch * kShare) {
+      float2 v[kBatch];
+      float y[kBatch][kPer];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const int at = x0 + x * kShare;
+        const bool have = at < n_chunks;
+        const int64_t slot = slot0 + (at == 0 ? u.base : u.more + at) * stride;
+        const float* src = a.o_part + slot * HD + lane * kPer;
+        v[x] = have ? __ldcg(a.ml_part + slot) : make_float2(-INFINITY, 0.f);
+        if constexpr (kPer == 4) {
+          const float4 f = have ? __ldcg(reinterpret_cast<const float4*>(src))
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+          y[x][0] = f.x, y[x][1] = f.y, y[x][2] = f.z, y[x][3] = f.w;
+        } else {
+          const float2 f = have ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
+          y[x][0] = f.x, y[x][1] = f.y;
+        }
+      }
+      float m_new = m;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) m_new = fmaxf(m_new, v[x].x);
+      const float mu = m_new == -INFINITY ? 0.f : m_new;
+      const float old = exp2_fast(m - mu);
+      m = m_new;
+      sum *= old;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] *= old;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const float f = exp2_fast(v[x].x - mu);  // 0 where there is none
+        sum += v[x].y * f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] += y[x][i] * f;
       }
     }
-    float m_new = m;
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) m_new = fmaxf(m_new, v[x].x);
-    const float mu = m_new == -INFINITY ? 0.f : m_new;
-    const float old = exp2_fast(m - mu);
-    m = m_new;
-    sum *= old;
+    for (int i = 0; i < kPer; ++i) part_o[warp][lane * kPer + i] = acc[i];
+    if (lane == 0) part_ml[warp] = make_float2(m, sum);
+    __syncthreads();
+    if (live && warp % kShare == 0) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] *= old;
+      for (int x = 0; x < kShare; ++x) m = fmaxf(m, part_ml[warp + x].x);
+      const float mu = m == -INFINITY ? 0.f : m;
+      sum = 0.f;
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      const float f = exp2_fast(v[x].x - mu);  // 0 where there is none
-      sum += v[x].y * f;
+      for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] += y[x][i] * f;
+      for (int x = 0; x < kShare; ++x) {
+        const float2 v = part_ml[warp + x];
+        const float f = exp2_fast(v.x - mu);
+        sum += v.y * f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] += part_o[warp + x][lane * kPer + i] * f;
+      }
+      const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+      uint16_t* dst =
+          a.o + (static_cast<int64_t>(seq) * a.n_tokens + t) * a.o_stride + h * HD + lane * kPer;
+      if constexpr (kPer == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                    pack_bf16x2(acc[2] * inv, acc[3] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
     }
+    __syncthreads();
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) part_o[warp][lane * kPer + i] = acc[i];
-  if (lane == 0) part_ml[warp] = make_float2(m, sum);
-  __syncthreads();
-  if (!live || warp % kShare) return;
-#pragma unroll
-  for (int x = 0; x < kShare; ++x) m = fmaxf(m, part_ml[warp + x].x);
-  const float mu = m == -INFINITY ? 0.f : m;
-  sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-#pragma unroll
-  for (int x = 0; x < kShare; ++x) {
-    const float2 v = part_ml[warp + x];
-    const float f = exp2_fast(v.x - mu);
-    sum += v.y * f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] += part_o[warp + x][lane * kPer + i] * f;
-  }
-  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-  uint16_t* dst = a.o + (static_cast<int64_t>(seq) * a.n_tokens + t) * a.o_stride + h * HD + lane * kPer;
-  if constexpr (kPer == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
-                                                pack_bf16x2(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
 }
 
 // ------------------------------------------------------------------ launch
@@ -1098,12 +1114,12 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
     a.ml_part = reinterpret_cast<float2*>(t.ws + static_cast<size_t>(most) * a.tile_rows *
                                                      t.head_dim * 4);
   }
-  cudaError_t ce = s.tiles ? launch_tile_attention(a, t.format, t.head_dim, grid, st)
+  cudaError_t ce = s.tiles ? launch_tile_attention(a, t.format, t.head_dim, grid, t.num_sms, st)
                    : t.head_dim == 128 ? launch_format<128>(a, t.format, s.nt, grid, st)
                                        : launch_format<64>(a, t.format, s.nt, grid, st);
   if (ce == cudaSuccess && a.slots > 0 && !s.tiles) {
     const int64_t rows = static_cast<int64_t>(c.n_seqs) * t.n_tokens * t.n_heads;
-    const dim3 blocks(static_cast<unsigned>((rows + 1) / 2));
+    const dim3 blocks(static_cast<unsigned>(std::min<int64_t>((rows + 1) / 2, 8 * t.num_sms)));
     ce = t.head_dim == 128 ? launch_after(cache_join_kernel<128>, blocks, 256, 0, st, a)
                            : launch_after(cache_join_kernel<64>, blocks, 256, 0, st, a);
   }

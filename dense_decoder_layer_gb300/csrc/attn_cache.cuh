@@ -390,7 +390,7 @@ __device__ __forceinline__ bool not_finite2(uint32_t w) {  // either bf16 of a p
 
 // The tensor-core kernel and its join (attn_cache_tc.cu): a step is 64 keys,
 // a.tile_rows 128 or 256 query rows per block, one block per SM.
-cudaError_t launch_tile_attention(const cacheattn::Args& a, int format, int hd, int64_t grid,
+cudaError_t launch_tile_attention(const cacheattn::Args& a, int format, int hd, int64_t grid, int num_sms,
                                   cudaStream_t st);
 
 }  // namespace pds

@@ -1073,89 +1073,93 @@ __global__ void __launch_bounds__(256) cache_join_tile_kernel(const __grid_const
   __shared__ Unit shared_unit;
   const int lane = threadIdx.x & 31;
   const int per = a.c.n_kv_heads * a.row_tiles;
-  const int seq = blockIdx.x / per, p = blockIdx.x - seq * per;
-  const int head = p % a.c.n_kv_heads, group_tile = p / a.c.n_kv_heads;
   Share share{};
   if (a.c.n_seqs > 1 && !a.fit) {
     __shared__ unsigned long long scratch[kShareScratch / 8];
     share = block_share(a, scratch);
-    if (!share.any) {
+    if (!share.any) {  // (the wait still: what follows may count on the chunks too)
       sm100::grid_dep_wait();
       sm100::grid_dep_launch();
       return;
     }
   }
-  if (threadIdx.x < 32) {
-    Unit u{};
-    if (a.c.n_seqs == 1) {
-      only_unit(a, -1, u);
-    } else if (!a.fit) {
-      chunks_of(a, share, seq, lane, u);
-    } else {
-      const Lane mine = lane_steps(a, lane);
-      find_unit(a, chunk_steps(a, lane, mine), -1, seq, lane, mine, u);
+#pragma unroll 1
+  for (int blk = blockIdx.x; blk < a.c.n_seqs * per; blk += gridDim.x) {
+    const int seq = blk / per, p = blk - seq * per;
+    const int head = p % a.c.n_kv_heads, group_tile = p / a.c.n_kv_heads;
+    if (threadIdx.x < 32) {
+      Unit u{};
+      if (a.c.n_seqs == 1) {
+        only_unit(a, -1, u);
+      } else if (!a.fit) {
+        chunks_of(a, share, seq, lane, u);
+      } else {
+        const Lane mine = lane_steps(a, lane);
+        find_unit(a, chunk_steps(a, lane, mine), -1, seq, lane, mine, u);
+      }
+      if (lane == 0) shared_unit = u;
     }
-    if (lane == 0) shared_unit = u;
-  }
-  __syncthreads();
-  const int n_chunks = shared_unit.n_chunks, base = shared_unit.base, more = shared_unit.more;
-  sm100::grid_dep_wait();
-  sm100::grid_dep_launch();
-  const int r = threadIdx.x & 127, half = blockIdx.z;
-  const int c4 = (blockIdx.y * 2 + (threadIdx.x >> 7)) * 2;  // of the row's float4 pieces
-  const int R = group_tile * a.tile_rows + half * 128 + r, rows = a.n_tokens * a.group;
-  if (n_chunks <= 1 || R >= rows) return;  // written by its block, or refused
-  const float2* ml = a.ml_part + static_cast<int64_t>(p) * a.tile_rows + half * 128 + r;
-  const float4* src = reinterpret_cast<const float4*>(a.o_part) +
-                      ((static_cast<int64_t>(p) * (a.tile_rows / 128) + half) * (HD / 4) + c4) * 128 + r;
-  const int64_t ml_step = static_cast<int64_t>(per) * a.tile_rows;
-  const int64_t o_step = static_cast<int64_t>(per) * (a.tile_rows / 128) * (HD / 4) * 128;
-  constexpr int kBatch = 6;  // chunks whose loads are in flight together
-  float acc[8];
+    __syncthreads();
+    const int n_chunks = shared_unit.n_chunks, base = shared_unit.base, more = shared_unit.more;
+    __syncthreads();
+    sm100::grid_dep_wait();
+    sm100::grid_dep_launch();
+    const int r = threadIdx.x & 127, half = blockIdx.z;
+    const int c4 = (blockIdx.y * 2 + (threadIdx.x >> 7)) * 2;  // of the row's float4 pieces
+    const int R = group_tile * a.tile_rows + half * 128 + r, rows = a.n_tokens * a.group;
+    if (n_chunks <= 1 || R >= rows) continue;  // written by its block, or refused
+    const float2* ml = a.ml_part + static_cast<int64_t>(p) * a.tile_rows + half * 128 + r;
+    const float4* src = reinterpret_cast<const float4*>(a.o_part) +
+                        ((static_cast<int64_t>(p) * (a.tile_rows / 128) + half) * (HD / 4) + c4) * 128 + r;
+    const int64_t ml_step = static_cast<int64_t>(per) * a.tile_rows;
+    const int64_t o_step = static_cast<int64_t>(per) * (a.tile_rows / 128) * (HD / 4) * 128;
+    constexpr int kBatch = 6;  // chunks whose loads are in flight together
+    float acc[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  float sum = 0.f, m = -INFINITY;
-  for (int x0 = 0; x0 < n_chunks; x0 += kBatch) {
-    float2 v[kBatch];
-    float4 y[kBatch][2];
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    float sum = 0.f, m = -INFINITY;
+    for (int x0 = 0; x0 < n_chunks; x0 += kBatch) {
+      float2 v[kBatch];
+      float4 y[kBatch][2];
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      const int k = x0 + x < n_chunks ? x0 + x : x0;
-      const int64_t at = k == 0 ? base : more + k;
-      v[x] = __ldcg(ml + at * ml_step);
-      y[x][0] = __ldcg(src + at * o_step);
-      y[x][1] = __ldcg(src + at * o_step + 128);
-    }
-    float m_new = m;
+      for (int x = 0; x < kBatch; ++x) {
+        const int k = x0 + x < n_chunks ? x0 + x : x0;
+        const int64_t at = k == 0 ? base : more + k;
+        v[x] = __ldcg(ml + at * ml_step);
+        y[x][0] = __ldcg(src + at * o_step);
+        y[x][1] = __ldcg(src + at * o_step + 128);
+      }
+      float m_new = m;
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) m_new = fmaxf(m_new, v[x].x);
-    const float mu = m_new == -INFINITY ? 0.f : m_new;
-    const float old = exp2_fast(m - mu);
-    m = m_new;
-    sum *= old;
+      for (int x = 0; x < kBatch; ++x) m_new = fmaxf(m_new, v[x].x);
+      const float mu = m_new == -INFINITY ? 0.f : m_new;
+      const float old = exp2_fast(m - mu);
+      m = m_new;
+      sum *= old;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] *= old;
+      for (int i = 0; i < 8; ++i) acc[i] *= old;
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      if (x0 + x >= n_chunks) break;
-      const float f = exp2_fast(v[x].x - mu);
-      sum += v[x].y * f;
+      for (int x = 0; x < kBatch; ++x) {
+        if (x0 + x >= n_chunks) break;
+        const float f = exp2_fast(v[x].x - mu);
+        sum += v[x].y * f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        acc[4 * i] += y[x][i].x * f;
-        acc[4 * i + 1] += y[x][i].y * f;
-        acc[4 * i + 2] += y[x][i].z * f;
-        acc[4 * i + 3] += y[x][i].w * f;
+        for (int i = 0; i < 2; ++i) {
+          acc[4 * i] += y[x][i].x * f;
+          acc[4 * i + 1] += y[x][i].y * f;
+          acc[4 * i + 2] += y[x][i].z * f;
+          acc[4 * i + 3] += y[x][i].w * f;
+        }
       }
     }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    const int t = token_of(a, R), i = R - t * a.group;
+    uint16_t* dst = a.o + (static_cast<int64_t>(seq) * a.n_tokens + t) * a.o_stride +
+                    (head * a.group + i) * HD + c4 * 4;
+    *reinterpret_cast<uint4*>(dst) =
+        make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                   pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
   }
-  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-  const int t = token_of(a, R), i = R - t * a.group;
-  uint16_t* dst = a.o + (static_cast<int64_t>(seq) * a.n_tokens + t) * a.o_stride +
-                  (head * a.group + i) * HD + c4 * 4;
-  *reinterpret_cast<uint4*>(dst) =
-      make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                 pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
 }
 
 template <int FMT, int HD, bool VAR>
@@ -1186,14 +1190,15 @@ cudaError_t launch_tile_format(const Args& a, int format, dim3 grid, cudaStream_
 
 }  // namespace
 
-cudaError_t launch_tile_attention(const Args& a, int format, int hd, int64_t grid,
+cudaError_t launch_tile_attention(const Args& a, int format, int hd, int64_t grid, int num_sms,
                                   cudaStream_t st) {
   const dim3 g(static_cast<unsigned>(grid));
   cudaError_t ce = hd == 128 ? launch_tile_format<128>(a, format, g, st)
                              : launch_tile_format<64>(a, format, g, st);
   if (ce != cudaSuccess || a.slots == 0) return ce;
-  const dim3 jg(static_cast<unsigned>(a.c.n_seqs) * a.c.n_kv_heads * a.row_tiles, hd / 16,
-                a.tile_rows / 128);
+  const int slices = hd / 16 * (a.tile_rows / 128);
+  const dim3 jg(std::min(a.c.n_seqs * a.c.n_kv_heads * a.row_tiles,
+                         std::max(1, 8 * num_sms / slices)), hd / 16, a.tile_rows / 128);
   return hd == 128 ? launch_after(cache_join_tile_kernel<128>, jg, 256, 0, st, a)
                    : launch_after(cache_join_tile_kernel<64>, jg, 256, 0, st, a);
 }
