@@ -492,20 +492,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t zero0 = sbase + C::kZero + (is_v ? C::kRaw * C::kZeroSlot : 0u) + tid * 4u;
     // copy tile t: bf16 rows to their places in the tile at `dst`, codes to this
     // thread's slots from `dst` on
+    static_assert(C::kQuant || kRowStep % 8 == 0, "a thread's pieces are swizzled alike");
+    const uint32_t piece0 = C::kQuant ? 0u : tile_at<64>(row0, col);
+    constexpr uint32_t kPieceStep = C::kQuant ? kLoadThreads * 16u : kRowStep * 128u;
+    const int64_t row_step = kRowStep * a.c.row_stride;
     auto issue = [&](int t, uint32_t dst, int slot) {
       if (t < n && ok) {
         const int key0 = (u.first + t) * kKeys;
+        const char* from = src0 + static_cast<int64_t>(key0 + row0) * a.c.row_stride;
+        const uint32_t* word = (is_v ? a.c.v_scale : a.c.k_scale) + word0 + key0 + row0;
+        const uint32_t zero = zero0 + slot * C::kZeroSlot;
+        if (key0 + kKeys <= end) {
 #pragma unroll
-        for (int i = 0; i < C::kPieces; ++i) {
-          const int r = row0 + i * kRowStep;
-          const bool live = key0 + r < end;
-          // a row past the end is not read: its address is that of the last one
-          const int64_t j = live ? key0 + r : end - 1;
-          copy16(C::kQuant ? dst + i * (kLoadThreads * 16u) : dst + tile_at<64>(r, col),
-                 src0 + j * a.c.row_stride, live);
-          if constexpr (FMT == PDS_KV_INT4)
-            copy4(zero0 + slot * C::kZeroSlot + i * (kLoadThreads * 4u),
-                  (is_v ? a.c.v_scale : a.c.k_scale) + word0 + j, live);
+          for (int i = 0; i < C::kPieces; ++i) {
+            copy16(dst + piece0 + i * kPieceStep, from, true);
+            from += row_step;
+            if constexpr (FMT == PDS_KV_INT4)
+              copy4(zero + i * (kLoadThreads * 4u), word + i * kRowStep, true);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < C::kPieces; ++i) {
+            // a row past the end is not read: its address is the sequence's first
+            const bool live = key0 + row0 + i * kRowStep < end;
+            copy16(dst + piece0 + i * kPieceStep, live ? from : src0, live);
+            from += row_step;
+            if constexpr (FMT == PDS_KV_INT4)
+              copy4(zero + i * (kLoadThreads * 4u),
+                    live ? word + i * kRowStep : word - (key0 + row0), live);
+          }
         }
         if (C::kQuant && !is_v) {  // the tile's scale words: K's by 64 threads, V's by 32
           const uint32_t at = sbase + C::kWords + (t % C::kWordTiles) * C::kWordSlot;
