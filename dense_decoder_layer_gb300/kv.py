@@ -61,6 +61,7 @@ def _rows(t, shape, n_lead, device, what):
         if size > 1:
             step = stride // count if step is None else step
             _need(stride == step * count, f"{what}: rows must be evenly spaced")
+            _need(step >= width, f"{what}: rows must not overlap (an expanded tensor?)")
         count *= size
     return width if step is None else step
 
@@ -160,6 +161,7 @@ class KvCache:
         self.k, self.v = have(k, shape, dtype, "k", False), have(v, shape, dtype, "v", False)
         packed = self.k.is_contiguous() and self.v.is_contiguous()
         _need(packed or self.k.stride() == self.v.stride(), "k and v: the same strides")
+        _need(packed or any(self.k.stride()[:3]), "k and v: rows of their own (an expanded tensor?)")
         self.k_scale = self.v_scale = None
         if word is not None:
             self.k_scale = have(k_scale, words, word, "k_scale", True)

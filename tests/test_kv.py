@@ -224,3 +224,21 @@ def test_more_heads_than_the_attention_takes_are_declined():
     assert lib.pds_attention_tree(c, PTR, PTR, 1, 8194, 0, 0, None, 0.0, 0, 0, None, 0,
                                   None) == pds.PDS_DECLINED
     assert lib.pds_attention_tree_workspace_bytes(c, 1, 8194) == 0
+
+
+def test_expanded_tensors_are_refused():
+    """Rows that share memory have stride 0, which to the C ABI says packed."""
+    torch = pytest.importorskip("torch")
+    from dense_decoder_layer_gb300 import kv
+
+    class Cuda(torch.Tensor):  # a host tensor that says it is on device 0
+        def get_device(self):
+            return 0
+
+    one = torch.empty(1, 1, 4, 64, dtype=torch.bfloat16)
+    for shape in ((2, 1, 4, 64), (1, 3, 4, 64), (2, 3, 4, 64)):
+        with pytest.raises(ValueError, match="overlap"):
+            kv._rows(one.expand(shape).as_subclass(Cuda), shape, 2, 0, "x")
+    row = torch.empty(1, 1, 1, 64, dtype=torch.bfloat16).expand(2, 8, 4, 64)
+    with pytest.raises(ValueError, match="expanded"):
+        kv.KvCache("bf16", 2, 8, 4, 64, k=row, v=row, lens=torch.zeros(2, dtype=torch.int32))
