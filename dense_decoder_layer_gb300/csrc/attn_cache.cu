@@ -1097,6 +1097,10 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
   const int64_t span = prefix + t.n_tokens;
   const int64_t least = static_cast<int64_t>(a.min_steps) << a.step_shift;
   const int64_t most_chunks = (span + least - 1) / least;
+  // One row tile's two streams take every other tile of keys: three each cost no
+  // more than a second chunk and the join (us uncut/cut for 4 sequences of 16 tokens,
+  // 32/8 heads of 64, over 350 rows: bf16 7.5/9.7, e4m3 9.1/10.8; over 550 10.2/10.2).
+  const int64_t uncut = s.tiles && s.tile_rows == 128 ? least + least / 2 : least;
   const int64_t units = static_cast<int64_t>(c.n_seqs) * s.per;
   int64_t grid = units;
   int cluster = 1;
@@ -1105,7 +1109,7 @@ pds_status tree_attention(const TreeAttnCall& t, cudaStream_t st, std::string* e
   if (!s.tiles && cluster > 1 && most_chunks <= kClusterChunks && units * cluster <= s.slots) {
     a.cluster = cluster;
     grid = units * cluster;
-  } else if (t.ws && most_chunks > 1 && s.per < s.slots) {  // (else a range per SM at least)
+  } else if (t.ws && span > uncut && s.per < s.slots) {  // (else a range per SM at least)
     a.slots = s.slots;
     a.fit = s.fit;
     a.per_chunk = 1.0f / static_cast<float>(s.slots / s.per);

@@ -10,8 +10,8 @@
 // at once.
 //
 // Measured (replayed graphs): 256 tokens of 32/8 heads of 128 over 8192 bf16 rows
-// 43.0 us (0.80 PFLOP/s), e4m3 56.3 (0.61); 64 tokens of 24/8 over 32768 4-bit rows
-// 51.0 (0.51); 32 tokens of 4 sequences over 16384 bf16 rows 50.8 (5.3 TB/s).  A
+// 43.8 us (0.79 PFLOP/s), e4m3 56.4 (0.61); 64 tokens of 24/8 over 32768 4-bit rows
+// 50.6 (0.51); 32 tokens of 4 sequences over 16384 bf16 rows 50.8 (5.3 TB/s).  A
 // tile of 64 keys for both streams takes ~1900 cycles with bf16 rows, ~2600 with
 // codes.  With the softmax taken out it takes ~1500 (products with 64 columns
 // read their 128 rows of Q from shared memory each time: 48 cycles where the
