@@ -837,11 +837,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       float z[kKeys];
       // Scores less the reference, in powers of two, and their exponentials.  The
       // maximum is only taken where the row has no reference yet or its weights
-      // have outgrown the old one, which their sum tells.
+      // have outgrown the old one, which their sum tells; at most once, because the
+      // weights behind it are at most one by construction: the reference is the
+      // largest of the rounded scores and is subtracted from these.  (The fused
+      // difference of the first pass also holds what the product's rounding drops,
+      // which from 2^28 on is above 8 now and then: as a measure of growth that
+      // would never end, from 2^31 on as a weight it would be nothing or infinite.)
       bool move = __any_sync(0xffffffffu, m_ref == -INFINITY || unit != v_exp);
+      bool rounded = move;
       float grown, pk[kKeys / 2];
-      for (;;) {
-        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // masked scores give 0
+#pragma unroll 1
+      for (int pass = 0; pass < 3; ++pass) {  // weights; the maximum; weights again
+        const float less = rounded ? 0.f : m_ref;
         tmem_load64(ts, z);
         if (VAR && cap > 0.f) {
 #pragma unroll
@@ -851,72 +858,79 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // c tanh(z / c) = c - 2 c / (2^(2 log2(e) z / c) + 1)
             const float y = z[x] * f;
             const float e = exp2_fast(y * (2.0f * 1.4426950408889634f / cap));
-            z[x] = cap - __fdividef(2.0f * cap, e + 1.0f) - m_use;
+            z[x] = cap - __fdividef(2.0f * cap, e + 1.0f) - less;
           }
         } else if constexpr (C::kQuant) {
 #pragma unroll
           for (int x = 0; x < kKeys / 4; ++x) {
             const float4 f = ld_shared_f4(words + x * 16);
-            fma2_pair(z[4 * x], z[4 * x + 1], f.x, f.y, -m_use);
-            fma2_pair(z[4 * x + 2], z[4 * x + 3], f.z, f.w, -m_use);
+            fma2_pair(z[4 * x], z[4 * x + 1], f.x, f.y, -less);
+            fma2_pair(z[4 * x + 2], z[4 * x + 3], f.z, f.w, -less);
           }
         } else {
 #pragma unroll
-          for (int x = 0; x < kKeys / 2; ++x) fma2(z[2 * x], z[2 * x + 1], sc, -m_use);
+          for (int x = 0; x < kKeys / 2; ++x) fma2(z[2 * x], z[2 * x + 1], sc, -less);
         }
         if (partial) {
 #pragma unroll
           for (int x = 0; x < kKeys; ++x)
             if (!((vis[x >> 5] >> (x & 31)) & 1u)) z[x] = -INFINITY;
         }
-        if (!move) {
-          float sum[8];
+        if (move) {
+          const float mx = fmaxf(max32(z), max32(z + 32));
+          float alpha = 1.f;
+          if (mx > m_ref) {
+            alpha = exp2_fast(m_ref - mx);  // 0 from -inf
+            m_ref = mx;
+            l *= alpha;
+          }
+          if (C::kQuant) {
+            alpha *= v_multiplier(unit) * v_inverse(v_exp);
+            v_exp = unit;
+          }
+          if (i > 0) {
+            // O at rest: the product of the tile before has completed
+            wait(bar_pv(s, b ^ 1), ((i - 1) >> 1) & 1);
+            if (!ok) break;
+#pragma unroll 1
+            for (int c = 0; c < HD / 16; ++c) {
+              float o[16];
+              tmem_load16(to + c * 16, o);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) sum[x] = 0.f;
-#pragma unroll
-          for (int x = 0; x < kKeys / 8; ++x) {
-            float* y = z + 8 * x;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = exp2_fast(y[e]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) add2(sum[2 * e], sum[2 * e + 1], y[2 * e], y[2 * e + 1]);
-            if constexpr (!C::kQuant) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                pk[4 * x + e] = __uint_as_float(pack_bf16x2(y[2 * e], y[2 * e + 1]));
+              for (int x = 0; x < 16; ++x) o[x] *= alpha;
+              tmem_store16(to + c * 16, o);
             }
           }
-          grown = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
-          move = __any_sync(0xffffffffu, grown > kMoveSum);
-          if (move) continue;
-          break;
+          move = false;
+          // (bf16 rows: held on from here beside O and P, the scores would not fit
+          // the registers, so they are loaded again)
+          if constexpr (!C::kQuant) continue;
         }
-        move = false;
-        const float mx = fmaxf(max32(z), max32(z + 32));
-        float alpha = 1.f;
-        if (m_ref == -INFINITY ? mx > -INFINITY : mx > 0.f) {
-          const float m_new = m_use + mx;
-          alpha = exp2_fast(m_ref - m_new);  // 0 from -inf
-          m_ref = m_new;
-          l *= alpha;
-        }
-        if (C::kQuant) {
-          alpha *= v_multiplier(unit) * v_inverse(v_exp);
-          v_exp = unit;
-        }
-        if (i > 0) {
-          // O at rest: the product of the tile before has completed
-          wait(bar_pv(s, b ^ 1), ((i - 1) >> 1) & 1);
-          if (!ok) break;
-#pragma unroll 1
-          for (int c = 0; c < HD / 16; ++c) {
-            float o[16];
-            tmem_load16(to + c * 16, o);
+        if (rounded) {
+          const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // masked scores give 0
 #pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] *= alpha;
-            tmem_store16(to + c * 16, o);
+          for (int x = 0; x < kKeys / 2; ++x) add2(z[2 * x], z[2 * x + 1], -m_use, -m_use);
+        }
+        float sum[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) sum[x] = 0.f;
+#pragma unroll
+        for (int x = 0; x < kKeys / 8; ++x) {
+          float* y = z + 8 * x;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = exp2_fast(y[e]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) add2(sum[2 * e], sum[2 * e + 1], y[2 * e], y[2 * e + 1]);
+          if constexpr (!C::kQuant) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              pk[4 * x + e] = __uint_as_float(pack_bf16x2(y[2 * e], y[2 * e + 1]));
           }
         }
+        grown = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+        if (rounded) break;
+        move = rounded = __any_sync(0xffffffffu, grown > kMoveSum);
+        if (!move) break;
       }
       if (!ok) break;
       l += grown;

@@ -1,0 +1,113 @@
+"""Cached decoding with values far from the ordinary.  Tolerances as in test_gpu_kv,
+whose helpers these tests use; what a test adds to them is derived beside it."""
+
+import math
+
+import numpy as np
+import pytest
+
+from oracle import decode as D
+from parity import bf16_to_f64
+from test_gpu_kv import EPS, _bf16, _filled, _i32, _kv, _normal
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+def _scales(cache):
+    """V's scales, float64 [n, Hkv, capacity]."""
+    w = cache.v_scale.view(torch.int32)
+    return (w & -65536 if cache.fmt == "int4" else w).view(torch.float32).double().cpu().numpy()
+
+
+def _close(cache, o, q64, k64, v64, length, parents=None, softcap=0.0, window=0, rows=None):
+    """One sequence's rows (all, or those listed) against the definition: test_gpu_kv's
+    tolerance, and over codes what fp16 drops.  A weight times its V scale is held in a
+    unit that gives the largest scale so far at least 64; below fp16's normal range it is off
+    by 2^-25 of that unit, and a row's weights sum to at least one: n 2^-31 of the largest scale
+    times the largest code for n keys."""
+    got = bf16_to_f64(o)[0]
+    want, size = D.tree_attention(q64[0], k64[0], v64[0], length, parents, softcap, window)
+    t, h, hd = got.shape
+    group = h // k64.shape[2]
+    floor = 0.0
+    if cache.fmt != "bf16":
+        scale = _scales(cache)[0][:, :length + t]
+        top = np.repeat(scale.max(-1), group)[None, :, None]
+        floor = (length + t) * 2.0 ** -31 * top * {"e4m3": 448, "int4": 15}[cache.fmt]
+    reach = np.abs(q64[0]) @ np.ones(hd) * np.abs(k64[0, :length + t]).max()
+    slack = (hd + 8) * 2.0 ** -23 * reach / math.sqrt(hd)
+    tol = EPS * np.abs(want) + (EPS + 2 * slack[..., None]) * size * 1.01 + floor
+    rows = range(t) if rows is None else rows
+    assert np.isfinite(got[rows]).all()
+    assert np.all((np.abs(got - want) <= tol)[rows]), float(np.max((np.abs(got - want) - tol)[rows]))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int4"])
+@pytest.mark.parametrize("t,h,hkv,hd", [(3, 4, 2, 128), (40, 4, 2, 128), (100, 6, 2, 64)])
+def test_large_finite_queries_take_the_best_key(fmt, t, h, hkv, hd):
+    """Scores so large that one key has all the weight, wherever it leads by more than the
+    scores' float32 rounding and by 40 besides (e^-40 is nothing next to a rounding).  Its
+    weight is rounded to bf16, its sum is not, and the result is rounded once more."""
+    kv = _kv()
+    rng = np.random.default_rng(t)
+    length = 400
+    cache, k64, v64 = _filled(kv, rng, fmt, 1, length + t, hkv, hd, [length])
+    k, v = k64[0], v64[0]
+    for size in (3e4, 1e7, 1e8, 4e8, 1e9, 1e10, 1e12, 1e20, 1e30, 1e35):
+        q, q64 = _normal(rng, 1, t, h, hd, scale=size)
+        o = bf16_to_f64(cache.attend(q))[0]
+        cache.sync()
+        decided = 0
+        for i in range(t):
+            rows = length + i + 1
+            for head in range(h):
+                g, x = head // (h // hkv), q64[0, i, head]
+                z = k[:rows, g] @ x / math.sqrt(hd)
+                reach = (np.abs(k[:rows, g]) @ np.abs(x)).max()
+                slack = (hd + 8) * 2.0 ** -23 * reach / math.sqrt(hd)
+                top, second = np.sort(z)[:-3:-1]
+                assert np.isfinite(o[i, head]).all()
+                if top - second > 2 * slack + 40:
+                    decided += 1
+                    want = v[z.argmax(), g]
+                    assert np.all(np.abs(o[i, head] - want) <=
+                                  2 * EPS * np.abs(want) + 2.0 ** -30 * np.abs(v).max())
+        assert decided > 0.8 * t * h
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int4"])
+@pytest.mark.parametrize("t", [3, 40, 150])
+def test_scores_far_apart_under_few_and_many_rows(fmt, t):
+    kv = _kv()
+    rng = np.random.default_rng(t + 1)
+    cache, k64, v64 = _filled(kv, rng, fmt, 1, 1500 + t, 2, 128, [1500], kscale=8.0)
+    q, q64 = _normal(rng, 1, t, 4, 128, scale=2.0)
+    o = cache.attend(q)
+    cache.sync()
+    _close(cache, o, q64, k64, v64, 1500)
+
+
+@pytest.mark.parametrize("fmt", ["bf16"])
+@pytest.mark.parametrize("t,h", [(6, 6), (40, 4), (100, 6)])
+def test_queries_of_padding_tokens_may_hold_anything(fmt, t, h):
+    kv = _kv()
+    rng = np.random.default_rng(t)
+    cache, k64, v64 = _filled(kv, rng, fmt, 1, 500 + t, 2, 64, [500])
+    parents = [[-1] + [int(rng.integers(max(-1, i - 5), i)) for i in range(1, t)]]
+    pad = [t - 1, t - 2, t // 2]
+    for i in pad:
+        parents[0] = [(-2 if j == i else -1 if p == i else p) for j, p in enumerate(parents[0])]
+    q, q64 = _normal(rng, 1, t, h, 64)
+    for fill in (1e8, 1e10, 1e20, 3e38, float("inf"), float("nan"), None):
+        if fill is None:  # bits as they come
+            bits = rng.integers(-2 ** 15, 2 ** 15, (len(pad), h, 64)).astype(np.int16)
+            q[0, pad] = torch.from_numpy(bits).cuda().view(torch.bfloat16)
+        else:
+            q[0, pad] = _bf16(fill * np.sign(rng.standard_normal((len(pad), h, 64))))[0]
+        o = cache.attend(q, parents=_i32(parents))
+        cache.sync()
+        assert (o[0, pad] == 0).all()
+        _close(cache, o, q64, k64, v64, 500, parents[0],
+               rows=[i for i in range(t) if i not in pad])
