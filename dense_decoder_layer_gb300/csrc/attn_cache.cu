@@ -299,8 +299,10 @@ struct Cfg {
   static constexpr int kDepth = kMask + kRows * kMaskWords * 4;
   static constexpr int kParent = kDepth + kMaxDraftTokens * 2;
   static constexpr int kMl = kParent + kMaxDraftTokens * 4;   // per warp and row: (maximum, sum)
-  static constexpr int kInv = kMl + kWarps * kRows * 8;       // per warp: O's unit; Q's maximum
-  static constexpr int kMisc = kInv + 2 * kWarps * 4;
+  static constexpr int kInv = kMl + kWarps * kRows * 8;       // per warp: O's unit
+  static constexpr int kQMax = kInv + kWarps * 4;             // per warp: Q's maximum in 8 rows
+  static constexpr int kQInv = kQMax + kWarps * 8 * 4;        // per row: the inverse of Q's multiplier
+  static constexpr int kMisc = (kQInv + kRows * 4 + 15) / 16 * 16;
   static constexpr int kRing = (kMisc + 64 + 127) / 128 * 128;
   static constexpr int kRingBytes = kWarps * kStages * F::kStage;
   // the warps' O rows are joined in the space of the ring
@@ -439,7 +441,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
   // Q as B fragments, in the contraction's channel order; rows past the last are zero
   constexpr int kQFrags = F::kKSteps * NT * 32;
   constexpr int kQIters = (kQFrags + kThreads - 1) / kThreads;
-  uint32_t* q_max = reinterpret_cast<uint32_t*>(smem + C::kInv) + kWarps;
+  uint32_t* q_max = reinterpret_cast<uint32_t*>(smem + C::kQMax);
+  static_assert(kWarps % NT == 0, "a thread's fragments are all of one row: 8 (warp % NT) + g");
   uint32_t qb[kQIters][2], q_top = 0u;
 #pragma unroll
   for (int it = 0; it < kQIters; ++it) {
@@ -471,20 +474,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
     }
   }
   if constexpr (!F::kBf16) {
-    q_top = __reduce_max_sync(0xffffffffu, q_top);
-    if (lane == 0) q_max[warp] = q_top;
+    q_top = max(q_top, __shfl_xor_sync(0xffffffffu, q_top, 1));
+    q_top = max(q_top, __shfl_xor_sync(0xffffffffu, q_top, 2));
+    if (t4 == 0) q_max[warp * 8 + g] = q_top;
   }
   // a tree's depths, and the ancestor sets of this tile's tokens
   const int t_first = token_of(a, r0);
   if (a.parents && threadIdx.x < a.n_tokens)
     par[threadIdx.x] = a.parents[static_cast<int64_t>(u.seq) * a.n_tokens + threadIdx.x];
   __syncthreads();
-  float q_inv = 1.f;  // what a score is multiplied by besides K's scale
+  float* q_inv = reinterpret_cast<float*>(smem + C::kQInv);
   float q_mul = 1.f;
   if constexpr (!F::kBf16) {
 #pragma unroll
-    for (int x = 0; x < kWarps; ++x) q_top = max(q_top, q_max[x]);
-    q_mul = q_multiplier(q_top, q_inv);
+    for (int x = warp % NT; x < kWarps; x += NT) q_top = max(q_top, q_max[x * 8 + g]);
+    const uint32_t e = q_exponent(q_top);
+    q_mul = q_multiplier(e);
+    if (warp < NT && t4 == 0) q_inv[8 * warp + g] = q_inverse(e) * a.scale_log2;
   }
 #pragma unroll
   for (int it = 0; it < kQIters; ++it) {
@@ -520,6 +526,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 
   // this lane's rows: 8 n + 2 t4 + {0, 1}; their tokens (within the tile) and positions
   int tok[NT][2], pos[NT][2];
+  // What scores are multiplied by besides K's scales, to be in powers of two.  Kept in
+  // registers where there are any left, else read anew for each step.
+  constexpr bool kKeep = F::kBf16 || NT == 1;
+  float2 row_scale[kKeep ? NT : 1];
   int pos_hi = 0;  // windows of all rows of the tile start at or below pos_hi - window + 1
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -533,6 +543,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
       pos_hi = max(pos_hi, pos[n][e]);
     }
   if (VAR) pos_hi = __reduce_max_sync(0xffffffffu, pos_hi);
+  const uint32_t row_scales = smem_addr(smem) + C::kQInv + 8 * t4;
+  if constexpr (!F::kBf16 && kKeep) {
+    const uint2 w = lds64(row_scales);
+    row_scale[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+  }
 
   float o[F::kMTiles][NT][4];
 #pragma unroll
@@ -547,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 #pragma unroll
     for (int e = 0; e < 2; ++e) m_ref[n][e] = -INFINITY, l[n][e] = 0.f;
 
+  const float cap = VAR ? a.cap * a.scale_log2 : 0.f;  // in powers of two
   uint32_t v_exp = kMinScaleExp;  // exponent of the largest V scale so far: O's unit
   const uint32_t q_frag = smem_addr(smem) + C::kQ;
   uint32_t st = ring;  // the step's stage
@@ -575,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
           const uint2 z = lds64(sw + 64 + (2 * t4 + 8 * e) * 4);
           vz[e] = int4_zero(z.x, z.y);
         }
-        kscale[e] = __uint_as_float(kw[e]) * q_inv;
+        kscale[e] = __uint_as_float(kw[e]);
         vscale[e] = __uint_as_float(vw[e]);
       }
     }
@@ -585,17 +601,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 
     // scaled scores in powers of two
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      float2 rs = make_float2(a.scale_log2, a.scale_log2);
+      if constexpr (!F::kBf16 && kKeep) rs = row_scale[0];
+      if constexpr (!kKeep) {
+        const uint2 w = lds64(row_scales + 32 * n);
+        rs = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float z = s[n][e] * kscale[e >> 1];
-        if (VAR && a.cap > 0.f) {
+        const float f = e & 1 ? rs.y : rs.x;
+        float z = s[n][e] * (F::kBf16 ? f : kscale[e >> 1] * f);
+        if (VAR && cap > 0.f) {
           // c tanh(z / c) = c - 2 c / (2^(2 log2(e) z / c) + 1)
-          const float ex = exp2_fast(z * (2.0f * 1.4426950408889634f / a.cap));
-          z = a.cap - __fdividef(2.0f * a.cap, ex + 1.0f);
+          const float ex = exp2_fast(z * (2.0f * 1.4426950408889634f / cap));
+          z = cap - __fdividef(2.0f * cap, ex + 1.0f);
         }
-        s[n][e] = z * a.scale_log2;
+        s[n][e] = z;
       }
+    }
     // a step that holds new tokens, the end, or a window's lower edge
     bool masked = j0 + kStep > u.len;
     if (VAR && a.window > 0) masked |= j0 <= pos_hi - a.window;

@@ -333,8 +333,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // bits to bf16 takes five, and the pipe that runs those was the busiest).
 // fp16's range is narrow, so both other operands are brought into it by powers
 // of two:
-//  * Q: all of a block's rows by one, so that its largest value is 2^14 .. 2^15.
-//    What that rounds is below 2^-31 of the largest value.
+//  * Q: each row by one of its own, so that its largest value is 2^14 .. 2^15 and
+//    what that rounds is below 2^-31 of it; a row's scale never depends on
+//    another's, which may be a padding token's or as large as bf16 goes.  (The
+//    tile kernel gives rows within 2^8 of the block's largest the block's one,
+//    with the same bound, and multiplies the scores of the others.)
 //  * P times V's scale: by one that keeps it below 2^15, from the largest V scale
 //    met so far.  A weight is then rounded to 2^-25 or finer, in units of 2^15
 //    for the largest possible one: what is lost is below 2^-32 of a row's
@@ -384,11 +387,18 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
   const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
   return b < 0x7f800000u ? b : 0u;
 }
-// Power of two that brings Q's largest value (its bits) to 2^14 .. 2^15, and its inverse.
-__device__ __forceinline__ float q_multiplier(uint32_t max_bits, float& inverse) {
-  const uint32_t e = max(max_bits >> 23, 20u);
-  inverse = __uint_as_float((e - 14u) << 23);
-  return __uint_as_float((268u - e) << 23);
+// From the bits of the largest value of a row (or block) of Q: its exponent, and
+// the power of two that brings it to 2^14 .. 2^15, with its inverse.
+__device__ __forceinline__ uint32_t q_exponent(uint32_t max_bits) { return max(max_bits >> 23, 20u); }
+__device__ __forceinline__ float q_multiplier(uint32_t e) { return __uint_as_float((268u - e) << 23); }
+__device__ __forceinline__ float q_inverse(uint32_t e) { return __uint_as_float((e - 14u) << 23); }
+// The block's exponent stays where its product with a scale of K cannot overflow.
+__device__ __forceinline__ uint32_t q_block_exponent(uint32_t max_bits) {
+  return min(max(q_exponent(max_bits), 127u - 40u), 127u + 40u);
+}
+__device__ __forceinline__ uint32_t q_row_exponent(uint32_t max_bits, uint32_t block) {
+  const uint32_t e = max_bits ? q_exponent(max_bits) : block;
+  return e <= block && block - e <= 8u ? block : e;
 }
 // The same for V's scales, from the biased exponent of the largest: their
 // products with the multiplier stay below 2^7 (P itself is at most 2^8).

@@ -106,7 +106,8 @@ struct TileCfg {
   static constexpr uint32_t kMask = kZero + (FMT == PDS_KV_INT4 ? 2 * kRaw * kZeroSlot : 0u);
   static constexpr uint32_t kPar = kMask + kMaskWords * 256u * 4u;
   static constexpr uint32_t kQMax = kPar + kMaxDraftTokens * 4u;  // Q's maximum per warp
-  static constexpr uint32_t kUnitAt = kQMax + 64u;                // O's unit of each stream
+  static constexpr uint32_t kQRow = kQMax + 64u;                  // exponents of rows of Q, bytes
+  static constexpr uint32_t kUnitAt = kQRow + 256u;               // O's unit of each stream
   static constexpr uint32_t kBar = kUnitAt + 16u;
   static constexpr int kNumBars = 2 + 2 * (kKStages + kVStages) + 14;
   static constexpr uint32_t kMisc = kBar + 8u * kNumBars;
@@ -332,6 +333,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int head = p % a.c.n_kv_heads, group_tile = p / a.c.n_kv_heads;
   const int rows = a.n_tokens * a.group, r0 = group_tile * a.tile_rows;
   const bool two_tiles = rows - r0 > kTileRows;  // the streams are row tiles, else key halves
+  if (C::kQuant && threadIdx.x < 64) reinterpret_cast<uint32_t*>(smem + C::kQRow)[threadIdx.x] = 0u;
   if (threadIdx.x == 0) {
     mbar_init(bar_q, kSoftmaxThreads / 32);
     mbar_init(bar_q_max, kSoftmaxThreads / 32);
@@ -589,9 +591,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t* q_max = reinterpret_cast<const uint32_t*>(smem + C::kQMax);
 #pragma unroll 1
         for (int x = 0; x < kSoftmaxThreads / 32; ++x) top = max(top, q_max[x]);
-        float inverse;
-        q_multiplier(top, inverse);
-        k_factor *= inverse;
+        k_factor *= q_inverse(q_block_exponent(top));
       }
       for (int t = 0; t < n && ok; ++t) {
         copies_wait<C::kRaw - 1>();
@@ -706,28 +706,37 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if constexpr (C::kQuant) {
         // bits of the largest |value|, two at a time; over again without the
         // infinities and NaN if there are any
-        uint32_t pair = 0u;
+        auto piece_max = [&](int row) -> uint32_t {
+          const uint4 x = lds128(place(row));
+          const uint32_t pair = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                         __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+          return max(pair & 0xffffu, pair >> 16);
+        };
+        auto finite_piece_max = [&](int row) -> uint32_t {
+          const uint4 x = lds128(place(row));
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t most = 0u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            most = max(most, max(finite_bits(__uint_as_float(w[e] << 16)),
+                                 finite_bits(__uint_as_float(w[e] & 0xffff0000u))));
+          return most >> 16;
+        };
+        uint32_t top = 0u, least = 0xffffu;  // of the pieces; the least that is not zero
 #pragma unroll 4
         for (int row = row0; row < q_rows; row += kStep) {
-          const uint4 x = lds128(place(row));
-          pair = __vmaxu2(pair, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                         __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+          const uint32_t most = piece_max(row);
+          top = max(top, most);
+          least = min(least, most - 1u);  // (zero goes to the top)
         }
-        uint32_t top = max(pair & 0xffffu, pair >> 16) << 16;
-        if (__any_sync(0xffffffffu, top >= 0x7f800000u)) {
+        if (__any_sync(0xffffffffu, top >= 0x7f80u)) {
           top = 0u;
 #pragma unroll 1
-          for (int row = row0; row < q_rows; row += kStep) {
-            const uint4 x = lds128(place(row));
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              top = max(top, max(finite_bits(__uint_as_float(w[e] << 16)),
-                                 finite_bits(__uint_as_float(w[e] & 0xffff0000u))));
-          }
+          for (int row = row0; row < q_rows; row += kStep) top = max(top, finite_piece_max(row));
+          least = 0u;
         }
         uint32_t* q_max = reinterpret_cast<uint32_t*>(smem + C::kQMax);
-        top = __reduce_max_sync(0xffffffffu, top);
+        top = __reduce_max_sync(0xffffffffu, top << 16);
         if (lane == 0) {
           q_max[warp - kFirstSoftmaxWarp] = top;
           mbar_arrive(bar_q_max);
@@ -735,11 +744,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         named_bar_sync(1, kSoftmaxThreads);
 #pragma unroll 1
         for (int c = 0; c < kSoftmaxThreads / 32; ++c) top = max(top, q_max[c]);
-        float inverse;
-        const float q_mul = q_multiplier(top, inverse);
+        const uint32_t block = q_block_exponent(top);
+        // Rows that may not take the block's multiplier: some piece of theirs is far
+        // below it, or the block's largest above it.  (A row's pieces are neighbouring
+        // lanes of one warp.)
+        uint8_t* q_row = smem + C::kQRow;  // exponents of such rows, else 0
+        if (__any_sync(0xffffffffu, ((least + 1u) >> 7) + 8u < block || (top >> 23) > block)) {
+#pragma unroll 1
+          for (int row = row0; row < q_rows; row += kStep) {
+            uint32_t most = finite_piece_max(row);
+#pragma unroll
+            for (int o = 1; o < kPieces; o <<= 1)
+              most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+            const uint32_t e = q_row_exponent(most << 16, block);
+            if (col == 0 && e != block) q_row[row] = static_cast<uint8_t>(e);
+          }
+          __syncwarp();
+        }
+        const float q_block = q_multiplier(block);
 #pragma unroll 4
         for (int row = row0; row < q_rows; row += kStep) {
           const uint4 x = lds128(place(row));
+          const uint32_t own = q_row[row];
+          const float q_mul = own ? q_multiplier(own) : q_block;
           uint32_t w[4] = {x.x, x.y, x.z, x.w};
           float f[8];
 #pragma unroll
@@ -768,6 +795,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (n > 0 && a.parents && tid < a.n_tokens)
       par[tid] = a.parents[static_cast<int64_t>(u.seq) * a.n_tokens + tid];
     named_bar_sync(1, kSoftmaxThreads);
+    // what the row's scores are multiplied by, besides the block's factor
+    float q_ratio = 1.f;
+    if constexpr (C::kQuant) {
+      if (n > 0) {
+        const uint32_t own = smem[C::kQRow + (two_tiles ? s * kTileRows : 0) + r];
+        if (own) {
+          uint32_t top = 0u;
+          const uint32_t* q_max = reinterpret_cast<const uint32_t*>(smem + C::kQMax);
+#pragma unroll 1
+          for (int c = 0; c < kSoftmaxThreads / 32; ++c) top = max(top, q_max[c]);
+          q_ratio = q_inverse(own) * q_multiplier(q_block_exponent(top));
+        }
+      }
+    }
+    const bool ratios = C::kQuant && __any_sync(0xffffffffu, q_ratio != 1.f);
     int depth = tok;
     if (n > 0 && a.parents) {
       depth = tree_depth(par, tok);
@@ -826,7 +868,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         continue;
       }
       const uint32_t ts = tmem + lane_off + C::kTmS + s * 128u + b * 64u;
-      const bool partial = key > hide_hi || key < hide_lo;
+      const bool partial = key > hide_hi || key < hide_lo, special = partial || ratios;
       uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
       if (partial) {
         vis[0] = visible32(key, len, lo, mask);
@@ -849,29 +891,37 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
       for (int pass = 0; pass < 3; ++pass) {  // weights; the maximum; weights again
         const float less = rounded ? 0.f : m_ref;
-        tmem_load64(ts, z);
-        if (VAR && cap > 0.f) {
+        auto scores = [&](bool times_ratio) {
+          tmem_load64(ts, z);
+          if (times_ratio) {
 #pragma unroll
-          for (int x = 0; x < kKeys; ++x) {
-            float f = sc;
-            if constexpr (C::kQuant) f = __uint_as_float(lds32(words + x * 4));
-            // c tanh(z / c) = c - 2 c / (2^(2 log2(e) z / c) + 1)
-            const float y = z[x] * f;
-            const float e = exp2_fast(y * (2.0f * 1.4426950408889634f / cap));
-            z[x] = cap - __fdividef(2.0f * cap, e + 1.0f) - less;
+            for (int x = 0; x < kKeys / 2; ++x) mul2(z[2 * x], z[2 * x + 1], q_ratio, q_ratio);
           }
-        } else if constexpr (C::kQuant) {
+          if (VAR && cap > 0.f) {
 #pragma unroll
-          for (int x = 0; x < kKeys / 4; ++x) {
-            const float4 f = ld_shared_f4(words + x * 16);
-            fma2_pair(z[4 * x], z[4 * x + 1], f.x, f.y, -less);
-            fma2_pair(z[4 * x + 2], z[4 * x + 3], f.z, f.w, -less);
+            for (int x = 0; x < kKeys; ++x) {
+              float f = sc;
+              if constexpr (C::kQuant) f = __uint_as_float(lds32(words + x * 4));
+              // c tanh(z / c) = c - 2 c / (2^(2 log2(e) z / c) + 1)
+              const float y = z[x] * f;
+              const float e = exp2_fast(y * (2.0f * 1.4426950408889634f / cap));
+              z[x] = cap - __fdividef(2.0f * cap, e + 1.0f) - less;
+            }
+          } else if constexpr (C::kQuant) {
+#pragma unroll
+            for (int x = 0; x < kKeys / 4; ++x) {
+              const float4 f = ld_shared_f4(words + x * 16);
+              fma2_pair(z[4 * x], z[4 * x + 1], f.x, f.y, -less);
+              fma2_pair(z[4 * x + 2], z[4 * x + 3], f.z, f.w, -less);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < kKeys / 2; ++x) fma2(z[2 * x], z[2 * x + 1], sc, -less);
           }
-        } else {
-#pragma unroll
-          for (int x = 0; x < kKeys / 2; ++x) fma2(z[2 * x], z[2 * x + 1], sc, -less);
-        }
-        if (partial) {
+        };
+        scores(false);
+        if (special) {
+          if (C::kQuant && ratios) scores(true);  // (rarely: so the others do not ask twice)
 #pragma unroll
           for (int x = 0; x < kKeys; ++x)
             if (!((vis[x >> 5] >> (x & 31)) & 1u)) z[x] = -INFINITY;

@@ -89,7 +89,7 @@ def test_scores_far_apart_under_few_and_many_rows(fmt, t):
     _close(cache, o, q64, k64, v64, 1500)
 
 
-@pytest.mark.parametrize("fmt", ["bf16"])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int4"])
 @pytest.mark.parametrize("t,h", [(6, 6), (40, 4), (100, 6)])
 def test_queries_of_padding_tokens_may_hold_anything(fmt, t, h):
     kv = _kv()
@@ -111,3 +111,32 @@ def test_queries_of_padding_tokens_may_hold_anything(fmt, t, h):
         assert (o[0, pad] == 0).all()
         _close(cache, o, q64, k64, v64, 500, parents[0],
                rows=[i for i in range(t) if i not in pad])
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int4"])
+@pytest.mark.parametrize("t,h,hkv,hd,softcap", [(2, 4, 2, 128, 0.0), (5, 4, 2, 64, 20.0), (12, 4, 2, 128, 0.0),
+                                                (40, 4, 2, 64, 0.0), (70, 8, 2, 128, 20.0)])
+def test_query_rows_far_apart_do_not_touch_each_other(fmt, t, h, hkv, hd, softcap):
+    """Live rows of one block whose sizes differ by up to 2^126: each is as exact as alone."""
+    kv = _kv()
+    rng = np.random.default_rng(t + hd)
+    cache, k64, v64 = _filled(kv, rng, fmt, 1, 300 + t, hkv, hd, [300])
+    size = 10.0 ** rng.choice([-8, -2, 0, 0, 0, 1, 3], (1, t, h, 1))
+    for big in (1.0, 1e4, 1e12, 1e30):
+        scale = size.copy()
+        scale[0, ::3, 1] = big
+        q, q64 = _normal(rng, 1, t, h, hd)
+        q, q64 = _bf16(q64 * scale)
+        o = cache.attend(q, softcap=softcap)
+        cache.sync()
+        # rows of size 1 and below; for larger ones the scores' own rounding decides
+        small = (scale[0, :, :, 0] <= 1.0)
+        got = bf16_to_f64(o)[0]
+        assert np.isfinite(got).all()
+        want, size_v = D.tree_attention(q64[0], k64[0], v64[0], 300, None, softcap, 0)
+        reach = np.abs(q64[0]).sum(-1) * np.abs(k64).max()
+        slack = (hd + 8) * 2.0 ** -23 * reach / math.sqrt(hd)
+        floor = (300 + t) * 2.0 ** -31 * _scales(cache).max() * {"e4m3": 448, "int4": 15}[fmt]
+        # a capped score: c - 2 c / (e + 1) is off by some 2^-21 c
+        cap = softcap * 2.0 ** -21
+        tol = EPS * np.abs(want) + (EPS + 2 * (slack[..., None] + cap)) * size_v * 1.01 + floor
+        assert np.all((np.abs(got - want) <= tol)[small])
