@@ -646,38 +646,56 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
           }
       }
     }
-    // move the reference maxima where a score is far above
+    // move the references where a score is far above
     bool far = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) far |= s[n][e] > m_ref[n][e & 1] + kMoveLog2;
-    uint32_t v_top = v_exp;
     if constexpr (!F::kBf16) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (seen[e]) v_top = max(v_top, finite_bits(vscale[e]) >> 23);
-      far |= v_top > v_exp;
+      for (int e = 0; e < 2; ++e) far |= seen[e] && finite_bits(vscale[e]) >> 23 > v_exp;
     }
     if (__any_sync(0xffffffffu, far)) {
+      float shift[2] = {0.f, 0.f};
       if constexpr (!F::kBf16) {
+        uint32_t v_top = v_exp;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (seen[e]) v_top = max(v_top, min(finite_bits(vscale[e]) >> 23, kMaxScaleExp));
         v_top = __reduce_max_sync(0xffffffffu, v_top);
-        if (v_top > v_exp) {  // O in units of the larger scale; exact
-          const float f = v_multiplier(v_top) * v_inverse(v_exp);
-          v_exp = v_top;
+        if (v_top > v_exp && i > 0) {
+          float most = 0.f;  // (sums are not negative: they order as their bits do)
 #pragma unroll
-          for (int t = 0; t < F::kMTiles; ++t)
+          for (int n = 0; n < NT; ++n) most = fmaxf(most, fmaxf(l[n][0], l[n][1]));
+          most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+          const int d = static_cast<int>(v_top - v_exp), k = unit_shift(d, most);
+          const float up = exp2_fast(static_cast<float>(k)), down = exp2_fast(static_cast<float>(k - d));
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[t][n][e] *= f;
+            for (int x = 0; x < 2; ++x) {
+              m_ref[n][x] -= static_cast<float>(k);
+              l[n][x] *= up;
+            }
+          if (k < d) {
+#pragma unroll
+            for (int t = 0; t < F::kMTiles; ++t)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][n][e] *= down;
+          }
         }
+        v_exp = v_top;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) shift[e] = level_shift(finite_bits(vscale[e]) >> 23, v_exp);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          float m = fmaxf(s[n][x], s[n][2 + x]);
+          float m = fmaxf(s[n][x] + shift[0], s[n][2 + x] + shift[1]);
 #pragma unroll
           for (int sh = 4; sh < 32; sh <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
           if (m > m_ref[n][x] + kMoveLog2) {

@@ -338,10 +338,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
 //    another's, which may be a padding token's or as large as bf16 goes.  (The
 //    tile kernel gives rows within 2^8 of the block's largest the block's one,
 //    with the same bound, and multiplies the scores of the others.)
-//  * P times V's scale: by one that keeps it below 2^15, from the largest V scale
-//    met so far.  A weight is then rounded to 2^-25 or finer, in units of 2^15
-//    for the largest possible one: what is lost is below 2^-32 of a row's
-//    weight per key, also where V's scales differ by 2^20.
+//  * P times V's scale: by one (the unit, from the largest V scale met so far) that
+//    brings that scale to 2^6 .. 2^7, and by the row's reference, which follows the
+//    row's largest product of a weight and a scale, not its largest weight: where the
+//    scale of the key with the largest score is below the unit by more than 2^4 the
+//    reference is lower by as much (level_shift).  So a row's largest product is 2^2
+//    or more when it is taken, later ones are below 2^15, and what rounding to fp16's
+//    smallest steps loses is below 2^-27 of the row's largest product per key, and below
+//    2^-31 of the largest scale: keys that a row does not see, or hardly, take no
+//    precision from it whatever their scales (up to 2^80 above; weights stay below 2^88,
+//    their sums in float32).
 __device__ __forceinline__ void e4m3_pairs(uint32_t r, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 l, h;\n\t"
       "mov.b32 {l, h}, %2;\n\t"
@@ -400,11 +406,22 @@ __device__ __forceinline__ uint32_t q_row_exponent(uint32_t max_bits, uint32_t b
   const uint32_t e = max_bits ? q_exponent(max_bits) : block;
   return e <= block && block - e <= 8u ? block : e;
 }
-// The same for V's scales, from the biased exponent of the largest: their
-// products with the multiplier stay below 2^7 (P itself is at most 2^8).
-constexpr uint32_t kMinScaleExp = 8;
+// V's unit, from the biased exponent of the largest scale: products of scales with the
+// multiplier are below 2^7.  Larger scales than 2^60 do not raise it further, so that
+// those of ordinary keys stay normal float32 numbers beside them.
+constexpr uint32_t kMinScaleExp = 8, kMaxScaleExp = 127 + 60;
 __device__ __forceinline__ float v_multiplier(uint32_t e) { return __uint_as_float((260u - e) << 23); }
 __device__ __forceinline__ float v_inverse(uint32_t e) { return __uint_as_float((e - 6u) << 23); }
+// What a key's score is moved by where its V scale (biased exponent e) is far from the unit.
+__device__ __forceinline__ float level_shift(uint32_t e, uint32_t unit) {
+  const int d = static_cast<int>(e) - static_cast<int>(unit);
+  return static_cast<float>(d < -4 ? max(d + 4, -80) : max(d, 0));
+}
+// The unit grows by 2^d: a row's reference goes down by as much instead of its O, which
+// keeps its bits, as far as its sum (at most `sum`) allows; O takes the rest.
+__device__ __forceinline__ int unit_shift(int d, float sum) {
+  return max(min(min(d, 90), 127 + 90 - static_cast<int>(__float_as_uint(sum) >> 23)), 0);
+}
 
 __device__ __forceinline__ bool not_finite2(uint32_t w) {  // either bf16 of a pair
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;

@@ -65,6 +65,7 @@ constexpr int kLoadWarps = 4, kLoadThreads = 32 * kLoadWarps;  // of K, and of V
 constexpr int kFirstLoadWarp = 4, kFirstSoftmaxWarp = kFirstLoadWarp + 2 * kLoadWarps;
 constexpr int kSoftmaxThreads = 256;   // 2 streams x 128 rows
 constexpr int kTileThreads = 32 * kFirstSoftmaxWarp + kSoftmaxThreads;
+constexpr uint32_t kAboveUnit = 256u, kFarFromUnit = 512u;  // beside a tile's unit
 constexpr float kMoveSum = 256.0f;     // a tile's weights sum to more: the reference moves
 // registers per thread: 96 at launch; 384 threads give up 32 each for the 256
 // softmax threads' 48 more
@@ -644,19 +645,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             word[tid] = scale(tid) * k_factor;
           } else if (tid < 96) {
             const float v0 = scale(tid), v1 = scale(tid + 32);
-            auto exponent = [&](float v, int key) -> uint32_t {
-              // (a padding token's row is not written: it may hold any scale)
-              if (key >= len && key < end && a.parents &&
-                  a.parents[static_cast<int64_t>(u.seq) * a.n_tokens + key - len] < -1)
-                return 0u;
-              return finite_bits(v) >> 23;
+            // (a padding token's row is not written: it may hold any scale)
+            auto counts = [&](int key) {
+              return key < len || (key < end && !(a.parents && a.parents[static_cast<int64_t>(u.seq) *
+                                                                         a.n_tokens + key - len] < -1));
             };
-            v_exp = __reduce_max_sync(0xffffffffu, max(v_exp, max(exponent(v0, key0 + tid - 64),
-                                                                  exponent(v1, key0 + tid - 32))));
+            const bool c0 = counts(key0 + tid - 64), c1 = counts(key0 + tid - 32);
+            const uint32_t e0 = finite_bits(v0) >> 23, e1 = finite_bits(v1) >> 23;
+            const uint32_t most = __reduce_max_sync(0xffffffffu, max(c0 ? e0 : 0u, c1 ? e1 : 0u));
+            const uint32_t least = __reduce_min_sync(0xffffffffu, min(c0 ? e0 : 255u, c1 ? e1 : 255u));
+            v_exp = max(v_exp, min(most, kMaxScaleExp));
+            // What the softmax has to look at: scales above the unit (in this tile), or
+            // far from it (where it looks at this tile's maximum).
+            const uint32_t flags = (most > v_exp ? kAboveUnit : 0u) |
+                                   (most > v_exp || least + 4u < v_exp ? kFarFromUnit : 0u);
             const float f = v_multiplier(v_exp);
             word[tid] = v0 * f;
             word[tid + 32] = v1 * f;
-            if (tid == 64) word[128] = __uint_as_float(v_exp);
+            if (tid == 64) word[128] = __uint_as_float(v_exp | flags);
           }
         }
         arrive(full0 + 8u * st);
@@ -878,14 +884,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if constexpr (C::kQuant) unit = lds32(words + 512u);
       float z[kKeys];
       // Scores less the reference, in powers of two, and their exponentials.  The
-      // maximum is only taken where the row has no reference yet or its weights
-      // have outgrown the old one, which their sum tells; at most once, because the
-      // weights behind it are at most one by construction: the reference is the
-      // largest of the rounded scores and is subtracted from these.  (The fused
+      // maximum is only taken where the row has no reference yet, its weights have
+      // outgrown the old one, which their sum tells, or V's unit has grown; at most once,
+      // because what is multiplied behind it is bounded by construction: the reference
+      // is the largest of the rounded scores (over codes, of their levels) and is
+      // subtracted from these.  (The fused
       // difference of the first pass also holds what the product's rounding drops,
       // which from 2^28 on is above 8 now and then: as a measure of growth that
       // would never end, from 2^31 on as a weight it would be nothing or infinite.)
-      bool move = __any_sync(0xffffffffu, m_ref == -INFINITY || unit != v_exp);
+      bool move = __any_sync(0xffffffffu, m_ref == -INFINITY || (unit & ~kFarFromUnit) != v_exp);
       bool rounded = move;
       float grown, pk[kKeys / 2];
 #pragma unroll 1
@@ -927,18 +934,42 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (!((vis[x >> 5] >> (x & 31)) & 1u)) z[x] = -INFINITY;
         }
         if (move) {
-          const float mx = fmaxf(max32(z), max32(z + 32));
-          float alpha = 1.f;
+          float alpha = 1.f, mx;
+          if constexpr (C::kQuant) {
+            const uint32_t v_new = unit & 255u;
+            const int d = static_cast<int>(v_new - v_exp), k = unit_shift(d, l);
+            v_exp = v_new;
+            alpha = exp2_fast(static_cast<float>(k - d));
+            m_ref -= static_cast<float>(k);
+            l *= exp2_fast(static_cast<float>(k));
+          }
+          if (!C::kQuant || !(unit & kFarFromUnit)) {
+            mx = fmaxf(max32(z), max32(z + 32));
+          } else {
+            float level[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) level[x] = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < kKeys / 4; ++x) {
+              const float4 f = ld_shared_f4(words + 256u + x * 16);
+              // (a factor is its scale over the unit, times 2^6)
+              auto shift = [&](float v) { return level_shift(__float_as_uint(v) << 1 >> 24, 133u); };
+              float* y = level + 4 * (x & 1);
+              y[0] = fmaxf(y[0], z[4 * x] + shift(f.x));
+              y[1] = fmaxf(y[1], z[4 * x + 1] + shift(f.y));
+              y[2] = fmaxf(y[2], z[4 * x + 2] + shift(f.z));
+              y[3] = fmaxf(y[3], z[4 * x + 3] + shift(f.w));
+            }
+            mx = fmaxf(max3(level[0], level[1], level[2]), max3(level[3], level[4], level[5]));
+            mx = max3(mx, level[6], level[7]);
+          }
           if (mx > m_ref) {
-            alpha = exp2_fast(m_ref - mx);  // 0 from -inf
+            const float f = exp2_fast(m_ref - mx);  // 0 from -inf
             m_ref = mx;
-            l *= alpha;
+            l *= f;
+            alpha *= f;
           }
-          if (C::kQuant) {
-            alpha *= v_multiplier(unit) * v_inverse(v_exp);
-            v_exp = unit;
-          }
-          if (i > 0) {
+          if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
             // O at rest: the product of the tile before has completed
             wait(bar_pv(s, b ^ 1), ((i - 1) >> 1) & 1);
             if (!ok) break;

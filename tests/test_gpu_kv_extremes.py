@@ -140,3 +140,132 @@ def test_query_rows_far_apart_do_not_touch_each_other(fmt, t, h, hkv, hd, softca
         cap = softcap * 2.0 ** -21
         tol = EPS * np.abs(want) + (EPS + 2 * (slack[..., None] + cap)) * size_v * 1.01 + floor
         assert np.all((np.abs(got - want) <= tol)[small])
+
+
+def _products_close(cache, o, q64, k64, v64, length, parents, rows, window=0):
+    """Rows of one sequence over codes, each measured by what it sees itself: test_gpu_kv's
+    tolerance, and 2^-27 of the row's largest product of a weight and a V scale, times the
+    largest code, per key (fp16's smallest step is 2^-24, off by half of it, and a row's largest
+    product is held as 4 or more)."""
+    got = bf16_to_f64(o)[0]
+    t, h, hd = got.shape
+    group = h // k64.shape[2]
+    scale = _scales(cache)[0]
+    paths = D.tree_paths(range(-1, t - 1) if parents is None else parents)
+    for i in rows:
+        keys = np.array(list(range(length)) + [length + a for a in paths[i]])
+        pos = np.array(list(range(length)) + [length + a for a in range(len(paths[i]))])
+        keys = keys[pos > pos[-1] - window] if window else keys
+        for head in range(h):
+            g, x = head // group, q64[0, i, head]
+            z = k64[0, keys, g] @ x / math.sqrt(hd)
+            w = np.exp(z - z.max())
+            w /= w.sum()
+            want, size = w @ v64[0, keys, g], w @ np.abs(v64[0, keys, g])
+            slack = (hd + 8) * 2.0 ** -23 * (np.abs(k64[0, keys, g]) @ np.abs(x)).max() / math.sqrt(hd)
+            floor = len(keys) * 2.0 ** -27 * (w * scale[g, keys]).max() * {"e4m3": 448, "int4": 15}[cache.fmt]
+            tol = EPS * np.abs(want) + (EPS + 2 * slack) * size * 1.01 + floor
+            assert np.all(np.abs(got[i, head] - want) <= tol), (i, head)
+
+
+def _set_scale(cache, rows, value):
+    """V's scale words of some rows; their codes as they are."""
+    if cache.fmt == "e4m3":
+        cache.v_scale[:, :, rows] = value
+    else:
+        bits = int(np.float32(value).view(np.int32)) & -65536
+        cache.v_scale[:, :, rows] = (cache.v_scale[:, :, rows] & 15) | bits
+
+
+def _values(cache):
+    from test_gpu_kv import _codes, _words
+    return (D.dequantise(_codes(x, cache.fmt), np.swapaxes(_words(w), 1, 2), cache.fmt)
+            for x, w in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+
+
+BIG = [2.0 ** 33, 2.0 ** 70, 3.0e38]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int4"])
+@pytest.mark.parametrize("t,h,hkv,hd,length", [(3, 4, 2, 128, 300), (12, 4, 2, 64, 300), (40, 4, 2, 64, 300),
+                                               (100, 6, 2, 128, 310), (20, 4, 2, 128, 2000)])
+def test_large_scales_that_a_row_does_not_see(fmt, t, h, hkv, hd, length):
+    """Below the window, in a padding token's row, in the row of a token with a bad parent
+    (which the write refuses), in a sibling's."""
+    from dense_decoder_layer_gb300 import pds
+    kv = _kv()
+    rng = np.random.default_rng(t)
+    window = 90
+    for big in BIG:
+        cache, _, _ = _filled(kv, rng, fmt, 1, length + t, hkv, hd, [length])
+        parents = [-1, 0, 0] + [int(rng.integers(max(0, i - 6), i)) for i in range(3, t)]
+        bad, pad = (t - 1, t - 2) if t > 5 else (None, None)
+        if bad:
+            parents[bad], parents[pad] = t + 3, -2
+        for rows in [slice(0, length - window), slice(length + 2, length + 3)] + \
+                ([slice(length + t - 2, length + t)] if bad else []):
+            _set_scale(cache, rows, big)
+        k64, v64 = _values(cache)
+        q, q64 = _normal(rng, 1, t, h, hd)
+        o = cache.attend(q, parents=_i32([parents]), window=window)
+        if bad:
+            with pytest.raises(pds.PdsError):
+                cache.sync()
+            parents[bad] = -2
+        else:
+            cache.sync()
+        paths = D.tree_paths(parents)
+        rest = [i for i, p in enumerate(paths) if p and 2 not in p]
+        assert len(rest) > 1
+        _products_close(cache, o, q64, k64, v64, length, parents, rest, window)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int4"])
+@pytest.mark.parametrize("t,h,hkv,hd", [(1, 2, 1, 128), (3, 4, 2, 128), (12, 4, 2, 64), (40, 4, 2, 64),
+                                        (100, 4, 2, 128)])
+def test_large_scales_of_keys_with_hardly_any_weight(fmt, t, h, hkv, hd):
+    """Visible keys whose scale is far above the others' and whose weight is as far below: the
+    largest product decides, wherever such keys lie."""
+    kv = _kv()
+    rng = np.random.default_rng(t + hd)
+    length = 600
+    for big, place in ((2.0 ** 20, 5), (2.0 ** 40, 300), (2.0 ** 60, 599), (2.0 ** 36, slice(64, 520, 57))):
+        cache, _, _ = _filled(kv, rng, fmt, 1, length + t, hkv, hd, [length])
+        base = rng.standard_normal(hd)
+        base *= 8 / np.linalg.norm(base)
+        q, q64 = _bf16(base + 0.3 * rng.standard_normal((1, t, h, hd)))
+        k, _ = _normal(rng, 1, length + t, hkv, hd)
+        if isinstance(place, int):
+            place = slice(place, place + 1)
+        k[:, place] = _bf16(-8.0 * base)[0]
+        v, _ = _normal(rng, 1, length + t, hkv, hd)
+        cache.lens.zero_()
+        cache.write(k, v)
+        cache.lens.fill_(length)
+        _set_scale(cache, place, big)
+        k64, v64 = _values(cache)
+        o = cache.attend(q)
+        cache.sync()
+        _products_close(cache, o, q64, k64, v64, length, None, range(t))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int4"])
+@pytest.mark.parametrize("t,h,hkv,hd", [(1, 2, 1, 128), (12, 4, 2, 64), (40, 4, 2, 64), (140, 4, 2, 128)])
+def test_scales_over_sixty_powers_of_two(fmt, t, h, hkv, hd):
+    kv = _kv()
+    rng = np.random.default_rng(t + 7)
+    length = 500
+    for spread in (10, 30):
+        cache, _, _ = _filled(kv, rng, fmt, 1, length + t, hkv, hd, [length])
+        scale = np.exp2(rng.uniform(-spread, spread, (1, hkv, length + t))).astype(np.float32)
+        scale[0, :, ::7] = 0  # rows of zeros among them
+        bits = torch.from_numpy(scale).cuda().view(torch.int32)
+        if fmt == "e4m3":
+            cache.v_scale.view(torch.int32).copy_(bits)
+        else:
+            cache.v_scale.copy_((bits & -65536) | (cache.v_scale & 15))
+        k64, v64 = _values(cache)
+        q, q64 = _normal(rng, 1, t, h, hd, scale=3.0)
+        o = cache.attend(q)
+        cache.sync()
+        _products_close(cache, o, q64, k64, v64, length, None, range(t))
