@@ -646,12 +646,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
           }
       }
     }
-    // move the references where a score is far above
+    // move the references where a score is far above (by their difference: from 2^26 on
+    // a reference and 8 more need not be a float32)
     bool far = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) far |= s[n][e] > m_ref[n][e & 1] + kMoveLog2;
+      for (int e = 0; e < 4; ++e) far |= s[n][e] - m_ref[n][e & 1] > kMoveLog2;
     if constexpr (!F::kBf16) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) far |= seen[e] && finite_bits(vscale[e]) >> 23 > v_exp;
@@ -698,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
           float m = fmaxf(s[n][x] + shift[0], s[n][2 + x] + shift[1]);
 #pragma unroll
           for (int sh = 4; sh < 32; sh <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
-          if (m > m_ref[n][x] + kMoveLog2) {
+          if (m - m_ref[n][x] > kMoveLog2) {
             const float alpha = exp2_fast(m_ref[n][x] - m);  // 0 from -inf
             m_ref[n][x] = m;
             l[n][x] *= alpha;

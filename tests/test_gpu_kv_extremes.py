@@ -269,3 +269,37 @@ def test_scales_over_sixty_powers_of_two(fmt, t, h, hkv, hd):
         o = cache.attend(q)
         cache.sync()
         _products_close(cache, o, q64, k64, v64, length, None, range(t))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int4"])
+@pytest.mark.parametrize("t,place", [(1, 128), (1, 384), (40, 64), (40, 192)])
+def test_large_scores_that_are_neighbours(fmt, t, place):
+    """Two keys whose scores, around 2^27 in powers of two, are one or a few float32 apart (16
+    each), the larger one met later: its weight is not 2^16.  A token's result is some mean of the
+    two values, whichever way the scores are rounded."""
+    kv = _kv()
+    hd, length = 128, 512
+    for step in range(24):
+        cache = kv.KvCache(fmt, 1, length + t, 1, hd)
+        k = torch.zeros(1, length + t, 1, hd, dtype=torch.bfloat16, device="cuda")
+        k[0, [0, place], 0, 0] = 448.0 if fmt == "e4m3" else 15.0
+        v = torch.ones_like(k)
+        v[0, place] = 3.0
+        cache.write(k, v)
+        cache.lens.fill_(length)
+        # the later key's scale: float32 steps up where the format has them, else K's first
+        # channel stays and the second adds the difference
+        q = torch.zeros(1, t, 1, hd, dtype=torch.bfloat16, device="cuda")
+        q[..., 0] = (2.0 ** 27 * (1 + step / 24)) / (0.1275 * float(k[0, 0, 0, 0]))
+        if fmt == "e4m3":
+            cache.k_scale.view(torch.int32)[0, 0, place] += 1 + step % 3
+        else:
+            k[0, place, 0, 1] = 1.0
+            q[..., 1] = 16.0 * (1 + step % 3) / 0.1275
+            cache.lens.zero_()
+            cache.write(k, v)
+            cache.lens.fill_(length)
+        o = cache.attend(q)
+        cache.sync()
+        got = bf16_to_f64(o)
+        assert np.all((got >= 1 - EPS) & (got <= 3 * (1 + EPS))), (step, got.min(), got.max())
