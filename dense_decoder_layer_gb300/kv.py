@@ -14,6 +14,9 @@ A decode step with drafted tokens::
     cache.write(k, v, rope=spec, parents=parents)
     o = cache.attend(q, parents=parents)
     cache.lens += accepted            # after the accepted rows are in place
+
+A call with ``stream`` does what it would do under ``torch.cuda.stream(stream)``:
+what it allocates belongs to that stream, and its inputs have to be ready there.
 """
 
 from __future__ import annotations
@@ -74,8 +77,18 @@ def _index(t, rows, device, what):
     return t.data_ptr()
 
 
+def _new(make, shape, device, stream):
+    """make(shape) in bf16, on the stream that the call is for."""
+    if stream is None:
+        return make(shape, dtype=_BF16, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=_BF16, device=device)
+
+
 def _call(fn, device, stream, *args):
     """fn(*args, stream) with the tensors' device current."""
+    if stream is not None and stream.device_index != device:
+        raise ValueError(f"stream: one of cuda:{stream.device_index}, the tensors are on cuda:{device}")
     if _current_device() == device:
         st = fn(*args, _raw_stream(device) if stream is None else stream.cuda_stream)
     else:
@@ -112,7 +125,7 @@ def rope(x, spec, positions=None, start_pos=0, out=None, inverse=False, stream=N
     if hd != spec.head_dim:
         raise ValueError(f"x: heads of {hd} channels, the spec's have {spec.head_dim}")
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _new(torch.empty, shape, x.device, stream)
     device, lead = x.get_device(), len(shape) - 2
     xs = _rows(x, shape, lead, device, "x")
     ys = xs if out is x else _rows(out, shape, lead, device, "out")
@@ -214,9 +227,9 @@ class KvCache:
         a sequence does not have are left as they are (zero in a new tensor)."""
         shape = (self.n_seqs, rows, self.n_kv_heads, self.head_dim)
         if k_out is None:
-            k_out = torch.zeros(shape, dtype=_BF16, device=self.device)
+            k_out = _new(torch.zeros, shape, self.device, stream)
         if v_out is None:
-            v_out = torch.zeros(shape, dtype=_BF16, device=self.device)
+            v_out = _new(torch.zeros, shape, self.device, stream)
         if _rows(k_out, shape, 0, self.index, "k_out") or _rows(v_out, shape, 0, self.index, "v_out"):
             raise ValueError("k_out, v_out: contiguous tensors")
         _call(pds.load().pds_cache_read, self.index, stream, self.c, first_row, rows,
@@ -237,7 +250,7 @@ class KvCache:
         if shape[0] != self.n_seqs or shape[3] != self.head_dim:
             raise ValueError(f"q: [{self.n_seqs}, tokens, heads, {self.head_dim}], not {tuple(shape)}")
         if out is None:
-            out = torch.empty(shape, dtype=_BF16, device=self.device)
+            out = _new(torch.empty, shape, self.device, stream)
         qs, os_ = _rows(q, shape, 2, device, "q"), _rows(out, shape, 2, device, "out")
         if workspace is None:
             workspace = self._ws.get((t, heads))
