@@ -38,6 +38,7 @@ SCALINGS = {"none": pds.PDS_ROPE_UNSCALED, "linear": pds.PDS_ROPE_LINEAR,
 # compared as a whole, strides looked at only for tensors that are not packed.
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_is_capturing = torch._C._cuda_isCurrentStreamCapturing
 _BF16, _I32 = torch.bfloat16, torch.int32
 
 
@@ -77,12 +78,20 @@ def _index(t, rows, device, what):
     return t.data_ptr()
 
 
-def _new(make, shape, device, stream):
-    """make(shape) in bf16, on the stream that the call is for."""
-    if stream is None:
-        return make(shape, dtype=_BF16, device=device)
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=_BF16, device=device)
+def _new(make, shape, device, stream, dtype=_BF16):
+    """make(shape) on the stream that the call is for."""
+    index = stream.device_index if stream is not None else None
+    if stream is None or stream.cuda_stream == _raw_stream(index):
+        return make(shape, dtype=dtype, device=device)
+    if _current_device() != index:
+        with torch.cuda.stream(stream):
+            return make(shape, dtype=dtype, device=device)
+    before = torch.cuda.current_stream(index)  # (a tenth of the context's microseconds)
+    torch.cuda.set_stream(stream)
+    try:
+        return make(shape, dtype=dtype, device=device)
+    finally:
+        torch.cuda.set_stream(before)
 
 
 def _call(fn, device, stream, *args):
@@ -186,7 +195,7 @@ class KvCache:
             seq * self.per_byte, row * self.per_byte, head * self.per_byte, self.k.data_ptr(),
             self.v.data_ptr(), self.k_scale.data_ptr() if word is not None else None,
             self.v_scale.data_ptr() if word is not None else None, self._lens.data_ptr())
-        self._ws = {}  # attention workspace by (tokens, heads)
+        self._ws = {}  # attention workspace by (tokens, heads, stream)
 
     @property
     def lens(self):
@@ -198,16 +207,31 @@ class KvCache:
         if value is not self._lens:
             self._lens.copy_(value)
 
-    def workspace(self, n_tokens, n_heads):
-        """The attention's workspace for this many tokens and heads, made on first use and
-        shared by the calls of that shape (so: one stream at a time)."""
-        ws = self._ws.get((n_tokens, n_heads))
+    def _workspace_bytes(self, n_tokens, n_heads):
+        with torch.cuda.device(self.device):
+            return pds.pds_attention_tree_workspace_bytes(self.c, n_tokens, n_heads)
+
+    def workspace(self, n_tokens, n_heads, stream=None):
+        """The attention's workspace for this many tokens and heads on a stream (the current
+        one), made on first use and shared by the calls of that shape on that stream."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        key = (n_tokens, n_heads, stream.cuda_stream)
+        ws = self._ws.get(key)
         if ws is None:
-            with torch.cuda.device(self.device):
-                n = pds.pds_attention_tree_workspace_bytes(self.c, n_tokens, n_heads)
-            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-            self._ws[n_tokens, n_heads] = ws
+            ws = _new(torch.empty, self._workspace_bytes(n_tokens, n_heads), self.device, stream,
+                      torch.uint8)
+            self._ws[key] = ws
         return ws
+
+    def _own_workspace(self, n_tokens, n_heads, stream):
+        """One for this call alone if the current stream is being captured, from the graph's
+        memory: a graph may be replayed beside other work on any stream.  Else None."""
+        with torch.cuda.device(self.index):
+            if not _is_capturing():
+                return None
+        return _new(torch.empty, self._workspace_bytes(n_tokens, n_heads), self.device, stream,
+                    torch.uint8)
 
     def write(self, k, v, rope=None, parents=None, positions=None, stream=None):
         """Store new rows [n_seqs, n_tokens, n_kv_heads, head_dim] (bf16) behind the cached
@@ -244,7 +268,8 @@ class KvCache:
                workspace=None):
         """Attention of the written tokens' queries ``q`` [n_seqs, n_tokens, heads, head_dim]
         (bf16, rotated) over the cache and each other; ``parents`` int32 [n_seqs, n_tokens]
-        makes them a tree, without it they are a chain."""
+        makes them a tree, without it they are a chain.  Without ``workspace`` the calls of a shape on a
+        stream share one, and in a captured graph each has its own from the graph's memory."""
         _, t, heads, _ = shape = q.shape
         device = self.index
         if shape[0] != self.n_seqs or shape[3] != self.head_dim:
@@ -253,9 +278,13 @@ class KvCache:
             out = _new(torch.empty, shape, self.device, stream)
         qs, os_ = _rows(q, shape, 2, device, "q"), _rows(out, shape, 2, device, "out")
         if workspace is None:
-            workspace = self._ws.get((t, heads))
+            raw = _raw_stream(device) if stream is None else stream.cuda_stream
+            if raw and (_current_device() != device or _is_capturing()):
+                workspace = self._own_workspace(t, heads, stream)  # (stream 0 is not captured)
             if workspace is None:
-                workspace = self.workspace(t, heads)
+                workspace = self._ws.get((t, heads, raw))
+            if workspace is None:
+                workspace = self.workspace(t, heads, stream)
         _call(pds.load().pds_attention_tree, device, stream, self.c, q.data_ptr(), out.data_ptr(),
               t, heads, qs, os_, _index(parents, self.n_seqs * t, device, "parents"), softcap,
               window, max_len, workspace.data_ptr(), workspace.numel())
