@@ -285,9 +285,11 @@ class KvCache:
                 workspace = self._ws.get((t, heads, raw))
             if workspace is None:
                 workspace = self.workspace(t, heads, stream)
+        elif workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: a contiguous tensor on cuda:{device}")
         _call(pds.load().pds_attention_tree, device, stream, self.c, q.data_ptr(), out.data_ptr(),
               t, heads, qs, os_, _index(parents, self.n_seqs * t, device, "parents"), softcap,
-              window, max_len, workspace.data_ptr(), workspace.numel())
+              window, max_len, workspace.data_ptr(), workspace.nbytes)
         return out
 
     def sync(self, stream=None):

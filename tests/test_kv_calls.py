@@ -1,0 +1,61 @@
+"""What the PyTorch side of cached decoding refuses, and what it hands to the C ABI, on the
+host: CPU tensors that say they are on device 0, and a library that takes notes."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from dense_decoder_layer_gb300 import kv, pds
+
+
+class Cuda(torch.Tensor):
+    def get_device(self):
+        return 0
+
+
+def cuda(t):
+    return t.as_subclass(Cuda)
+
+
+class Notes:
+    """Stands for libpds.so: every entry point succeeds and its arguments are kept."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *args: self.calls.append((name, args)) or 0
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    notes = Notes()
+    monkeypatch.setattr(pds, "load", lambda: notes)
+    monkeypatch.setattr(kv, "_current_device", lambda: 0)
+    monkeypatch.setattr(kv, "_raw_stream", lambda device: 0)
+    return notes
+
+
+def make_cache(fmt="bf16", n=2, cap=16, hkv=2, hd=64):
+    k = torch.zeros(n, cap, hkv, hd, dtype=torch.bfloat16)
+    cache = kv.KvCache(fmt, n, cap, hkv, hd, k=k, v=k.clone(),
+                       lens=torch.zeros(n, dtype=torch.int32))
+    cache.index = 0
+    return cache
+
+
+def rows(*shape):
+    return cuda(torch.zeros(*shape, dtype=torch.bfloat16))
+
+
+def test_a_workspace_has_to_be_memory_of_the_device(lib):
+    cache, q = make_cache(), rows(2, 1, 4, 64)
+    good = cuda(torch.empty(64, dtype=torch.int32))
+    cache.attend(q, out=rows(2, 1, 4, 64), workspace=good)
+    assert lib.calls[-1][1][-3:-1] == (good.data_ptr(), 256)  # bytes
+    for bad in (torch.empty(256, dtype=torch.uint8),                       # of the host
+                cuda(torch.empty(1, dtype=torch.uint8)).expand(1 << 20),   # one byte
+                cuda(torch.empty(512, dtype=torch.uint8))[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            cache.attend(q, out=rows(2, 1, 4, 64), workspace=bad)
+    assert len(lib.calls) == 1
