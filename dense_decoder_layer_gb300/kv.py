@@ -47,6 +47,13 @@ def _need(ok, what):
         raise ValueError(what)
 
 
+def _int32(x, what):
+    """x, which the C ABI takes in 32 bits (ctypes would drop the others)."""
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{what}: {x} does not fit 32 bits")
+    return x
+
+
 def _rows(t, shape, n_lead, device, what):
     """Element stride (0: packed) between consecutive rows of a bf16 tensor of `shape`: its
     first `n_lead` sizes count rows, which are contiguous and evenly spaced."""
@@ -121,9 +128,11 @@ class RopeSpec:
             _need(len(freq_factors) == pairs, f"freq_factors: {pairs} values, one per rotated pair")
             arr = (ctypes.c_float * pairs)(*[float(f) for f in freq_factors])
         self._factors = arr
-        self.c = pds.pds_rope_spec(theta, LAYOUTS[layout], rot_dim, SCALINGS[scaling],
+        self.c = pds.pds_rope_spec(theta, LAYOUTS[layout], _int32(rot_dim, "rot_dim"),
+                                   SCALINGS[scaling],
                                    ctypes.cast(arr, ctypes.POINTER(ctypes.c_float)) if arr else None,
-                                   mscale, factor, orig_context, beta_fast, beta_slow)
+                                   mscale, factor, _int32(orig_context, "orig_context"), beta_fast,
+                                   beta_slow)
 
 
 def rope(x, spec, positions=None, start_pos=0, out=None, inverse=False, stream=None):
@@ -140,9 +149,10 @@ def rope(x, spec, positions=None, start_pos=0, out=None, inverse=False, stream=N
     ys = xs if out is x else _rows(out, shape, lead, device, "out")
     n = x.numel()
     if n:
-        rows = n // (heads * hd)
+        rows = _int32(n // (heads * hd), "x: its rows")
         _call(pds.load().pds_rope, device, stream, spec.c, x.data_ptr(), out.data_ptr(), rows,
-              heads, hd, xs, ys, _index(positions, rows, device, "positions"), start_pos, inverse)
+              heads, hd, xs, ys, _index(positions, rows, device, "positions"),
+              _int32(start_pos, "start_pos"), inverse)
     return out
 
 
@@ -162,6 +172,8 @@ class KvCache:
                  k_scale=None, v_scale=None, lens=None):
         self.fmt, self.n_seqs, self.capacity = fmt, int(n_seqs), int(capacity)
         self.n_kv_heads, self.head_dim = int(n_kv_heads), int(head_dim)
+        for name in ("n_seqs", "capacity", "n_kv_heads", "head_dim"):
+            _int32(getattr(self, name), name)
         self.device = torch.device(device) if k is None else k.device
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
@@ -256,7 +268,8 @@ class KvCache:
             v_out = _new(torch.zeros, shape, self.device, stream)
         if _rows(k_out, shape, 0, self.index, "k_out") or _rows(v_out, shape, 0, self.index, "v_out"):
             raise ValueError("k_out, v_out: contiguous tensors")
-        _call(pds.load().pds_cache_read, self.index, stream, self.c, first_row, rows,
+        _call(pds.load().pds_cache_read, self.index, stream, self.c,
+              _int32(first_row, "first_row"), _int32(rows, "rows"),
               k_out.data_ptr(), v_out.data_ptr())
         return k_out, v_out
 
@@ -289,7 +302,7 @@ class KvCache:
             raise ValueError(f"workspace: a contiguous tensor on cuda:{device}")
         _call(pds.load().pds_attention_tree, device, stream, self.c, q.data_ptr(), out.data_ptr(),
               t, heads, qs, os_, _index(parents, self.n_seqs * t, device, "parents"), softcap,
-              window, max_len, workspace.data_ptr(), workspace.nbytes)
+              _int32(window, "window"), _int32(max_len, "max_len"), workspace.data_ptr(), workspace.nbytes)
         return out
 
     def sync(self, stream=None):

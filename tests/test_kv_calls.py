@@ -59,3 +59,28 @@ def test_a_workspace_has_to_be_memory_of_the_device(lib):
         with pytest.raises(ValueError, match="workspace"):
             cache.attend(q, out=rows(2, 1, 4, 64), workspace=bad)
     assert len(lib.calls) == 1
+
+
+@pytest.mark.parametrize("far", [2 ** 32, 2 ** 31, 2 ** 32 + 3, -2 ** 31 - 1])
+def test_numbers_past_32_bits_are_refused(lib, far):
+    """ctypes would keep the low 32 bits: a window of 2^32 would be none."""
+    cache, spec = make_cache(), kv.RopeSpec(1.0e4, 64)
+    q = rows(2, 1, 4, 64)
+    ws = cuda(torch.empty(64, dtype=torch.uint8))
+    calls = [lambda: cache.attend(q, out=rows(2, 1, 4, 64), workspace=ws, window=far),
+             lambda: cache.attend(q, out=rows(2, 1, 4, 64), workspace=ws, max_len=far),
+             lambda: cache.read(far, 4, k_out=rows(2, 4, 2, 64), v_out=rows(2, 4, 2, 64)),
+             lambda: kv.rope(q, spec, start_pos=far, out=rows(2, 1, 4, 64)),
+             lambda: kv.RopeSpec(1.0e4, 64, rot_dim=far), lambda: kv.RopeSpec(1.0e4, 64, orig_context=far),
+             lambda: kv.KvCache("bf16", 2, far, 2, 64), lambda: kv.KvCache("bf16", far, 2, 2, 64)]
+    for call in calls:
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    many = cuda(torch.empty(1, dtype=torch.bfloat16)).expand(abs(far), 1, 64)
+    many.is_contiguous = lambda: True
+    with pytest.raises(ValueError, match="32 bits"):
+        kv.rope(many, spec, out=many)
+    for number in (2 ** 31 - 1, 5):
+        cache.attend(q, out=rows(2, 1, 4, 64), window=number, workspace=ws)
+        kv.rope(q, spec, start_pos=-number, out=rows(2, 1, 4, 64))
+    assert [name for name, _ in lib.calls] == ["pds_attention_tree", "pds_rope"] * 2
