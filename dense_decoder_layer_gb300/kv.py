@@ -17,6 +17,7 @@ A decode step with drafted tokens::
 
 A call with ``stream`` does what it would do under ``torch.cuda.stream(stream)``:
 what it allocates belongs to that stream, and its inputs have to be ready there.
+The calls record no gradients and refuse tensors that require one.
 """
 
 from __future__ import annotations
@@ -52,6 +53,12 @@ def _int32(x, what):
     if not -2**31 <= x < 2**31:
         raise ValueError(f"{what}: {x} does not fit 32 bits")
     return x
+
+
+def _no_gradient(t, what, instead=""):
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} requires a gradient, which this call does not record: detach it or "
+                         f"call under torch.no_grad(){instead}")
 
 
 def _rows(t, shape, n_lead, device, what):
@@ -137,11 +144,13 @@ class RopeSpec:
 
 def rope(x, spec, positions=None, start_pos=0, out=None, inverse=False, stream=None):
     """The rows of ``x`` [..., heads, head_dim] (bf16) turned at ``positions`` (int32, one per
-    row) or ``start_pos + row``; ``out`` may be ``x``.  ``inverse`` turns back (the gradient)."""
+    row) or ``start_pos + row``; ``out`` may be ``x``.  ``inverse`` turns back: it is the gradient,
+    which a caller takes by that call (an ``x`` that requires one is refused)."""
     shape = x.shape
     heads, hd = shape[-2], shape[-1]
     if hd != spec.head_dim:
         raise ValueError(f"x: heads of {hd} channels, the spec's have {spec.head_dim}")
+    _no_gradient(x, "x", "; the gradient is rope(..., inverse=True) of the result's")
     if out is None:
         out = _new(torch.empty, shape, x.device, stream)
     device, lead = x.get_device(), len(shape) - 2
@@ -248,6 +257,7 @@ class KvCache:
     def write(self, k, v, rope=None, parents=None, positions=None, stream=None):
         """Store new rows [n_seqs, n_tokens, n_kv_heads, head_dim] (bf16) behind the cached
         ones, K rotated by ``rope`` (a :class:`RopeSpec`) at the tokens' positions."""
+        _no_gradient(k, "k"), _no_gradient(v, "v")
         t, device = k.shape[1], self.index
         shape = (self.n_seqs, t, self.n_kv_heads, self.head_dim)
         ks, vs = _rows(k, shape, 2, device, "k"), _rows(v, shape, 2, device, "v")
@@ -287,6 +297,7 @@ class KvCache:
         device = self.index
         if shape[0] != self.n_seqs or shape[3] != self.head_dim:
             raise ValueError(f"q: [{self.n_seqs}, tokens, heads, {self.head_dim}], not {tuple(shape)}")
+        _no_gradient(q, "q")
         if out is None:
             out = _new(torch.empty, shape, self.device, stream)
         qs, os_ = _rows(q, shape, 2, device, "q"), _rows(out, shape, 2, device, "out")

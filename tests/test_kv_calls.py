@@ -84,3 +84,22 @@ def test_numbers_past_32_bits_are_refused(lib, far):
         cache.attend(q, out=rows(2, 1, 4, 64), window=number, workspace=ws)
         kv.rope(q, spec, start_pos=-number, out=rows(2, 1, 4, 64))
     assert [name for name, _ in lib.calls] == ["pds_attention_tree", "pds_rope"] * 2
+
+
+def test_tensors_that_require_a_gradient_are_refused(lib):
+    """The results would lack it without a word."""
+    cache, spec = make_cache(), kv.RopeSpec(1.0e4, 64)
+    ws = cuda(torch.empty(64, dtype=torch.uint8))
+    q, k = rows(2, 1, 4, 64).requires_grad_(), rows(2, 1, 2, 64).requires_grad_()
+    plain = rows(2, 1, 2, 64)
+    calls = [lambda: kv.rope(q, spec, out=rows(2, 1, 4, 64)), lambda: cache.write(k, plain),
+             lambda: cache.write(plain, k),
+             lambda: cache.attend(q, out=rows(2, 1, 4, 64), workspace=ws)]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    assert not lib.calls
+    with torch.no_grad():
+        for call in calls:
+            call()
+    assert len(lib.calls) == 4
