@@ -448,6 +448,25 @@ pds_status make_turns(const char* fn, const pds_rope_spec* spec, int hd, bool in
   return PDS_OK;
 }
 
+// Whether the rows of a cache, `width` elements each, are apart: from the smallest
+// stride on each one steps over all that lies within the ones before it (sizes of
+// one have none).
+bool rows_apart(const pds_cache& c, int64_t ss, int64_t rs, int64_t hs) {
+  struct Dim {
+    int64_t stride, size;
+  } dims[3] = {{ss, c.n_seqs}, {rs, c.capacity}, {hs, c.n_kv_heads}};
+  std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  int64_t extent = c.head_dim;
+  for (const Dim& d : dims) {
+    if (d.size == 1) continue;
+    int64_t span;
+    if (d.stride < extent || __builtin_mul_overflow(d.stride, d.size - 1, &span) ||
+        __builtin_add_overflow(span, extent, &extent))
+      return false;
+  }
+  return extent <= INT64_MAX / 2;  // in bytes
+}
+
 // The kernels' view of a cache, or the reason it is refused.
 pds_status make_view(const char* fn, const pds_cache* cache, pds::CacheView* v) {
   const std::string name = fn;
@@ -484,6 +503,8 @@ pds_status make_view(const char* fn, const pds_cache* cache, pds::CacheView* v) 
     return fail(PDS_EINVAL, name + ": a cache stride is smaller than a head's row");
   if (hs % per16 || rs % per16 || ss % per16)
     return fail(PDS_EINVAL, name + ": cache strides must be multiples of 16 bytes");
+  if (!rows_apart(c, ss, rs, hs))
+    return fail(PDS_EINVAL, name + ": cache strides let rows overlap");
   // half bytes: elements to bytes
   auto bytes = [&](int64_t e) { return c.format == PDS_KV_BF16 ? 2 * e : c.format == PDS_KV_E4M3 ? e : e / 2; };
   *v = pds::CacheView{static_cast<char*>(c.k), static_cast<char*>(c.v), c.k_scale, c.v_scale,

@@ -431,9 +431,10 @@ pds_status pds_rope(const pds_rope_spec* spec, const uint16_t* x, uint16_t* y, i
  * j and kv head g starts at element s seq_stride + j row_stride +
  * g head_stride of k / v (all three 0: packed [n_seqs, capacity, n_kv_heads,
  * head_dim]; an "element" is one channel, so half a byte for PDS_KV_INT4; every
- * stride a multiple of 16 bytes and no smaller than a head's row, and rows
- * must not overlap).  The head's channels are contiguous.  A cache of
- * pds_prefill_dense_stack is the PDS_KV_BF16 cache with n_seqs = 1.
+ * stride a multiple of 16 bytes and no smaller than a head's row).  Strides that
+ * let rows overlap are refused: each has to step over all that the smaller ones
+ * span.  The head's channels are contiguous.  A cache of pds_prefill_dense_stack
+ * is the PDS_KV_BF16 cache with n_seqs = 1.
  *
  * Formats:
  *   PDS_KV_BF16  the values, bf16.

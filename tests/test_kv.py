@@ -242,3 +242,30 @@ def test_expanded_tensors_are_refused():
     row = torch.empty(1, 1, 1, 64, dtype=torch.bfloat16).expand(2, 8, 4, 64)
     with pytest.raises(ValueError, match="expanded"):
         kv.KvCache("bf16", 2, 8, 4, 64, k=row, v=row, lens=torch.zeros(2, dtype=torch.int32))
+
+
+@needs_lib
+@pytest.mark.parametrize("shape,strides,apart", [
+    ((2, 64, 2), (64 * 256, 256, 128), True),        # packed
+    ((2, 64, 2), (64 * 256, 128, 64 * 128), True),   # heads first
+    ((2, 64, 2), (256, 512, 128), True),             # rows first
+    ((2, 64, 2), (64 * 512, 512, 256), True),        # half of wider rows
+    ((2, 64, 2), (64 * 256, 128, 128), False),       # a row is the next one's second head
+    ((2, 64, 2), (256, 256, 128), False),            # sequences a row apart
+    ((2, 64, 2), (64 * 128, 256, 128), False),       # sequences half a cache apart
+    ((2, 64, 3), (64 * 256, 256, 128), False),       # a third head in a row of two
+    ((1, 64, 2), (0, 256, 128), True), ((1, 1, 2), (0, 128, 128), True),
+    ((2, 64, 1), (64 * 128, 128, 128), True),
+    ((2, 64, 2), (2 ** 62, 256, 128), False),        # past 64 bits
+    ((4096, 64, 2), (2 ** 52, 256, 128), False)])
+def test_strides_that_let_rows_overlap_are_refused(shape, strides, apart):
+    """(Where nothing is refused the call ends at the missing device, or the missing memory.)"""
+    n, cap, hkv = shape
+    ss, rs, hs = strides
+    c = _cache(n_seqs=n, capacity=cap, n_kv_heads=hkv, seq_stride=ss, row_stride=rs, head_stride=hs)
+    lib = pds.load()
+    for st in (lib.pds_cache_read(c, 0, 1, PTR, PTR, None),
+               lib.pds_cache_write(c, None, PTR, PTR, 1, 0, 0, None, None, None),
+               lib.pds_attention_tree(c, PTR, PTR, 1, 2 * hkv, 0, 0, None, 0.0, 0, 0, None, 0, None)):
+        assert st != pds.PDS_OK
+        assert ("overlap" in pds.last_error()) == (not apart)
