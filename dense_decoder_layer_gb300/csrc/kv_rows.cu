@@ -459,7 +459,7 @@ cudaError_t launch_rope(const RopeTurns& r, const uint16_t* x, uint16_t* y, int 
   const int slices = std::min((units + threads - 1) / threads, 65535);
   // many rows: enough blocks of two to fill the GPU
   if (rows >= kManyRows)
-    return launch_after(rope_kernel<2>, dim3((rows + 1) / 2), threads, 0, st, x, y, rows, heads, hd,
+    return launch_after(rope_kernel<2>, dim3(rows / 2 + rows % 2), threads, 0, st, x, y, rows, heads, hd,
                         x_stride, y_stride, positions, start_pos, r);
   // few: the units of a row are spread over several blocks
   return launch_after(rope_kernel<1>, dim3(rows, slices), threads, 0, st, x, y, rows, heads, hd,

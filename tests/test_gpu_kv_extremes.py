@@ -303,3 +303,23 @@ def test_large_scores_that_are_neighbours(fmt, t, place):
         cache.sync()
         got = bf16_to_f64(o)
         assert np.all((got >= 1 - EPS) & (got <= 3 * (1 + EPS))), (step, got.min(), got.max())
+
+
+def test_as_many_rope_rows_as_32_bits_count():
+    """2^31 - 1 rows of one 16-wide head, in place; positions past 32 bits at their end."""
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 69 GB")
+    kv = _kv()
+    n = 2 ** 31 - 1
+    x = torch.empty(n, 1, 16, dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(0)
+    at = [0, 1, 2 ** 30 - 1, 2 ** 30, n - 2, n - 1]
+    _, want = _normal(rng, len(at), 1, 16)
+    for i, j in enumerate(at):
+        x[j] = torch.from_numpy(want[i]).to("cuda", torch.bfloat16)
+    spec = kv.RopeSpec(1.0e4, 16)
+    kv.rope(x, spec, start_pos=3, out=x)
+    got = bf16_to_f64(torch.stack([x[j] for j in at]))
+    want = D.rotate(want, [3 + j for j in at], D.scaled_inv_freq(16, 1.0e4))
+    # float64 angles of positions around 2^31 are themselves off by 2^-22
+    assert np.all(np.abs(got - want) <= EPS * np.abs(want) + 2.0 ** -16)
