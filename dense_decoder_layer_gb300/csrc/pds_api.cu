@@ -20,6 +20,7 @@
 #include <vector>
 
 #include "../../include/pds.h"
+#include "facts.h"
 #include "kernels.h"
 #include "kv.h"
 #include "plan.h"
@@ -524,13 +525,8 @@ pds_status row_stride(const char* fn, int64_t packed, int64_t* stride) {
 // The status word and SM count of the current device, looked up once per
 // device; ptr has to be memory of that device.
 constexpr int kMaxDevices = 64;
-struct DeviceFacts {
-  std::once_flag once;
-  uint32_t* status = nullptr;
-  int sms = 0;
-};
 pds_status device_facts(const char* fn, const void* ptr, uint32_t** status, int* sms) {
-  static DeviceFacts facts[kMaxDevices];
+  static pds::DeviceFacts facts[kMaxDevices];
   const std::string name = fn;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
@@ -545,15 +541,18 @@ pds_status device_facts(const char* fn, const void* ptr, uint32_t** status, int*
   if ((at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) ||
       (at.type == cudaMemoryTypeDevice && at.device != dev))
     return fail(PDS_EINVAL, name + ": a buffer is not memory of the current device");
-  DeviceFacts& f = facts[dev];
   std::string err;
-  std::call_once(f.once, [&] {
-    f.status = pds::component_status(&err);
-    if (cudaDeviceGetAttribute(&f.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) f.sms = 0;
-  });
-  if (!f.status || f.sms < 1) return fail(PDS_ELAUNCH, name + ": status word or SM count: " + err);
-  *status = f.status;
-  *sms = f.sms;
+  auto lookup = [&](uint32_t** word, int* n) {
+    *word = pds::component_status(&err);
+    if (!*word) return false;
+    const cudaError_t ce = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+    if (ce != cudaSuccess) err = cudaGetErrorString(ce);
+    return ce == cudaSuccess && *n > 0;
+  };
+  if (!facts[dev].get(lookup, status, sms)) {
+    cudaGetLastError();
+    return fail(PDS_ELAUNCH, name + ": status word or SM count: " + err);
+  }
   return PDS_OK;
 }
 

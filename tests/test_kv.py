@@ -269,3 +269,32 @@ def test_strides_that_let_rows_overlap_are_refused(shape, strides, apart):
                lib.pds_attention_tree(c, PTR, PTR, 1, 2 * hkv, 0, 0, None, 0.0, 0, 0, None, 0, None)):
         assert st != pds.PDS_OK
         assert ("overlap" in pds.last_error()) == (not apart)
+
+
+def test_a_failed_lookup_of_a_device_is_made_again(tmp_path):
+    """facts.h as the calls use it, in a program of its own: the first lookups fail."""
+    import shutil
+    import subprocess
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no g++")
+    src = tmp_path / "facts.cpp"
+    src.write_text("""
+        #include "facts.h"
+        int main() {
+          pds::DeviceFacts facts;
+          uint32_t word = 0, *status = nullptr;
+          int sms = 0, looked = 0;
+          bool good = false;
+          auto lookup = [&](uint32_t** s, int* n) { ++looked; *s = &word; *n = good ? 152 : 0; return good; };
+          if (facts.get(lookup, &status, &sms) || facts.get(lookup, &status, &sms)) return 1;
+          if (status || sms) return 2;
+          good = true;
+          for (int i = 0; i < 3; ++i)
+            if (!facts.get(lookup, &status, &sms) || status != &word || sms != 152) return 3;
+          return looked == 3 ? 0 : 4;
+        }""")
+    csrc = os.path.join(os.path.dirname(pds.__file__), "csrc")
+    subprocess.run([cxx, "-std=c++17", "-pthread", "-I", csrc, str(src), "-o", str(tmp_path / "facts")],
+                   check=True, timeout=120)
+    assert subprocess.run([str(tmp_path / "facts")], timeout=20).returncode == 0
