@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 #pragma unroll
     for (int e = 0; e < 2; ++e) m_ref[n][e] = -INFINITY, l[n][e] = 0.f;
 
-  const float cap = VAR ? a.cap * a.scale_log2 : 0.f;  // in powers of two
+  const SoftCap cap = soft_cap(VAR ? a.cap * a.scale_log2 : 0.f);  // (in powers of two)
   uint32_t v_exp = kMinScaleExp;  // exponent of the largest V scale so far: O's unit
   const uint32_t q_frag = smem_addr(smem) + C::kQ;
   uint32_t st = ring;  // the step's stage
@@ -611,13 +611,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float f = e & 1 ? rs.y : rs.x;
-        float z = s[n][e] * (F::kBf16 ? f : kscale[e >> 1] * f);
-        if (VAR && cap > 0.f) {
-          // c tanh(z / c) = c - 2 c / (2^(2 log2(e) z / c) + 1)
-          const float ex = exp2_fast(z * (2.0f * 1.4426950408889634f / cap));
-          z = cap - __fdividef(2.0f * cap, ex + 1.0f);
-        }
-        s[n][e] = z;
+        s[n][e] *= F::kBf16 ? f : kscale[e >> 1] * f;
+      }
+    }
+    if (VAR && cap.c > 0.f) {
+      if (cap.wide()) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] = capped_wide(s[n][e], cap);
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] = capped(s[n][e], cap);
       }
     }
     // a step that holds new tokens, the end, or a window's lower edge

@@ -327,6 +327,27 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// c tanh(y / c) = c - 2 c / (2^(2 log2(e) y / c) + 1), scores and cap in powers of two.
+// The difference is off by some 2^-22 c, which a small cap makes nothing (2^-15 in
+// the exponent at 64) and a large one more than the scores: beyond that, where |y| is
+// below c / 4, it is y (1 - u^2/3 + 2 u^4/15 - 17 u^6/315), u = y / c, the start of
+// tanh's series, off by 2^-21 of y, and elsewhere c times a difference of 2^-1 and more.
+struct SoftCap {
+  float c, rate;
+  __device__ __forceinline__ bool wide() const { return c > 64.f * 1.4426950408889634f; }
+};
+__device__ __forceinline__ SoftCap soft_cap(float c) {
+  return SoftCap{c, fminf(2.0f * 1.4426950408889634f / c, 3.0e38f)};
+}
+__device__ __forceinline__ float capped(float y, const SoftCap& s) {
+  return s.c - __fdividef(2.0f * s.c, exp2_fast(y * s.rate) + 1.0f);
+}
+__device__ __forceinline__ float capped_wide(float y, const SoftCap& s) {
+  const float x = y * s.rate, u2 = x * x * (0.25f * 0.6931471805599453f * 0.6931471805599453f);
+  const float near = y * (1.0f + u2 * (-1.0f / 3 + u2 * (2.0f / 15 - u2 * (17.0f / 315))));
+  return u2 < 0.0625f ? near : s.c * (1.0f - __fdividef(2.0f, exp2_fast(x) + 1.0f));
+}
+
 // 8- and 4-bit rows go into the products as fp16, whose 11 bits hold every code
 // exactly and round P eight times finer than bf16 would; the conversions are
 // few and cheap (one instruction per pair of e4m3 codes, where spreading the

@@ -848,7 +848,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int lo = VAR && a.window > 0 ? len + depth - a.window + 1 : 0;
 
     const bool warp_live = r0 + (two_tiles ? s * kTileRows : 0) + (warp & 3) * 32 < rows;
-    const float sc = a.scale_log2, cap = VAR ? a.cap * a.scale_log2 : 0.f;  // powers of two
+    const float sc = a.scale_log2;
+    const SoftCap cap = soft_cap(VAR ? a.cap * a.scale_log2 : 0.f);  // (in powers of two)
     float m_ref = -INFINITY, l = 0.f;
     uint32_t v_exp = kMinScaleExp;  // O's unit: the exponent of the largest V scale so far
     const int n_mine = s == 0 ? n_tiles0 : n_tiles1;
@@ -904,16 +905,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int x = 0; x < kKeys / 2; ++x) mul2(z[2 * x], z[2 * x + 1], q_ratio, q_ratio);
           }
-          if (VAR && cap > 0.f) {
+          if (VAR && cap.c > 0.f) {
+            auto apply = [&](auto&& one) {
 #pragma unroll
-            for (int x = 0; x < kKeys; ++x) {
-              float f = sc;
-              if constexpr (C::kQuant) f = __uint_as_float(lds32(words + x * 4));
-              // c tanh(z / c) = c - 2 c / (2^(2 log2(e) z / c) + 1)
-              const float y = z[x] * f;
-              const float e = exp2_fast(y * (2.0f * 1.4426950408889634f / cap));
-              z[x] = cap - __fdividef(2.0f * cap, e + 1.0f) - less;
-            }
+              for (int x = 0; x < kKeys; ++x) {
+                float f = sc;
+                if constexpr (C::kQuant) f = __uint_as_float(lds32(words + x * 4));
+                z[x] = one(z[x] * f, cap) - less;
+              }
+            };
+            if (cap.wide())
+              apply([](float y, const SoftCap& k) { return capped_wide(y, k); });
+            else
+              apply([](float y, const SoftCap& k) { return capped(y, k); });
           } else if constexpr (C::kQuant) {
 #pragma unroll
             for (int x = 0; x < kKeys / 4; ++x) {

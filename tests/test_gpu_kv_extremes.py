@@ -323,3 +323,20 @@ def test_as_many_rope_rows_as_32_bits_count():
     want = D.rotate(want, [3 + j for j in at], D.scaled_inv_freq(16, 1.0e4))
     # float64 angles of positions around 2^31 are themselves off by 2^-22
     assert np.all(np.abs(got - want) <= EPS * np.abs(want) + 2.0 ** -16)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int4"])
+@pytest.mark.parametrize("t,h,hkv,hd", [(1, 3, 1, 128), (5, 4, 2, 64), (40, 4, 2, 64), (100, 6, 2, 128)])
+def test_any_softcap(fmt, t, h, hkv, hd):
+    """Caps far above the scores leave them as they are; far below, all are the cap."""
+    kv = _kv()
+    rng = np.random.default_rng(t + hd)
+    cache, k64, v64 = _filled(kv, rng, fmt, 1, 300 + t, hkv, hd, [300])
+    q, q64 = _normal(rng, 1, t, h, hd, scale=3.0)
+    for softcap in (1.0e-3, 0.5, 10.0, 60.0, 70.0, 1.0e3, 1.0e5, 1.0e8, 1.0e30, 3.0e38):
+        o = cache.attend(q, softcap=softcap)
+        cache.sync()
+        _close(cache, o, q64, k64, v64, 300, softcap=softcap)
+    # without one: within the same distance of the same values (a cap of 3e38 moves them by
+    # less than 1e-70), so the two calls differ by two such tolerances at most
+    _close(cache, cache.attend(q), q64, k64, v64, 300, softcap=3.0e38)
