@@ -692,6 +692,8 @@ pds_status pds_attention_tree(const pds_cache* cache, const uint16_t* q, uint16_
     return rc;
   if (static_cast<int64_t>(cache->n_seqs) * n_tokens * n_heads > INT32_MAX)
     return fail(PDS_DECLINED, "declined: pds_attention_tree: too many query rows");
+  if (q == o)  // (its blocks read rows of q after others have written theirs of o)
+    return fail(PDS_EINVAL, "pds_attention_tree: q and o are the same buffer");
   if ((rc = device_facts("pds_attention_tree", cache->k, &a.status, &a.num_sms)) != PDS_OK)
     return rc;
   if (workspace && workspace_bytes < pds::tree_attention_ws_bytes(

@@ -518,7 +518,7 @@ pds_status pds_cache_read(const pds_cache* cache, int32_t first_row, int32_t row
  * head groups as in pds_attention; the softmax's statistics are float32.
  *  q, o     bf16, token t of sequence s at element (s n_tokens + t) * q_stride
  *           (o_stride), [n_heads, head_dim] each (0: packed; multiples of 8).
- *           o may not overlap q.
+ *           o may not overlap q (the same buffer is refused).
  *  n_tokens 1 .. 256; n_heads a multiple of n_kv_heads, at most 8192.
  *  max_len  an upper bound of lens known on the host, or 0 (the capacity less
  *           n_tokens); sizes the launch, not the result's meaning.  A longer

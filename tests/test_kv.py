@@ -298,3 +298,34 @@ def test_a_failed_lookup_of_a_device_is_made_again(tmp_path):
     subprocess.run([cxx, "-std=c++17", "-pthread", "-I", csrc, str(src), "-o", str(tmp_path / "facts")],
                    check=True, timeout=120)
     assert subprocess.run([str(tmp_path / "facts")], timeout=20).returncode == 0
+
+
+@needs_lib
+def test_attention_in_place_is_refused():
+    lib, c = pds.load(), _cache()
+    assert lib.pds_attention_tree(c, PTR, PTR, 1, 4, 0, 0, None, 0.0, 0, 0, None, 0, None) == pds.PDS_EINVAL
+    assert "same buffer" in pds.last_error()
+    lib.pds_attention_tree(c, PTR, 2 * PTR, 1, 4, 0, 0, None, 0.0, 0, 0, None, 0, None)
+    assert "same buffer" not in pds.last_error()
+
+
+def test_yarn_by_counting_turns():
+    """The ramp's ends found from what they mean, without the closed form: the (real) index of
+    the pair that turns beta times within the original context, by bisection of its turns."""
+    theta, rot, ctx, factor, fast, slow = 5.0e5, 128, 8192, 8.0, 32.0, 1.0
+
+    def index(beta):
+        lo, hi = -64.0, 2.0 * rot
+        for _ in range(200):
+            mid = (lo + hi) / 2
+            turns = ctx * theta ** (-2 * mid / rot) / (2 * math.pi)
+            lo, hi = (mid, hi) if turns > beta else (lo, mid)
+        return lo
+    first, last = max(0, math.floor(index(fast))), min(rot - 1, math.ceil(index(slow)))
+    w = D.scaled_inv_freq(rot, theta, scaling="yarn", factor=factor, orig_context=ctx,
+                          beta_fast=fast, beta_slow=slow)
+    for i in range(rot // 2):
+        kept = theta ** (-2 * i / rot)
+        part = min(1.0, max(0.0, (i - first) / (last - first)))
+        assert abs(w[i] - (kept * (1 - part) + kept / factor * part)) <= 1e-12 * kept
+    assert 0 < first < last < rot // 2
