@@ -340,3 +340,38 @@ def test_any_softcap(fmt, t, h, hkv, hd):
     # without one: within the same distance of the same values (a cap of 3e38 moves them by
     # less than 1e-70), so the two calls differ by two such tolerances at most
     _close(cache, cache.attend(q), q64, k64, v64, 300, softcap=3.0e38)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int4"])
+def test_accepted_rows_that_moved_up_are_the_rows_decoded_one_by_one(fmt):
+    """Codes and scale words: afterwards the two caches give the same bits."""
+    kv = _kv()
+    rng = np.random.default_rng(71)
+    h, hkv, hd, length = 6, 2, 128, 333
+    spec = kv.RopeSpec(5.0e5, hd)
+    parents, path = [-1, 0, 0, 2, 1, 3, 5, 3], [0, 2, 3, 5, 6]
+    tree, _, _ = _filled(kv, rng, fmt, 1, 400, hkv, hd, [length])
+    words = [] if fmt == "bf16" else [tree.k_scale, tree.v_scale]
+    one = kv.KvCache(fmt, 1, 400, hkv, hd, k=tree.k.clone(), v=tree.v.clone(), lens=tree.lens.clone(),
+                     k_scale=words[0].clone() if words else None,
+                     v_scale=words[1].clone() if words else None)
+    k, v = (_normal(rng, 1, len(parents), hkv, hd)[0] for _ in range(2))
+    tree.write(k, v, rope=spec, parents=_i32([parents]))
+    for node in path:
+        one.write(k[:, node:node + 1], v[:, node:node + 1], rope=spec)
+        one.lens += 1
+    src = torch.tensor(path, device="cuda") + length
+    to = slice(length, length + len(path))
+    for x in (tree.k, tree.v):
+        x.view(torch.uint8)[:, to] = x.view(torch.uint8)[:, src]
+    for x in words:
+        x[:, :, to] = x[:, :, src]
+    tree.lens += len(path)
+    for x, y in zip(tree.read(0, 338), one.read(0, 338)):
+        assert torch.equal(x, y)
+    q, _ = _normal(rng, 1, 3, h, hd)
+    k, v = (_normal(rng, 1, 3, hkv, hd)[0] for _ in range(2))
+    for cache in (tree, one):
+        cache.write(k, v, rope=spec)
+    assert torch.equal(tree.attend(q), one.attend(q))
+    tree.sync()
