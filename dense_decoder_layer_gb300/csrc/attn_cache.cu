@@ -13,7 +13,7 @@
 // the keys), and o (once).
 //
 // What bounds it: every cached row is used by T G query rows, one to a few
-// dozen, so at 2 T G flop per byte of bf16 the call is bound by reading the
+// dozen, so at T G flop per byte of bf16 the call is bound by reading the
 // cache (HBM); few-row calls by latency.  Hence the split: the keys of a
 // sequence are cut into chunks over all SMs, each block holds the T G rows
 // of one kv head (up to 32) and its 8 warps walk the chunk's 16-key steps
@@ -23,18 +23,18 @@
 // tile (a decode step has 3 or 4: a query-major tile would be 3/4 empty), and
 // O^T = V^T P^T the same way, P^T being S^T's fragments transposed inside the
 // warp.  A key's scales are then one factor per accumulator row, and a running
-// maximum that moves only when a score exceeds it by 2^8 needs no reduction
-// over keys until the end.
+// reference that moves only when a score exceeds it by 8 (a weight of 2^8) needs no
+// reduction over keys until the end.
 //
 // Chunks write unnormalised rows and (maximum, sum) to the workspace; a second
 // kernel joins them in chunk order.  The chunk length is made from the
 // sequences' lengths on the device (they change between replays of a graph).
 //
 // Measured (32/8 heads of 128; replayed graphs, so without the host's part), one
-// token of 16 sequences of 4096 rows: bf16 44.5 us (6.0 TB/s), e4m3 29.7 (4.7),
-// 4-bit 31.3 (2.3): bf16 is bound by HBM, the others by the conversion's
+// token of 16 sequences of 4096 rows: bf16 44.5 us (6.0 TB/s), e4m3 29.4 (4.7),
+// 4-bit 31.1 (2.3): bf16 is bound by HBM, the others by the conversion's
 // instructions (the ALU pipe is the busiest, 38% and 56%) on the SMs that hold
-// two of the 256 blocks.  24/8 heads, one token over 2048 bf16 rows: 5.9 us, of
+// two of the 256 blocks.  24/8 heads, one token over 2048 bf16 rows: 5.8 us, of
 // which some 4 are a launch, fetching the code and one round of loads.
 #include <cuda_bf16.h>
 #include <math.h>
@@ -1036,9 +1036,10 @@ constexpr int kMaxCluster = 8;
 constexpr int kClusterChunks = 16;
 
 // From this many query rows per kv head on, the tcgen05 kernel.  us here and there
-// for 8 sequences of 4096 rows, 24 rows: bf16 33.6/30.6, e4m3 33.3/35.9, 4-bit
-// 33.9/35.0; one sequence of 8192: 14.3/17.1, 14.1/18.1, 14.6/18.0.  36 rows (two
-// row tiles here): 45.5/31.2, 48.8/37.2, 53.4/36.2.
+// for 8 sequences of 4096 rows, 24 rows: bf16 33.9/32.2, e4m3 33.8/36.5, 4-bit
+// 34.5/36.1; one sequence of 8192: 13.1/17.0, 13.3/18.8, 13.9/19.0.  36 rows (two
+// row tiles here): 46.9/32.8, 49.4/37.3, 53.6/37.1.  (Several bf16 sequences alone would
+// gain a twentieth from a limit of their own.)
 constexpr int kTileMinRows = 33;
 
 struct Shape {

@@ -10,9 +10,9 @@
 // at once.
 //
 // Measured (replayed graphs): 256 tokens of 32/8 heads of 128 over 8192 bf16 rows
-// 43.8 us (0.79 PFLOP/s), e4m3 56.4 (0.61); 64 tokens of 24/8 over 32768 4-bit rows
-// 50.6 (0.51); 32 tokens of 4 sequences over 16384 bf16 rows 50.8 (5.3 TB/s).  A
-// tile of 64 keys for both streams takes ~1900 cycles with bf16 rows, ~2600 with
+// 44.3 us (0.78 PFLOP/s), e4m3 56.5 (0.61); 64 tokens of 24/8 over 32768 4-bit rows
+// 50.6 (0.51) as a chain, 3 more as a tree; 32 tokens of 4 sequences over 16384 bf16
+// rows 50.8 (5.3 TB/s).  A tile of 64 keys for both streams takes ~1900 cycles with bf16 rows, ~2600 with
 // codes.  With the softmax taken out it takes ~1500 (products with 64 columns
 // read their 128 rows of Q from shared memory each time: 48 cycles where the
 // multipliers need 32), with the products taken out nearly the whole time
@@ -34,9 +34,9 @@
 //                4-bit codes land in slots private to their thread, which
 //                turns them into the fp16 tile (no barrier in between)
 //   warps 12-19  softmax, one thread per query row (so nothing is exchanged):
-//                64 scores at a time, exponentials against the row's reference
-//                maximum, which moves only when a tile's weights sum to more
-//                than 2^8 (no maximum is taken otherwise)
+//                64 scores at a time, exponentials against the row's reference,
+//                which moves only when a tile's weights sum to more than 2^8 (no
+//                maximum is taken otherwise, and at most one per tile)
 // The key's scales are applied to the scores (K) and to P (V): the tiles of 8-
 // and 4-bit rows hold the codes themselves, in fp16.
 //

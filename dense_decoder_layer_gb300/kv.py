@@ -317,6 +317,6 @@ class KvCache:
         return out
 
     def sync(self, stream=None):
-        """Wait for the stream; raises PdsError where a call met a length or a parent that it
-        could not serve."""
+        """Wait for the stream; raises PdsError where a call on this device, of any stream and any
+        cache, met a length or a parent that it could not serve (reported once)."""
         _call(pds.load().pds_component_sync, self.index, stream)

@@ -419,8 +419,10 @@ typedef struct pds_rope_spec {
  * or, with positions NULL, start_pos + r.  inverse != 0 turns the other way:
  * for mscale 1 it undoes the rotation, and for any mscale it is the
  * transpose, i.e. the gradient with respect to x of a loss whose gradient
- * with respect to y is given as x.  Angles are exact to 2^-31 of a turn at any position;
- * the products are float32, rounded once to bf16.
+ * with respect to y is given as x.  A position's angle is exact to 2^-31 of a
+ * turn but for the frequency, which is float64 arithmetic: off by at most 2^-48 of
+ * itself, so the angle by that part of the turns made until there (2^-30 of a turn
+ * at position 2^20, 2^-19 at 2^31).  The products are float32, rounded once to bf16.
  */
 pds_status pds_rope(const pds_rope_spec* spec, const uint16_t* x, uint16_t* y, int32_t rows,
                     int32_t n_heads, int32_t head_dim, int64_t x_stride, int64_t y_stride,
@@ -450,7 +452,7 @@ pds_status pds_rope(const pds_rope_spec* spec, const uint16_t* x, uint16_t* y, i
  *                (code - z) * scale.
  * A row whose scale would be below the smallest normal float32 is stored as
  * zeros (scale 0); a row with an infinity or a NaN has a NaN scale and
- * stands for NaN throughout.  The scale words of sequence s, kv head g and
+ * stands for NaN throughout (codes of NaN are never stored, and mean nothing).  The scale words of sequence s, kv head g and
  * row j sit at [(s n_kv_heads + g) capacity + j].
  *
  * lens[s] is the number of cached rows of sequence s before the call.  The
@@ -515,7 +517,12 @@ pds_status pds_cache_read(const pds_cache* cache, int32_t first_row, int32_t row
  * written) over its cache: token t sees the lens[s] cached rows, its
  * ancestors and itself; with window > 0 only those whose position (a cached
  * row's is its index) is above its own less window.  Scores, softcap and the
- * head groups as in pds_attention; the softmax's statistics are float32.
+ * head groups as in pds_attention; the softmax's statistics are float32.  The
+ * weights that go into the products with V are rounded, to bf16 (2^-8 of each at
+ * most) over a bf16 cache and to fp16 (2^-11) over codes; the sum that divides them is
+ * not.  Over codes a weight times its V scale is held in fp16: what is lost below
+ * its smallest steps is under 2^-27 of the token's largest such product per key,
+ * as long as the V scales lie within 2^80 of each other.
  *  q, o     bf16, token t of sequence s at element (s n_tokens + t) * q_stride
  *           (o_stride), [n_heads, head_dim] each (0: packed; multiples of 8).
  *           o may not overlap q (the same buffer is refused).
@@ -531,7 +538,8 @@ pds_status pds_cache_read(const pds_cache* cache, int32_t first_row, int32_t row
  *           max_len and on lens; the same call on the same inputs gives the
  *           same bits.
  * A row that sees no key (padding) is zero.  An infinity or a NaN in a row
- * that a token does not see does not reach its output.
+ * that a token does not see does not reach its output, nor does a finite value of
+ * any size, nor another token's query (a padding token's may hold anything).
  */
 pds_status pds_attention_tree(const pds_cache* cache, const uint16_t* q, uint16_t* o,
                               int32_t n_tokens, int32_t n_heads, int64_t q_stride,
