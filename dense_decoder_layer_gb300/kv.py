@@ -16,7 +16,8 @@ A decode step with drafted tokens::
     cache.lens += accepted            # after the accepted rows are in place
 
 A call with ``stream`` does what it would do under ``torch.cuda.stream(stream)``:
-what it allocates belongs to that stream, and its inputs have to be ready there.
+what it allocates belongs to that stream, its inputs have to be ready there and to be
+kept until it is done with them.
 The calls record no gradients and refuse tensors that require one.
 """
 
@@ -201,22 +202,30 @@ class KvCache:
             _need(t.is_contiguous() if packed else t.stride(-1) == 1, f"{what}: layout")
             return t
 
-        self.k, self.v = have(k, shape, dtype, "k", False), have(v, shape, dtype, "v", False)
-        packed = self.k.is_contiguous() and self.v.is_contiguous()
-        _need(packed or self.k.stride() == self.v.stride(), "k and v: the same strides")
-        _need(packed or any(self.k.stride()[:3]), "k and v: rows of their own (an expanded tensor?)")
-        self.k_scale = self.v_scale = None
+        k, v = have(k, shape, dtype, "k", False), have(v, shape, dtype, "v", False)
+        packed = k.is_contiguous() and v.is_contiguous()
+        _need(packed or k.stride() == v.stride(), "k and v: the same strides")
+        _need(packed or any(k.stride()[:3]), "k and v: rows of their own (an expanded tensor?)")
         if word is not None:
-            self.k_scale = have(k_scale, words, word, "k_scale", True)
-            self.v_scale = have(v_scale, words, word, "v_scale", True)
+            k_scale = have(k_scale, words, word, "k_scale", True)
+            v_scale = have(v_scale, words, word, "v_scale", True)
+        else:
+            k_scale = v_scale = None
+        self._tensors = k, v, k_scale, v_scale
         self._lens = have(lens, (self.n_seqs,), torch.int32, "lens", True)
-        seq, row, head, _ = (0, 0, 0, 0) if packed else self.k.stride()
+        seq, row, head, _ = (0, 0, 0, 0) if packed else k.stride()
         self.c = pds.pds_cache(
             FORMATS[fmt], self.n_seqs, self.capacity, self.n_kv_heads, self.head_dim, 0,
-            seq * self.per_byte, row * self.per_byte, head * self.per_byte, self.k.data_ptr(),
-            self.v.data_ptr(), self.k_scale.data_ptr() if word is not None else None,
-            self.v_scale.data_ptr() if word is not None else None, self._lens.data_ptr())
+            seq * self.per_byte, row * self.per_byte, head * self.per_byte, k.data_ptr(), v.data_ptr(),
+            k_scale.data_ptr() if word is not None else None,
+            v_scale.data_ptr() if word is not None else None, self._lens.data_ptr())
         self._ws = {}  # attention workspace by (tokens, heads, stream)
+
+    # The kernels have these tensors' addresses: they can be written to, not replaced.
+    k = property(lambda self: self._tensors[0], doc="The K rows.")
+    v = property(lambda self: self._tensors[1], doc="The V rows.")
+    k_scale = property(lambda self: self._tensors[2], doc="K's scale words (None: bf16).")
+    v_scale = property(lambda self: self._tensors[3], doc="V's scale words (None: bf16).")
 
     @property
     def lens(self):

@@ -103,3 +103,14 @@ def test_tensors_that_require_a_gradient_are_refused(lib):
         for call in calls:
             call()
     assert len(lib.calls) == 4
+
+
+def test_the_tensors_of_a_cache_cannot_be_replaced():
+    """The C ABI's struct holds their addresses: another tensor in their place would not be
+    used, and the old one's memory could be gone."""
+    cache = make_cache()
+    for name in ("k", "v", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, torch.zeros_like(cache.k))
+    cache.k[0, 0] = 1.0
+    assert cache.c.k == cache.k.data_ptr() and cache.c.v == cache.v.data_ptr()
