@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
   int tok[NT][2], pos[NT][2];
   // What scores are multiplied by besides K's scales, to be in powers of two.  Kept in
   // registers where there are any left, else read anew for each step.
-  constexpr bool kKeep = F::kBf16 || NT == 1;
+  constexpr bool kKeep = F::kBf16 || NT == 1 || (NT == 4 && HD == 64);
   float2 row_scale[kKeep ? NT : 1];
   int pos_hi = 0;  // windows of all rows of the tile start at or below pos_hi - window + 1
 #pragma unroll
@@ -545,8 +545,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
   if (VAR) pos_hi = __reduce_max_sync(0xffffffffu, pos_hi);
   const uint32_t row_scales = smem_addr(smem) + C::kQInv + 8 * t4;
   if constexpr (!F::kBf16 && kKeep) {
-    const uint2 w = lds64(row_scales);
-    row_scale[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint2 w = lds64(row_scales + 32 * n);
+      row_scale[n] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+    }
   }
 
   float o[F::kMTiles][NT][4];
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float2 rs = make_float2(a.scale_log2, a.scale_log2);
-      if constexpr (!F::kBf16 && kKeep) rs = row_scale[0];
+      if constexpr (!F::kBf16 && kKeep) rs = row_scale[n];
       if constexpr (!kKeep) {
         const uint2 w = lds64(row_scales + 32 * n);
         rs = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
@@ -672,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::kBlocks)
         for (int e = 0; e < 2; ++e)
           if (seen[e]) v_top = max(v_top, min(finite_bits(vscale[e]) >> 23, kMaxScaleExp));
         v_top = __reduce_max_sync(0xffffffffu, v_top);
-        if (v_top > v_exp && i > 0) {
+        if (__builtin_expect(v_top > v_exp && i > 0, 0)) {
           float most = 0.f;  // (sums are not negative: they order as their bits do)
 #pragma unroll
           for (int n = 0; n < NT; ++n) most = fmaxf(most, fmaxf(l[n][0], l[n][1]));
