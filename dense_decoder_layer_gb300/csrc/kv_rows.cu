@@ -23,6 +23,8 @@
 namespace pds {
 namespace {
 
+// The kernels below start while the one before them may still write what they read, and wait for it: no
+// pointer to const is __restrict__, which would let its loads pass the wait.
 constexpr int kRowThreads = 256;
 
 // One block per ROWS rows (and slice of their units): a thread's units of all of
@@ -34,8 +36,7 @@ template <int ROWS>
 __global__ void __launch_bounds__(kRowThreads) rope_kernel(const uint16_t* x, uint16_t* y, int rows,
                                                            int heads, int hd, int64_t x_stride,
                                                            int64_t y_stride,
-                                                           const int32_t* __restrict__ positions,
-                                                           int start_pos,
+                                                           const int32_t* positions, int start_pos,
                                                            const __grid_constant__ RopeTurns r) {
   __shared__ float2 table[ROWS * kMaxTurnPairs];
   const int row0 = blockIdx.x * ROWS;
@@ -96,9 +97,8 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const uint16_t* x, ui
 template <int FMT, int HD>
 __global__ void __launch_bounds__(kRowThreads)
     cache_write_kernel(const __grid_constant__ CacheView c, const __grid_constant__ RopeTurns r,
-                       const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
-                       int n_tokens, int64_t k_stride, int64_t v_stride,
-                       const int32_t* __restrict__ parents, const int32_t* __restrict__ positions,
+                       const uint16_t* k, const uint16_t* v, int n_tokens, int64_t k_stride,
+                       int64_t v_stride, const int32_t* parents, const int32_t* positions,
                        uint32_t* status) {
   constexpr int kPerHead = HD / 16;
   __shared__ float2 table[HD / 2];

@@ -240,6 +240,9 @@ __global__ void __launch_bounds__(kMaxScanThreads, 1)
 }
 
 // ------------------------------------------------------- rows by slot
+//
+// Slots, positions and rows may come from the kernel before, which is waited for: no pointer to
+// const is __restrict__, which would let its loads pass the wait.
 
 constexpr int kRowThreads = 256;
 
@@ -267,9 +270,8 @@ __device__ __forceinline__ int64_t word_at(const PageView& p, int32_t slot, int 
 template <int FMT, int HD, int ROWS>
 __global__ void __launch_bounds__(kRowThreads)
     pages_write_kernel(const __grid_constant__ PageView p, const __grid_constant__ RopeTurns r,
-                       const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
-                       const int32_t* __restrict__ slots, int n_rows, int64_t k_stride,
-                       int64_t v_stride, const int32_t* __restrict__ positions, uint32_t* status) {
+                       const uint16_t* k, const uint16_t* v, const int32_t* slots, int n_rows,
+                       int64_t k_stride, int64_t v_stride, const int32_t* positions, uint32_t* status) {
   constexpr int kPerHead = HD / 16;
   __shared__ float2 table[ROWS][HD / 2];
   const int row0 = blockIdx.x * ROWS;
@@ -364,9 +366,8 @@ constexpr int kReadThreads = 128;
 // 9.7 thousand 4-bit rows of 8 x 64 8.9.
 template <int FMT, int HD>
 __global__ void __launch_bounds__(kReadThreads)
-    pages_read_kernel(const __grid_constant__ PageView p, const int32_t* __restrict__ slots,
-                      int n_rows, uint16_t* __restrict__ k_out, uint16_t* __restrict__ v_out,
-                      uint32_t* status) {
+    pages_read_kernel(const __grid_constant__ PageView p, const int32_t* slots, int n_rows,
+                      uint16_t* __restrict__ k_out, uint16_t* __restrict__ v_out, uint32_t* status) {
   constexpr int kPerHead = HD / 16, kRows = 2, kFlight = 2;
   const bool is_v = k_out == nullptr || blockIdx.y == 1;
   char* pool = is_v ? p.v : p.k;
