@@ -1185,11 +1185,13 @@ __global__ void __launch_bounds__(Cfg<FMT, HD, GT>::kThreads, kBlocksPerSm)
         // while the products end: what the sums are good for
         float scale[GT], shift[kZ];
         const float unit = C::kCodes ? exp2_fast((lv0 - 7.f) * 0.5f) : 1.f;  // (its square may be out of range)
+        const bool to_end = w.t + 1 == w.cur.tiles, whole = from_start && to_end;
 #pragma unroll
         for (int g = 0; g < GT; ++g) {
           const float4 t = ld_shared_f4(sum_at + g * 16);
           l[g] = (t.x + t.y) + (t.z + t.w);
-          scale[g] = unit * __frcp_rn(l[g]);
+          // (a part whose scores are all -infinity counts for nothing in the join, but its 0 / 0 would)
+          scale[g] = l[g] == 0.f && !whole ? 0.f : unit * __frcp_rn(l[g]);
           if constexpr (C::kInt4) {
             const float4 z = ld_shared_f4(sum_at + (GT + g) * 16);
             shift[g] = (z.x + z.y) + (z.z + z.w);
@@ -1208,7 +1210,6 @@ __global__ void __launch_bounds__(Cfg<FMT, HD, GT>::kThreads, kBlocksPerSm)
         of_unit = 0;
         const int kvh = w.kvh, head0 = w.part * a.chunk;
         const int heads = min(a.chunk, a.group - head0);
-        const bool to_end = w.t + 1 == w.cur.tiles;
         // lane -> channel: 64 rows of O lie in the first 16 lanes of each warp
         const bool has = HD == 128 || lane < 16;
         const int pos = HD == 128 ? tid : 16 * warp + lane;
@@ -1228,7 +1229,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD, GT>::kThreads, kBlocksPerSm)
                 asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sb + kMaxHeads * HD * 4 + g * 8),
                              "f"(m[g] - lv0), "f"(l[g])
                              : "memory");
-            } else if (from_start && to_end) {
+            } else if (whole) {
               out[g * HD] = f32_to_bf16(x);
             } else {
               a.part[(static_cast<int64_t>(slot) * kMaxHeads + g) * HD + ch] = x;

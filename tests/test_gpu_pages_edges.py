@@ -57,6 +57,36 @@ def test_values_that_are_not_finite_stay_with_their_sequence_and_head(fmt):
         assert np.all(np.abs(bf16_to_f64(ref)[s, h] - want[h]) <= 2.0 ** -7 * size[h] + 1e-6)
 
 
+@pytest.mark.parametrize("group,hd", [(3, 128), (8, 64)])
+@pytest.mark.parametrize("extra", [0, 4000])
+@pytest.mark.parametrize("where", ["last", "tile", "first", "both"])
+def test_scores_of_minus_infinity_weigh_nothing(where, extra, group, hd):
+    """A part of a cut sequence may hold only rows that weigh nothing: the others make the result, whichever
+    schedule cuts it (clusters over a narrow table, equal shares over a wide one).
+
+    |o| and the weighted sum of |v| that the errors are measured by are both below `size`: 2^-8 of it for the
+    result's rounding, and less than that for the scores (sums of |q k| below 400, times 136 2^-23 twice)
+    and the weights (2^-16)."""
+    rng = np.random.default_rng(21)
+    hkv, lens = 8, [1024, 130]
+    cache = _cache("bf16", lens, [1, 1], 16, hkv, hd, extra=extra)
+    total = [x + 1 for x in lens]
+    k = rng.standard_normal((sum(total), hkv, hd)).astype(np.float32)
+    v = rng.standard_normal((sum(total), hkv, hd)).astype(np.float32)
+    rows = {"last": [1024], "tile": range(256, 384), "first": range(128), "both": [*range(512), 1024]}[where]
+    k[list(rows), :, 5] = -np.inf
+    _write_all(cache, total, _bf16(k)[0], _bf16(v)[0])
+    q = rng.standard_normal((2, hkv * group, hd)).astype(np.float32)
+    q[:, :, 5] = np.abs(q[:, :, 5]) + 0.1
+    q, q64 = _bf16(q)
+    got = bf16_to_f64(cache.attend(q))
+    cache.sync()
+    for s, kv in enumerate(_values(cache, total)):
+        want, size, _ = P.attend(q64[s], *kv, 0, total[s])
+        assert np.isfinite(want).all()
+        assert np.all(np.abs(got[s] - want) <= 2.0 ** -7 * size)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int4"])
 @pytest.mark.parametrize("spread", [0, 20, 60, -60])
 def test_scales_far_apart(fmt, spread):
