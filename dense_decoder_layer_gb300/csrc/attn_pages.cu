@@ -23,7 +23,8 @@
 //   * bf16 rows: Q as it is, P as the sum of two bf16 pieces (2^-16).
 // Over codes P is the weight times V's scale, against the largest such product met (to within
 // the scale's mantissa); the sum of the weights is kept against the same number less
-// the exponent of the unit's first V scale, so it stays in range while scales lie within 2^80.
+// the exponent of the unit's first V scale that is not 0, so it stays in range while scales lie within
+// 2^80; a row of zeros takes part with 2^-80 of that scale.
 //
 // The tiles of all (sequence, kv head, group of heads) units, in this order, are cut into
 // equal shares, one per block, whatever the lengths: a block works on the end of one unit, on
@@ -482,6 +483,22 @@ struct Walk {
     return key0() < cur.lo || key0() + kKeys > cur.hi;
   }
 };
+
+// Of 128 scale words in shared memory, those of the rows lo .. hi - 1: the biased exponent of the first that
+// is neither 0 nor none (else 0), in all lanes.  Seldom run.
+__device__ __noinline__ uint32_t first_exponent(uint32_t words, int lo, int hi) {
+  const int row = 4 * (threadIdx.x & 31);
+  const uint4 w = lds128(words + row * 4);
+  const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+  uint32_t e = 0;
+#pragma unroll
+  for (int k = 3; k >= 0; --k) {
+    const uint32_t mine = word[k] >> 23 & 255u;
+    if (row + k >= lo && row + k < hi && mine - 1u < 254u) e = mine;
+  }
+  const unsigned have = __ballot_sync(0xffffffffu, e != 0);
+  return have ? __shfl_sync(0xffffffffu, e, __ffs(have) - 1) : 0u;
+}
 
 // Sums over the warp of N values per lane (N a power of two up to 16): N - 1 exchanges
 // halve them, the others finish; lane l ends with value number l % N.
@@ -983,7 +1000,8 @@ __global__ void __launch_bounds__(Cfg<FMT, HD, GT>::kThreads, kBlocksPerSm)
     constexpr int kQm = kKeepQ ? GT : 1, kZ = C::kInt4 ? GT : 1;
     float acc[GT], l[GT], m[GT], zl[kZ], q_mul[kQm], q_sum[kQm];
     float fix_a[GT], fix_b[GT];  // of O two tiles ago, and one
-    float lv0 = 0.f;  // exponent of the unit's first V scale here
+    float lv0 = 0.f;  // exponent of the unit's first V scale here that is not 0
+    bool find_lv0 = false;
     bool from_start = w.t == 0;  // the unit's first tile is this block's
     int of_unit = 0;             // tiles of the unit so far
     int unit_no = 0, flags = 0, end_s = 0, end_unit = 0;
@@ -1016,10 +1034,8 @@ __global__ void __launch_bounds__(Cfg<FMT, HD, GT>::kThreads, kBlocksPerSm)
           kw = lds32(at + tid * 4);
           vw = lds32(at + 512 + tid * 4);
           if (hides && !live) vw = 0u;  // (what is not seen may be a NaN)
-          if (of_unit == 0) {
-            const uint32_t e = (lds32(at + 512 + max(w.cur.lo - w.key0(), 0) * 4) >> 23) & 255u;
-            lv0 = e == 0 || e == 255 ? 0.f : static_cast<float>(static_cast<int>(e) - 127);
-            if constexpr (kKeepQ) {
+          if constexpr (kKeepQ) {
+            if (of_unit == 0) {
 #pragma unroll
               for (int g = 0; g < GT; ++g) {
                 q_mul[g] = __uint_as_float(lds32(qm + g * 4));
@@ -1034,6 +1050,26 @@ __global__ void __launch_bounds__(Cfg<FMT, HD, GT>::kThreads, kBlocksPerSm)
             acc[g] = l[g] = fix_b[g] = 0.f;
             m[g] = -3.402823466e38f;  // (finite: differences stay numbers)
             if constexpr (C::kInt4) zl[g] = 0.f;
+          }
+        }
+        if constexpr (C::kCodes) {
+          // As long as no scale was found the sums are of rows of zeros alone, and move with lv0: l is kept
+          // against m - lv0, O is 0.
+          if (of_unit == 0) {
+            const int first = max(w.cur.lo - w.key0(), 0);
+            const uint32_t e = lds32(sb + C::kWordsAt + (i % W) * 1024u + 512 + first * 4) >> 23 & 255u;
+            find_lv0 = e - 1u >= 254u;
+            lv0 = find_lv0 ? 0.f : small_float(e) - 127.f;
+          }
+          if (__builtin_expect(find_lv0, 0)) {
+            const uint32_t e = first_exponent(sb + C::kWordsAt + (i % W) * 1024u + 512, w.cur.lo - w.key0(),
+                                              w.cur.hi - w.key0());
+            if (e) {
+              find_lv0 = false;
+              lv0 = small_float(e) - 127.f;
+#pragma unroll
+              for (int g = 0; g < GT; ++g) m[g] += lv0;
+            }
           }
         }
         if constexpr (GT <= 4) {  // (without an O to take, what is there is read and left)

@@ -665,7 +665,8 @@ pds_status pds_pages_read(const pds_pages* pages, const int32_t* slots, int32_t 
  * Over codes the query enters as two 8-bit numbers per channel: exact down to 2^-13 of the head's
  * largest, off by at most 2^-21 of that largest below; and a weight times its row's V scale is
  * rounded to fp16 (2^-11 of itself), and off by at most 2^-25 of the largest such product where it is
- * far smaller, as long as the V scales that the token sees lie within 2^80 of each other.
+ * far smaller, as long as the V scales that the token sees lie within 2^80 of each other; a row whose V
+ * scale is 0 counts there as one of 2^-80 of the first other's.
  * Rows that a token does not see may hold anything: infinities and NaN there, in scale words
  * too, do not reach its output.  The same call on the same inputs gives the same bits.
  */

@@ -110,6 +110,33 @@ def test_scales_far_apart(fmt, spread):
         _check(fmt, o, q64, _values(cache, total), lens, [1, 1], window=window)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int4"])
+@pytest.mark.parametrize("group,hd", [(3, 128), (8, 64)])
+@pytest.mark.parametrize("extra", [0, 4000])
+@pytest.mark.parametrize("power", [-100, -40, 0, 60, 100])
+def test_rows_of_zeros_before_small_and_large_scales(fmt, power, extra, group, hd):
+    """V rows of zeros at a sequence's start, over whole tiles and between tiles, the others' scales close
+    together but far from 1: what a row of zeros is taken for goes by theirs."""
+    rng = np.random.default_rng(22)
+    hkv, lens = 2, [1100, 300, 3, 640]
+    total = [x + 1 for x in lens]
+    cache = _cache(fmt, lens, [1] * 4, 16, hkv, hd, extra=extra)
+    k = rng.standard_normal((sum(total), hkv, hd)) * 0.2
+    v = rng.standard_normal((sum(total), hkv, hd)) * 2.0 ** power
+    at = np.cumsum([0] + total)
+    for s, rows in enumerate(([0, 1, *range(256, 700)], range(290), [0], [*range(130), *range(200, 390), 640])):
+        v[at[s] + np.array(rows)] = 0
+    v[at[3] + 150, 0] = 0  # and in one head only
+    _write_all(cache, total, _bf16(k.astype(np.float32))[0], _bf16(v.astype(np.float32))[0])
+    q, q64 = _normal(rng, 4, hkv * group, hd)
+    values = _values(cache, total)
+    assert all((np.abs(x[1]).max() > 2.0 ** power) for x in values)
+    for window in (0, 200):
+        o = cache.attend(q, window=window)
+        cache.sync()
+        _check(fmt, o, q64, values, lens, [1] * 4, window=window)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("scale", [1e-6, 30.0])
 def test_flat_and_steep_scores(fmt, scale):
