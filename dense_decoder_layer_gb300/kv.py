@@ -154,6 +154,8 @@ def rope(x, spec, positions=None, start_pos=0, out=None, inverse=False, stream=N
     _no_gradient(x, "x", "; the gradient is rope(..., inverse=True) of the result's")
     if out is None:
         out = _new(torch.empty, shape, x.device, stream)
+    elif out is not x:
+        _no_gradient(out, "out")
     device, lead = x.get_device(), len(shape) - 2
     xs = _rows(x, shape, lead, device, "x")
     ys = xs if out is x else _rows(out, shape, lead, device, "out")
@@ -199,6 +201,7 @@ class KvCache:
                 return torch.zeros(shape, dtype=dtype, device=self.device)
             _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.device == self.device,
                   f"{what}: {dtype} {tuple(shape)} on {self.device}")
+            _no_gradient(t, what)
             _need(t.is_contiguous() if packed else t.stride(-1) == 1, f"{what}: layout")
             return t
 
@@ -285,6 +288,7 @@ class KvCache:
             k_out = _new(torch.zeros, shape, self.device, stream)
         if v_out is None:
             v_out = _new(torch.zeros, shape, self.device, stream)
+        _no_gradient(k_out, "k_out"), _no_gradient(v_out, "v_out")
         if _rows(k_out, shape, 0, self.index, "k_out") or _rows(v_out, shape, 0, self.index, "v_out"):
             raise ValueError("k_out, v_out: contiguous tensors")
         _call(pds.load().pds_cache_read, self.index, stream, self.c,
@@ -309,6 +313,8 @@ class KvCache:
         _no_gradient(q, "q")
         if out is None:
             out = _new(torch.empty, shape, self.device, stream)
+        else:
+            _no_gradient(out, "out")
         qs, os_ = _rows(q, shape, 2, device, "q"), _rows(out, shape, 2, device, "out")
         if workspace is None:
             raw = _raw_stream(device) if stream is None else stream.cuda_stream

@@ -68,6 +68,7 @@ class PagedKvCache:
                 return torch.zeros(shape, dtype=dtype, device=self.device)
             _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.device == self.device,
                   f"{what}: {dtype} {tuple(shape)} on {self.device}")
+            _no_gradient(t, what)
             _need(t.is_contiguous() if packed else t.stride(-1) == 1, f"{what}: layout")
             return t
 
@@ -195,6 +196,7 @@ class PagedKvCache:
             k_out = _new(torch.zeros, shape, self.device, stream)
         if v_out is None:
             v_out = _new(torch.zeros, shape, self.device, stream)
+        _no_gradient(k_out, "k_out"), _no_gradient(v_out, "v_out")
         if _rows(k_out, shape, 0, self.index, "k_out") or _rows(v_out, shape, 0, self.index, "v_out"):
             raise ValueError("k_out, v_out: contiguous tensors")
         at = _index(slots, rows, self.index, "slots")
@@ -240,6 +242,8 @@ class PagedKvCache:
         _no_gradient(q, "q")
         if out is None:
             out = _new(torch.empty, shape, self.device, stream)
+        else:
+            _no_gradient(out, "out")
         qs, os_ = _rows(q, shape, 1, device, "q"), _rows(out, shape, 1, device, "out")
         if workspace is None:
             raw = kv._raw_stream(device) if stream is None else stream.cuda_stream

@@ -15,7 +15,7 @@ from oracle import pages as P
 torch = pytest.importorskip("torch")
 
 from dense_decoder_layer_gb300 import kv, pages
-from test_kv_calls import cuda, lib  # noqa: F401 (a fixture)
+from test_kv_calls import cuda, lib, make_cache  # noqa: F401 (a fixture)
 
 needs_lib = pytest.mark.skipif(not os.path.exists(pds.LIB_PATH), reason="libpds.so not built")
 PTR = 0x10000
@@ -200,6 +200,31 @@ def test_what_the_calls_hand_over_and_refuse(lib):  # noqa: F811
             cache.attend(*args, **{"out": o, "workspace": ws, **kw})
     with pytest.raises(ValueError, match="gradient"):
         cache.attend(cuda(torch.zeros(3, 4, 64, dtype=torch.bfloat16).requires_grad_()), out=o, workspace=ws)
+
+
+def test_outputs_and_pools_that_require_a_gradient_are_refused(lib):  # noqa: F811
+    """A write into them would be recorded by nobody."""
+    leaf = lambda *s: cuda(torch.zeros(*s, dtype=torch.bfloat16).requires_grad_())
+    plain = lambda *s: cuda(torch.zeros(*s, dtype=torch.bfloat16))
+    ws, slots = cuda(torch.zeros(64, dtype=torch.int32)), cuda(torch.zeros(7, dtype=torch.int32))
+    cache, flat = _cache(), make_cache()
+    spec = kv.RopeSpec(1e4, 64)
+    calls = [lambda: cache.attend(plain(3, 4, 64), out=leaf(3, 4, 64), workspace=ws),
+             lambda: cache.read(slots, k_out=leaf(7, 2, 64), v_out=plain(7, 2, 64)),
+             lambda: cache.read(slots, k_out=plain(7, 2, 64), v_out=leaf(7, 2, 64)),
+             lambda: _cache(k=leaf(6, 2, 16, 64)), lambda: _cache(v=leaf(6, 2, 16, 64)),
+             lambda: flat.attend(plain(2, 1, 4, 64), out=leaf(2, 1, 4, 64), workspace=ws),
+             lambda: flat.read(0, 4, k_out=leaf(2, 4, 2, 64), v_out=plain(2, 4, 2, 64)),
+             lambda: flat.read_new(4, k_out=plain(2, 4, 2, 64), v_out=leaf(2, 4, 2, 64)),
+             lambda: kv.KvCache("bf16", 2, 16, 2, 64, k=leaf(2, 16, 2, 64), v=plain(2, 16, 2, 64)),
+             lambda: kv.rope(plain(7, 2, 64), spec, out=leaf(7, 2, 64))]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    assert not lib.calls
+    with torch.no_grad():
+        calls[0](), calls[-1]()
+    assert len(lib.calls) == 2
 
 
 # ----------------------------------------------------------- definitions
