@@ -325,3 +325,51 @@ def test_a_few_long_sequences_among_many(fmt, n, t, h, hkv, hd, window):
     assert torch.equal(out, again)
     with pytest.raises(pds.PdsError):
         cache.sync()
+
+
+def test_rotations_called_in_turn_keep_to_their_own_numbers():
+    """A rotation that was made before may be used again, and only for a call that names all of its numbers:
+    each variant differs from the base in one of them and is called right behind it, with a refused call
+    between, forward and back, by rope, by the contiguous and by the paged write."""
+    kv = _kv()
+    from dense_decoder_layer_gb300 import pages, pds
+    rng = np.random.default_rng(41)
+    base = dict(theta=5.0e5, head_dim=128, rot_dim=0, layout="neox", freq_factors=None, mscale=1.25,
+                scaling="yarn", factor=4.0, orig_context=4096, beta_fast=32.0, beta_slow=1.0)
+    ff = (1 + rng.random(64)).astype(np.float32)
+    # (one with the number that makes the two scalings alike otherwise)
+    variants = [dict(theta=4.0e5), dict(layout="norm"), dict(rot_dim=64), dict(freq_factors=ff), dict(mscale=0.0),
+                dict(scaling="linear"), dict(scaling="none"), dict(factor=8.0), dict(orig_context=1024),
+                dict(beta_fast=16.0), dict(beta_slow=4.0), dict(head_dim=64)]
+    rows, heads = 40, 2
+    pos = rng.integers(1, 1 << 20, rows)
+    x = {hd: _normal(rng, rows, heads, hd) for hd in (64, 128)}
+
+    def check(kw):
+        hd, rot = kw["head_dim"], kw["rot_dim"] or kw["head_dim"]
+        spec = kv.RopeSpec(*[kw[f] for f in ("theta", "head_dim", "rot_dim", "layout", "freq_factors", "mscale")],
+                           **{f: kw[f] for f in ("scaling", "factor", "orig_context", "beta_fast", "beta_slow")})
+        omega = D.scaled_inv_freq(rot, kw["theta"], kw["freq_factors"], kw["scaling"], kw["factor"],
+                                  kw["orig_context"], kw["beta_fast"], kw["beta_slow"])
+        t, t64 = x[hd]
+        most = 2 * np.abs(t64).max() * max(1.0, kw["mscale"])
+        for inverse in (False, True):
+            want = D.rotate(t64, pos, omega, kw["layout"], kw["mscale"] or 1.0, inverse)
+            got = bf16_to_f64(kv.rope(t, spec, positions=_i32(pos), inverse=inverse))
+            assert np.all(np.abs(got - want) <= EPS * np.abs(want) + 2.0 ** -19 * most), (kw, inverse)
+        turned = kv.rope(t, spec, positions=_i32(pos))
+        flat = kv.KvCache("bf16", 1, rows, heads, hd)
+        flat.write(t[None], t[None], rope=spec, positions=_i32(pos))
+        paged = pages.PagedKvCache("bf16", 1, 5, 8, 1, heads, hd)
+        paged.write(t, t, torch.arange(rows, dtype=torch.int32, device="cuda"), rope=spec, positions=_i32(pos))
+        assert torch.equal(flat.k[0], turned) and torch.equal(paged.k.transpose(1, 2).reshape(turned.shape), turned)
+        return got if hd == 128 else None
+
+    first = check(base)
+    for change in variants:
+        other = check({**base, **change})
+        # (a call that took the base's rotation would be seen)
+        assert other is None or np.abs(other - first).max() > 0.1, change
+        with pytest.raises(pds.PdsError):
+            kv.rope(x[128][0], kv.RopeSpec(**{**base, "factor": -1.0}), positions=_i32(pos))
+        assert np.array_equal(check(base), first)

@@ -8,7 +8,7 @@ import pytest
 
 from oracle import decode as D
 from parity import bf16_to_f64
-from test_gpu_kv import EPS, _bf16, _filled, _i32, _kv, _normal
+from test_gpu_kv import EPS, _bf16, _codes, _filled, _i32, _kv, _normal, _words
 
 pytestmark = pytest.mark.gpu
 
@@ -375,3 +375,51 @@ def test_accepted_rows_that_moved_up_are_the_rows_decoded_one_by_one(fmt):
         cache.write(k, v, rope=spec)
     assert torch.equal(tree.attend(q), one.attend(q))
     tree.sync()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("fmt", ["e4m3", "int4"])
+def test_codes_of_rows_of_every_magnitude(fmt, paged):
+    """Codes and scale words are the definition's, bit for bit: rows from below the smallest scale to
+    bf16's largest numbers, some with values that lie on the borders between codes, where the scale is a power of
+    two (halfway between neighbours of the e4m3 grid, or between whole numbers)."""
+    kv, hd, hkv = _kv(), 64, 8
+    rng = np.random.default_rng(31)
+    powers = np.repeat(np.arange(-133, 127), 4)
+    n = len(powers)
+    x = rng.standard_normal((2, n, hkv, hd))
+    x /= np.abs(x).max(-1, keepdims=True)
+    x *= 1 + 0.99 * rng.random((2, n, hkv, 1))
+    if fmt == "e4m3":
+        grid = D.e4m3_values()[:127]
+        borders = np.concatenate(((grid[1:] + grid[:-1]) / 2, grid))
+        most, unit = 448.0, 2.0 ** -8
+    else:
+        borders = np.arange(-8, 23) / 2
+        most, unit = 11.0, 2.0 ** -3
+    rows = rng.choice(borders, (2, n, 2, hd)) * (rng.choice([-1, 1], (2, n, 2, hd)) if fmt == "e4m3" else 1)
+    rows[..., 0] = most
+    if fmt == "int4":
+        rows[..., 1] = -4.0
+    x[:, :, :2] = rows * unit
+    x = np.ldexp(x, powers[None, :, None, None])
+    (k, k64), (v, v64) = (_bf16(y.astype(np.float32)) for y in x)
+    if paged:
+        from dense_decoder_layer_gb300 import pages
+        cache = pages.PagedKvCache(fmt, 1, n // 8, 8, 1, hkv, hd)
+        cache.write(k, v, torch.arange(n, dtype=torch.int32, device="cuda"))
+        flat = lambda t: t.transpose(1, 2).reshape(n, hkv, *t.shape[3:])
+    else:
+        cache = kv.KvCache(fmt, 1, n, hkv, hd)
+        for at in range(0, n, 256):  # (at most 256 tokens a call)
+            cache.lens.fill_(at)
+            cache.write(k[None, at:at + 256], v[None, at:at + 256])
+        flat = lambda t: t[0] if t.dim() == 4 else t[0].T
+    cache.sync()
+    for x64, codes, words in ((k64, cache.k, cache.k_scale), (v64, cache.v, cache.v_scale)):
+        want, w = D.quantise(x64.astype(np.float32), fmt)
+        assert np.array_equal(_words(flat(words)), w)
+        have = _codes(flat(codes), fmt)
+        same = (have == want) | ((fmt == "e4m3") & (have & 127 == 0) & (want & 127 == 0))  # (a zero's sign)
+        assert same.all()
+        assert (w >> 23 == 0).any() and ((w >> 23 > 0) & (w >> 23 < 67)).any() and (w >> 23 > 240).any()
