@@ -98,15 +98,28 @@ def _new(make, shape, device, stream, dtype=_BF16):
     index = stream.device_index if stream is not None else None
     if stream is None or stream.cuda_stream == _raw_stream(index):
         return make(shape, dtype=dtype, device=device)
-    if _current_device() != index:
+    return _under(stream, lambda: make(shape, dtype=dtype, device=device))
+
+
+def _under(stream, do):
+    """do() with the stream current."""
+    if _current_device() != stream.device_index:
         with torch.cuda.stream(stream):
-            return make(shape, dtype=dtype, device=device)
-    before = torch.cuda.current_stream(index)  # (a tenth of the context's microseconds)
+            return do()
+    before = torch.cuda.current_stream(stream.device_index)  # (a tenth of the context's microseconds)
     torch.cuda.set_stream(stream)
     try:
-        return make(shape, dtype=dtype, device=device)
+        return do()
     finally:
         torch.cuda.set_stream(before)
+
+
+def _captures(device, stream):
+    """Whether the stream that a call is for (None: the current one) is being captured."""
+    if stream is not None and stream.cuda_stream != _raw_stream(device):
+        return _under(stream, _is_capturing)
+    with torch.cuda.device(device):
+        return _is_capturing()
 
 
 def _call(fn, device, stream, *args):
@@ -258,11 +271,10 @@ class KvCache:
         return ws
 
     def _own_workspace(self, n_tokens, n_heads, stream):
-        """One for this call alone if the current stream is being captured, from the graph's
+        """One for this call alone if its stream is being captured, from the graph's
         memory: a graph may be replayed beside other work on any stream.  Else None."""
-        with torch.cuda.device(self.index):
-            if not _is_capturing():
-                return None
+        if not _captures(self.index, stream):
+            return None
         return _new(torch.empty, self._workspace_bytes(n_tokens, n_heads), self.device, stream,
                     torch.uint8)
 
@@ -318,7 +330,7 @@ class KvCache:
         qs, os_ = _rows(q, shape, 2, device, "q"), _rows(out, shape, 2, device, "out")
         if workspace is None:
             raw = _raw_stream(device) if stream is None else stream.cuda_stream
-            if raw and (_current_device() != device or _is_capturing()):
+            if raw and (stream is not None or _current_device() != device or _is_capturing()):
                 workspace = self._own_workspace(t, heads, stream)  # (stream 0 is not captured)
             if workspace is None:
                 workspace = self._ws.get((t, heads, raw))

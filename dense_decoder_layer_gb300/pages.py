@@ -222,11 +222,10 @@ class PagedKvCache:
         return ws
 
     def _own_workspace(self, n_heads, stream):
-        """One for this call alone if the current stream is being captured, from the graph's
+        """One for this call alone if its stream is being captured, from the graph's
         memory: a graph may be replayed beside other work on any stream.  Else None."""
-        with torch.cuda.device(self.index):
-            if not kv._is_capturing():
-                return None
+        if not kv._captures(self.index, stream):
+            return None
         return _new(torch.empty, self._workspace_bytes(n_heads), self.device, stream, torch.uint8)
 
     def attend(self, q, new=None, out=None, softcap=0.0, window=0, stream=None, workspace=None):
@@ -247,7 +246,7 @@ class PagedKvCache:
         qs, os_ = _rows(q, shape, 1, device, "q"), _rows(out, shape, 1, device, "out")
         if workspace is None:
             raw = kv._raw_stream(device) if stream is None else stream.cuda_stream
-            if raw and (kv._current_device() != device or kv._is_capturing()):
+            if raw and (stream is not None or kv._current_device() != device or kv._is_capturing()):
                 workspace = self._own_workspace(heads, stream)  # (stream 0 is not captured)
             if workspace is None:
                 workspace = self._ws.get((heads, raw))

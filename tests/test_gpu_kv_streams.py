@@ -120,3 +120,40 @@ def test_lengths_still_move_between_replays():
         want = cache.attend(q)
         assert torch.equal(out, want)
     cache.sync()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_graphs_captured_while_another_stream_is_current(paged):
+    """The captured stream is named by the calls; each graph has a workspace of its own all the same, and
+    runs beside the other and eager calls on that stream."""
+    kv = _kv()
+    rng = np.random.default_rng(6)
+    if paged:
+        from test_gpu_pages import _filled as paged_filled
+        cache, _ = paged_filled("e4m3", rng, [6000, 2500], [1, 1], 16, 2, 128)
+        qs = [_normal(rng, 2, 8, 128)[0] for _ in range(3)]
+    else:
+        cache, _, _ = _filled(kv, rng, "e4m3", 2, 6100, 2, 128, [6000, 2500])
+        qs = [_normal(rng, 2, 1, 8, 128)[0] for _ in range(3)]
+    wants = [cache.attend(q) for q in qs]
+    side, outs, graphs = torch.cuda.Stream(), [torch.empty_like(q) for q in qs], []
+    torch.cuda.synchronize()
+    for q, out in zip(qs[:2], outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            graph.capture_begin()
+        for _ in range(3):
+            cache.attend(q, out=out, stream=side)
+        with torch.cuda.stream(side):
+            graph.capture_end()
+        graphs.append(graph)
+    assert all(key[-1] != side.cuda_stream for key in cache._ws)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        cache.attend(qs[2], out=outs[2], stream=side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, wants))
+    cache.sync()

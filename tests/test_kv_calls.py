@@ -5,7 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from dense_decoder_layer_gb300 import kv, pds
+from dense_decoder_layer_gb300 import kv, pages, pds
 
 
 class Cuda(torch.Tensor):
@@ -114,3 +114,81 @@ def test_the_tensors_of_a_cache_cannot_be_replaced():
             setattr(cache, name, torch.zeros_like(cache.k))
     cache.k[0, 0] = 1.0
     assert cache.c.k == cache.k.data_ptr() and cache.c.v == cache.v.data_ptr()
+
+
+class Stream:
+    """Stands for a CUDA stream of device 0."""
+
+    def __init__(self, raw):
+        self.cuda_stream, self.device_index = raw, 0
+
+
+@pytest.fixture
+def streams(lib, monkeypatch):
+    """A current stream that can be set, and the streams (by number) that are being captured."""
+    class State:
+        current, captured = Stream(5), set()
+
+        @staticmethod
+        def set(stream):
+            State.current = stream
+
+    class Under:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            self.before, State.current = State.current, self.stream
+
+        def __exit__(self, *_):
+            State.current = self.before
+
+    class Device:
+        def __init__(self, _):
+            pass
+
+        def __enter__(self):
+            pass
+
+        def __exit__(self, *_):
+            pass
+
+    State.current, State.captured = Stream(5), set()
+    monkeypatch.setattr(kv, "_raw_stream", lambda device: State.current.cuda_stream)
+    monkeypatch.setattr(kv, "_is_capturing", lambda: State.current.cuda_stream in State.captured)
+    monkeypatch.setattr(torch.cuda, "set_stream", State.set)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: State.current)
+    monkeypatch.setattr(torch.cuda, "stream", Under)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    return State
+
+
+def _attenders():
+    flat = make_cache()
+    k = torch.zeros(6, 2, 16, 64, dtype=torch.bfloat16)
+    paged = pages.PagedKvCache("bf16", 2, 6, 16, 4, 2, 64, k=k, v=k.clone())
+    paged.index = 0
+    for cache in (flat, paged):
+        cache._workspace_bytes = lambda *_: 64
+    return ((flat, rows(2, 1, 4, 64)), (paged, rows(2, 4, 64)))
+
+
+def test_a_call_on_a_captured_stream_has_a_workspace_of_its_own(lib, streams):
+    """Whichever stream is the current one: the stream that counts is the call's.  Graphs that shared a
+    workspace could overwrite each other's when they run at the same time."""
+    for cache, q in _attenders():
+        for current, on, captured, own in ((5, 7, {7}, True), (5, 7, {5}, False), (5, 7, set(), False),
+                                           (5, None, {5}, True), (5, None, {7}, False), (5, 5, {5}, True),
+                                           (7, 5, {7}, False), (7, 5, {5, 7}, True), (0, 7, {7}, True)):
+            streams.current, streams.captured = Stream(current), captured
+            cache._ws.clear()
+            used = []
+            for _ in range(2):
+                cache.attend(q, out=torch.empty_like(q), stream=None if on is None else Stream(on))
+                used.append(lib.calls[-1][1][-3])
+            key = current if on is None else on
+            assert bool(cache._ws) != own, (current, on, captured)
+            if not own:
+                (at, ws), = cache._ws.items()
+                assert at[-1] == key and used == [ws.data_ptr()] * 2
+            assert streams.current.cuda_stream == current
