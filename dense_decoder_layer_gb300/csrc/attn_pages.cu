@@ -38,13 +38,15 @@
 // the status word; from then on no wait waits, nothing is copied or multiplied any more, and the
 // block runs to its end in order.
 //
-// Measured in replayed graphs, us (and the bytes at a copy's rate): 32 sequences of 8192 rows,
-// 32/8 x 128, pages of 16: bf16 162 (158), e4m3 85 (81.5), 4 bits 77 (42; pages of 64: 72); 16 of
-// 4096 rows 46 (39.5), 27 (20.4), 26 (10.5); one of 2048 rows, 24/8, bf16 7.0.  bf16 and e4m3 are
-// bound by HBM.  4 bits are by the conversion (without it 59 of the 72), which reads codes from shared
+// Measured in replayed graphs, us (and the bytes at a copy's rate, which a kernel that only reads may
+// beat by a hundredth or two): 32 sequences of 8192 rows, 32/8 x 128, pages of 16: bf16 162 (158), e4m3 85 (81.5),
+// 4 bits 77 (42; pages of 64: 72); 16 of 4096 rows 46 (39.5), 27 (20.4), 26 (10.5); one of 2048 rows, 24/8, bf16
+// 6.9.  bf16 and e4m3 are bound by HBM.  4 bits are by the conversion (without it 59 of the 72), which reads codes from shared
 // memory and writes bytes that the products read again, half of shared memory's cycles in all; and
 // then, as e4m3 of 64 channels (52, HBM 42), by warp 5, which takes 1600 cycles for a tile's waits, products
 // and commits.  Single tokens are a chain of latencies: length, table, page, scores, weights, O.
+// More than eight query heads per kv head are units of their own, a length each: 64/4 heads over 16 sequences of 4096
+// bf16 rows read 217 MB where the rows are 134, over 32 of 8192 164 us take twice the bytes' time (79).
 #include <cuda.h>
 #include <math.h>
 
@@ -1421,7 +1423,10 @@ Groups head_groups(int group) {
 // Blocks of a cluster that share a unit, 1 if the units are cut into equal shares over all
 // blocks instead.  A cluster needs no second kernel and no search; but it cuts every
 // sequence into as many pieces, so the longest one decides, and blocks stay idle that no whole
-// cluster fills.  So clusters serve up to one tile a block of bf16 rows and two of codes, whose
+// cluster fills.  The host does not know the lengths: `tiles` are those of the longest sequence that the table, or
+// the window, has room for, and a short sequence in a wide table is cut into shares (one of 1024 / 2048 rows, 24/8 x
+// 128, in a table of as many rows and of 32768: bf16 5.4 and 7.4 / 6.7 and 7.6 us, e4m3 5.7 and 7.6 / 6.7 and 8.1, 4
+// bits 6.0 and 8.4 / 7.3 and 9.0).  So clusters serve up to one tile a block of bf16 rows and two of codes, whose
 // tiles wait more for each other and less for HBM, and twice as many where they take a quarter of the
 // places or less, so that hardly two blocks share an SM.  24/8 x 128, us by clusters / by shares, bf16:
 // one sequence of 1024 rows 5.4 / 7.4, of 2048 7.0 / 7.7, of 4096 9.9 / 8.8; two of 2048 9.7 / 8.2; eight of 512

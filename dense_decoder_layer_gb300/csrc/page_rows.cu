@@ -19,10 +19,13 @@ namespace {
 // the latency of a launch, the lengths' loads, the sums, a table entry's load and its
 // store, one after the other; so blocks are as small as the work and loads go out early.
 // Measured in replayed graphs, a reserve and a release together: 8 sequences, one row each, 4.3 us;
-// 256 with up to 512 rows each 12.9; 64 with 1000 to 4096 10.5.
+// 256 with up to 512 rows each 12.8; 64 with 1000 to 4096 10.4.
 
 constexpr int kMaxScanThreads = 1024;
-// Up to this many rows the block that takes pages writes their slots too.
+// Up to this many rows the block that takes pages writes their slots too: a launch less, but one SM's loads
+// and stores.  us of a reserve and a release with one block / with a second kernel, pages of 16: 256 sequences
+// of 4 rows 5.8 / 9.4, 8 of 512 6.2 / 7.0, 8 of 1024 8.4 / 7.0, 64 of 128 10.9 / 7.7, 64 of 256 17.1 / 8.2, 256 of 64
+// 18.8 / 9.6.  (They meet between 4096 and 8192 rows.)
 constexpr int kRowsOfOneBlock = 8192;
 constexpr int kSlotThreads = 256, kSlotsPerThread = 4;
 
@@ -263,9 +266,10 @@ __device__ __forceinline__ int64_t word_at(const PageView& p, int32_t slot, int 
 }
 
 // A block takes ROWS new rows, their K and V heads.  Few rows are bound by latency (64 rows of
-// 8 x 128, rotated, to e4m3: 2.4 us), so a block has one; many by issuing the turns, the rounding
-// and the addresses, in 0.66 of all cycles: 8.8 thousand bf16 rows, rotated, 14.5 us, 73% of a copy's
-// rate; 20.5 us in e4m3, 30.7 in 4 bits, whose extrema, quotients and codes are as many again.
+// 8 x 128, rotated, to e4m3: 2.2 us), so a block has one; many by issuing the turns, the rounding
+// and the addresses, in 0.66 of all cycles (e4m3 0.70, 4 bits 0.75): 8750 rows of 8 x 128, rotated, 14.3 us in
+// bf16, 74% of a copy's rate; e4m3 20.3 (39%), 4 bits 22.9 (29%), whose extrema, quotients and codes are as many
+// again.
 // (A row per warp saved addresses but made every turn once per warp: 64 rows took 3.7 us.)
 template <int FMT, int HD, int ROWS>
 __global__ void __launch_bounds__(kRowThreads)
@@ -362,8 +366,9 @@ constexpr int kReadThreads = 128;
 
 // A warp takes two rows (or twice as many as fit its lanes) of K or V.  A thread's 16 channels are two
 // pieces of 8, half a head apart, so that a warp's stores lie side by side.  Bound by HBM, as far as the
-// output does not stay in L2, and the ramp: 24.6 thousand e4m3 rows of 8 x 128 28.5 us (5.4 TB/s),
-// 9.7 thousand 4-bit rows of 8 x 64 8.9.
+// output does not stay in L2, and the ramp.  262 thousand rows of 8 x 128: bf16 303 us, e4m3 231, 4 bits 200 (7.1,
+// 7.1, 6.8 TB/s); 24.6 thousand e4m3 with their slot map 28.5 (5.3), 9.7 thousand 4-bit rows of 8 x 64 with it 8.9
+// (2.9).
 template <int FMT, int HD>
 __global__ void __launch_bounds__(kReadThreads)
     pages_read_kernel(const __grid_constant__ PageView p, const int32_t* slots, int n_rows,
@@ -456,6 +461,9 @@ cudaError_t by_format(int format, int hd, F&& f) {
   }
 }
 
+// From this many rows on a block takes four.  us with one / four, rows of 8 x 128, rotated: 64 bf16 1.9 / 2.5, e4m3
+// 2.2 / 3.4, 4 bits 2.2 / 3.5; 1024 3.1 / 3.1, 3.8 / 4.3, 4.2 / 4.6; 4096 6.4 / 6.5, 9.3 / 10.1, 10.9 / 11.3, whose
+// inputs lie in L2.
 constexpr int kManyRows = 1024;
 
 // Threads of a block that makes the sums of n sequences, one or four each.
@@ -500,6 +508,8 @@ cudaError_t launch_pages_release(const PageView& p, const int32_t* keep, uint32_
                                  cudaStream_t st) {
   const int n = p.n_seqs, per = n <= kMaxScanThreads ? 1 : 4;
   const auto kernel = per == 1 ? pages_release_kernel<1> : pages_release_kernel<4>;
+  // A small block starts sooner, a large one moves many pages faster.  us with 128 threads / 1024, with
+  // two small copies that set the case up: 8 sequences, one page each, 3.9 / 4.0, 16 3.8 / 4.0, 128 5.8 / 4.0; 64 of 16 6.9 / 4.3.
   return launch_after(kernel, dim3(1), scan_threads(n, per, n <= 32 ? 128 : kMaxScanThreads),
                       2 * static_cast<size_t>(n) * 4, st, p, keep, status);
 }

