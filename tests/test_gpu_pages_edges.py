@@ -290,6 +290,39 @@ def test_a_serving_run_beside_the_contiguous_cache(fmt):
     assert int(cache.n_free) == 40 and sorted(cache.free.tolist()) == list(range(40))
 
 
+def test_a_prefix_in_pages_goes_on_in_a_stack():
+    """A prompt's rows, kept in pages layer by layer, gathered by slot into another stack's contiguous
+    caches: its next tokens are those of the stack that made the rows, bit for bit."""
+    import synth
+    from dense_decoder_layer_gb300.stack import DenseStack
+    _, pages = _mods()
+    dims = synth.Dims(2, 512, 8, 2, 64, 1536, 100, 0, 1.0e4)
+    layers, _, _, hidden = synth.draw_workload(dims)
+    more = np.random.default_rng(51).standard_normal((30, dims.d_model)).astype(np.float32)
+    first, second = (DenseStack(dims, 200, 100) for _ in range(2))
+    for stack in (first, second):
+        stack.load_layers(layers)
+    first.prefill(torch.from_numpy(hidden), 0)
+    first.sync()
+    hkv, hd, rows = dims.n_kv_heads, dims.head_dim, hidden.shape[0]
+    for l in range(dims.n_layers):
+        # (one book could serve all layers; another request's pages lie between)
+        cache = pages.PagedKvCache("bf16", 2, 40, 16, 10, hkv, hd)
+        slots, _, _ = cache.reserve(_i32([23, 0]), rows=23)
+        cache.lens = _i32([23, 0])
+        slots, _, _ = cache.reserve(_i32([0, rows]), rows=rows)
+        cache.write(*first.rows(l, 0, rows), slots)
+        there, _, _ = cache.slots(_i32([0, 0]), _i32([0, rows]), rows=rows)
+        cache.read(there, k_out=second.rows(l, 0, rows)[0], v_out=second.rows(l, 0, rows)[1])
+        cache.sync()
+        assert torch.equal(first.k_cache[l][:rows], second.k_cache[l][:rows])
+    a, b = (stack.prefill(torch.from_numpy(more), rows) for stack in (first, second))
+    assert torch.equal(a, b) and a.abs().max() > 0
+    for l in range(dims.n_layers):
+        for x, y in zip(first.rows(l, rows, 30), second.rows(l, rows, 30)):
+            assert torch.equal(x, y)
+
+
 # ------------------------------------------------------- streams and graphs
 
 
