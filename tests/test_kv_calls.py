@@ -120,7 +120,8 @@ class Stream:
     """Stands for a CUDA stream of device 0."""
 
     def __init__(self, raw):
-        self.cuda_stream, self.device_index = raw, 0
+        self.cuda_stream = self.stream_id = raw
+        self.device_index = 0
 
 
 @pytest.fixture
@@ -130,8 +131,9 @@ def streams(lib, monkeypatch):
         current, captured = Stream(5), set()
 
         @staticmethod
-        def set(stream):
-            State.current = stream
+        def set(stream_id, device_index, device_type):
+            assert (device_index, device_type) == (0, 1)
+            State.current = Stream(stream_id)
 
     class Under:
         def __init__(self, stream):
@@ -156,7 +158,8 @@ def streams(lib, monkeypatch):
     State.current, State.captured = Stream(5), set()
     monkeypatch.setattr(kv, "_raw_stream", lambda device: State.current.cuda_stream)
     monkeypatch.setattr(kv, "_is_capturing", lambda: State.current.cuda_stream in State.captured)
-    monkeypatch.setattr(torch.cuda, "set_stream", State.set)
+    monkeypatch.setattr(kv, "_get_stream", lambda index: (State.current.stream_id, index, 1))
+    monkeypatch.setattr(kv, "_set_stream", State.set)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: State.current)
     monkeypatch.setattr(torch.cuda, "stream", Under)
     monkeypatch.setattr(torch.cuda, "device", Device)
